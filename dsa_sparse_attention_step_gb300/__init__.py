@@ -20,7 +20,8 @@ __all__ = ["DsaError", "Batch", "KEYS_FP8", "KEYS_MXFP4", "TOPK", "library_path"
            "dsa_dcp_topk_workspace_size", "dsa_dcp_topk", "dsa_lse_combine",
            "LATENT_FP8", "LATENT_NVFP4", "dsa_sparse_mla_ex", "dsa_decode_ex",
            "dsa_indexer_front", "FRONT_QLAT_DIM", "FRONT_HIDDEN_DIM", "PreparedCall",
-           "prepare_decode", "prepare_append_cache"]
+           "prepare_decode", "prepare_append_cache", "KvCache", "Rope", "dsa_build_tables",
+           "prepare_build_tables", "dsa_rope_append", "prepare_rope_append"]
 
 KEYS_FP8 = 0
 KEYS_MXFP4 = 1
@@ -64,12 +65,25 @@ class ShardPart(ctypes.Structure):
             self.request, self.token_begin, self.num_tokens, self.seq_len)
 
 
+class _CKvCache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3),
+                ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 _bp = ctypes.POINTER(_CBatch)
+_kp = ctypes.POINTER(_CKvCache)
 
 _SIGS = {
     "dsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -100,6 +114,11 @@ _SIGS = {
     "dsa_plan_token_shards": (ctypes.c_int32, [ctypes.POINTER(ctypes.c_int32),
                                                ctypes.POINTER(ctypes.c_int32), _i32, _i32, _i32,
                                                ctypes.POINTER(ShardPart), _i32]),
+    "dsa_build_tables": (ctypes.c_int, [_i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dsa_rope_append": (ctypes.c_int, [_i32, _kp, ctypes.c_int, ctypes.POINTER(_CRope), _vp, _vp,
+                                       _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                       _vp]),
     "dsa_test_sparse_mla_wait_timeout": (ctypes.c_int, [_bp, _vp, _vp, _f32, _f32, _vp, _i32, _vp,
                                                         _vp, _vp, _sz, _vp, _vp]),
 }
@@ -438,3 +457,136 @@ def dsa_append_cache(batch, new_keys, new_latent, kv_scale, index_pages, latent_
                                  int(key_format), _ptr(dev_status, torch.int32, "dev_status"),
                                  _stream(stream))
     _check(rc, "dsa_append_cache")
+
+
+# ---- dense attention over the same pages ----------------------------------------
+
+_FLOAT_FORMATS = {torch.bfloat16: 0, torch.float16: 1}
+_KV_FORMATS = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+
+
+class KvCache:
+    """One layer's paged keys and values (dsa_kv_cache): two CUDA tensors
+    [num_pages, num_kv_heads, 64, head_dim], bfloat16, float16 or float8_e4m3fn;
+    an FP8 element x stands for x * k_scale (x * v_scale)."""
+
+    def __init__(self, k_pages, v_pages, k_scale=1.0, v_scale=1.0):
+        if k_pages.dim() != 4 or k_pages.shape[2] != PAGE or k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must be [num_pages, num_kv_heads, 64, head_dim]")
+        if k_pages.dtype not in _KV_FORMATS:
+            raise TypeError("k_pages has dtype %s" % k_pages.dtype)
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.num_pages, self.num_kv_heads, _, self.head_dim = k_pages.shape
+        self._c = _CKvCache(self.num_pages, self.num_kv_heads, self.head_dim,
+                            _KV_FORMATS[k_pages.dtype], _ptr(k_pages, None, "k_pages"),
+                            _ptr(v_pages, k_pages.dtype, "v_pages"), float(k_scale),
+                            float(v_scale))
+
+    def ref(self):
+        return ctypes.byref(self._c)
+
+
+class Rope:
+    """Rotary positions (dsa_rope): inv_freq, a float64 CUDA tensor with one
+    frequency per pair of a head; sections, the pairs of each of 1 to 3 axes
+    (default: one axis); interleaved, whether pair i is (2i, 2i + 1)."""
+
+    def __init__(self, inv_freq, sections=None, interleaved=False):
+        pairs = inv_freq.numel()
+        sections = [pairs] if sections is None else [int(n) for n in sections]
+        if len(sections) > 3 or sum(sections) != pairs:
+            raise ValueError("sections must be 1 to 3 counts that add up to inv_freq's %d" % pairs)
+        self.inv_freq, self.sections = inv_freq, sections
+        self._c = _CRope(len(sections), (ctypes.c_int32 * 3)(*sections), int(bool(interleaved)),
+                         _ptr(inv_freq, torch.float64, "inv_freq"))
+
+    def ref(self):
+        return ctypes.byref(self._c)
+
+
+def _rows(t, heads, head_dim, dtype, name):
+    """Pointer and token stride of [tokens, heads, head_dim] rows, which may be
+    a slice of wider rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s" % (name, t.dtype))
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+        raise ValueError("%s must be [tokens, %d, %d]" % (name, heads, head_dim))
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError("%s must have the heads of a token contiguous" % name)
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def _sized(t, n, dtype, name):
+    """Pointer of an array of at least n elements (None stays None)."""
+    if t is not None and t.numel() < n:
+        raise ValueError("%s has %d elements, %d are needed" % (name, t.numel(), n))
+    return _ptr(t, dtype, name)
+
+
+def prepare_build_tables(cached_lens, new_lens, free_pages, num_pages, block_table, q_offsets,
+                         seq_lens, slots=None, positions=None, token_requests=None,
+                         pages_taken=None, dev_status=None, stream=None):
+    """dsa_build_tables as a PreparedCall (same arguments)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    n = cached_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] < n:
+        raise ValueError("block_table must be [num_requests, max_pages]")
+    per_token = [x for x in (slots, positions, token_requests) if x is not None]
+    cap = min([x.numel() for x in per_token], default=0x7fffffff)
+    i32 = torch.int32
+    args = (n, _ptr(cached_lens, i32, "cached_lens"), _sized(new_lens, n, i32, "new_lens"),
+            _ptr(free_pages, i32, "free_pages"), free_pages.numel(), int(num_pages),
+            int(block_table.shape[1]), cap, _ptr(block_table, i32, "block_table"),
+            _sized(q_offsets, n + 1, i32, "q_offsets"), _sized(seq_lens, n, i32, "seq_lens"),
+            _ptr(slots, torch.int64, "slots"), _ptr(positions, i32, "positions"),
+            _ptr(token_requests, i32, "token_requests"),
+            _sized(pages_taken, 1, i32, "pages_taken"), _ptr(dev_status, i32, "dev_status"),
+            _stream(stream))
+    keep = (cached_lens, new_lens, free_pages, block_table, q_offsets, seq_lens, slots, positions,
+            token_requests, pages_taken, dev_status, stream)
+    return PreparedCall("dsa_build_tables", load().dsa_build_tables, args, keep)
+
+
+def dsa_build_tables(cached_lens, new_lens, free_pages, num_pages, block_table, q_offsets,
+                     seq_lens, slots=None, positions=None, token_requests=None, pages_taken=None,
+                     dev_status=None, stream=None):
+    """Block table, query offsets, lengths and per-token cache slots of a step
+    from the requests' cached and new lengths (see include/dsa.h).  The
+    capacity for tokens is the length of the per-token outputs given."""
+    prepare_build_tables(cached_lens, new_lens, free_pages, num_pages, block_table, q_offsets,
+                         seq_lens, slots, positions, token_requests, pages_taken, dev_status,
+                         stream)()
+
+
+def prepare_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_status=None,
+                        stream=None):
+    """dsa_rope_append as a PreparedCall (same arguments)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    dtype, tokens, dim = k.dtype, k.shape[0], cache.head_dim
+    if dtype not in _FLOAT_FORMATS:
+        raise TypeError("k has dtype %s" % dtype)
+    hq = 0 if q is None else q.shape[1]
+    rows = [_rows(k, cache.num_kv_heads, dim, dtype, "k"),
+            _rows(v, cache.num_kv_heads, dim, dtype, "v")]
+    rows += [(None, 0)] * 2 if q is None else [_rows(q, hq, dim, dtype, "q"),
+                                               _rows(q_out, hq, dim, dtype, "q_out")]
+    if any(x is not None and x.shape[0] != tokens for x in (q, v, q_out)):
+        raise ValueError("q, k, v and q_out must have the same tokens")
+    (kp, ks), (vp, vs), (qp, qs), (op, os_) = rows
+    args = (tokens, cache.ref(), _FLOAT_FORMATS[dtype], rope.ref(),
+            _sized(positions, len(rope.sections) * tokens, torch.int32, "positions"),
+            _sized(slots, tokens, torch.int64, "slots"), hq, qp, qs, kp, ks, vp, vs, op, os_,
+            _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    keep = (cache, rope, positions, slots, q, k, v, q_out, dev_status, stream)
+    return PreparedCall("dsa_rope_append", load().dsa_rope_append, args, keep)
+
+
+def dsa_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_status=None, stream=None):
+    """Rotary positions on q (into q_out) and k, and the write of k and v into
+    the cache at `slots` (see include/dsa.h).  positions: int32 [axes, tokens];
+    q, k, v: [tokens, heads, head_dim], also as slices of a fused projection."""
+    prepare_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_status, stream)()

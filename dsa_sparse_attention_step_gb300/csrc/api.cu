@@ -1,6 +1,7 @@
 // api.cu -- the extern "C" boundary of libdsa.so: argument validation,
 // workspace arithmetic and kernel launches.  See include/dsa.h.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "common.cuh"
@@ -43,6 +44,20 @@ cudaError_t launch_indexer_front(const BatchArgs& bt, const uint16_t* q_c, const
                                  const uint16_t* w_q, const uint16_t* w_k, const uint16_t* w_w,
                                  uint8_t* q8, float* qscale, float* w, void* index_pages,
                                  float* q_f32, float* k_f32, int32_t* status, cudaStream_t stream);
+
+bool build_tables_supported(int num_requests);
+cudaError_t launch_build_tables(int num_requests, const int32_t* cached, const int32_t* added,
+                                const int32_t* free_pages, int num_free, int num_pages,
+                                int max_pages, int max_tokens, int32_t* block_table,
+                                int32_t* q_offsets, int32_t* seq_lens, int64_t* slots,
+                                int32_t* positions, int32_t* token_requests, int32_t* pages_taken,
+                                int32_t* status, cudaStream_t stream);
+cudaError_t launch_rope_append(int num_tokens, const dsa_kv_cache& cache, int format,
+                               const dsa_rope& rope, const int32_t* positions,
+                               const int64_t* slots, int num_q_heads, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, void* q_out, int64_t q_out_stride,
+                               int32_t* status, cudaStream_t stream);
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int32_t> g_batch_invariant{0};  // dsa_set_batch_invariant
@@ -120,6 +135,35 @@ dsa_status check_mla_args(const dsa_batch* bt, const uint16_t* q_lat, const void
     if (!(kv_scale > 0.f) || !(sm_scale > 0.f)) return DSA_ERR_INVALID_ARG;
     return DSA_OK;
 }
+
+// A 16-bit cache holds the type of the queries, unscaled; an FP8 cache serves
+// both types.
+dsa_status check_kv_cache(const dsa_kv_cache* c, dsa_float_format format) {
+    if (c == nullptr) return DSA_ERR_INVALID_ARG;
+    if (format != DSA_FLOAT_BF16 && format != DSA_FLOAT_F16) return DSA_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DSA_ERR_UNSUPPORTED;
+    if (c->format != DSA_KV_FP8_E4M3 &&
+        c->format != (format == DSA_FLOAT_BF16 ? DSA_KV_BF16 : DSA_KV_F16))
+        return DSA_ERR_UNSUPPORTED;
+    if (c->num_pages < 1 || c->num_kv_heads < 1 ||
+        (int64_t)c->num_pages * c->num_kv_heads > INT32_MAX)
+        return DSA_ERR_INVALID_ARG;
+    if (!c->k_pages || !c->v_pages || !aligned16(c->k_pages) || !aligned16(c->v_pages))
+        return DSA_ERR_INVALID_ARG;
+    if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) ||
+        !std::isfinite(c->v_scale))
+        return DSA_ERR_INVALID_ARG;
+    if (c->format != DSA_KV_FP8_E4M3 && (c->k_scale != 1.f || c->v_scale != 1.f))
+        return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+// Token rows of `heads` heads: 16-byte accesses need 8-element strides.
+bool row_ok(const void* p, int64_t stride, int64_t heads, int head_dim) {
+    return p && aligned16(p) && stride % 8 == 0 && stride >= heads * head_dim;
+}
+
+constexpr int kMaxHeads = 1 << 14;  // query heads, and KV heads, of one layer
 
 }  // namespace
 
@@ -379,6 +423,60 @@ dsa_status dsa_append_cache(const dsa_batch* batch, const float* new_keys,
     return cuda_status(launch_append_cache(to_args(batch), new_keys, new_latent, kv_scale,
                                            index_pages, latent_pages, dev_status,
                                            (cudaStream_t)stream));
+}
+
+dsa_status dsa_build_tables(int32_t num_requests, const int32_t* cached_lens,
+                            const int32_t* new_lens, const int32_t* free_pages, int32_t num_free,
+                            int32_t num_pages, int32_t max_pages, int32_t max_tokens,
+                            int32_t* block_table, int32_t* q_offsets, int32_t* seq_lens,
+                            int64_t* slots, int32_t* positions, int32_t* token_requests,
+                            int32_t* pages_taken, int32_t* dev_status, dsa_stream_t stream) {
+    if (num_requests < 1 || num_free < 0 || num_pages < 1 || max_pages < 1 || max_tokens < 0)
+        return DSA_ERR_INVALID_ARG;
+    if (!build_tables_supported(num_requests)) return DSA_ERR_UNSUPPORTED;
+    if (!cached_lens || !new_lens || (num_free > 0 && !free_pages) || !block_table ||
+        !q_offsets || !seq_lens || !pages_taken)
+        return DSA_ERR_INVALID_ARG;
+    if ((slots && !aligned16(slots)) || (positions && !aligned16(positions)) ||
+        (token_requests && !aligned16(token_requests)))
+        return DSA_ERR_INVALID_ARG;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(launch_build_tables(num_requests, cached_lens, new_lens, free_pages,
+                                           num_free, num_pages, max_pages, max_tokens, block_table,
+                                           q_offsets, seq_lens, slots, positions, token_requests,
+                                           pages_taken, dev_status, (cudaStream_t)stream));
+}
+
+dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_float_format format,
+                           const dsa_rope* rope, const int32_t* positions, const int64_t* slots,
+                           int32_t num_q_heads, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                           int64_t q_out_stride, int32_t* dev_status, dsa_stream_t stream) {
+    const dsa_status st = check_kv_cache(cache, format);
+    if (st != DSA_OK) return st;
+    if (rope == nullptr || num_tokens < 0 || num_q_heads < 0) return DSA_ERR_INVALID_ARG;
+    if (num_q_heads > kMaxHeads || cache->num_kv_heads > kMaxHeads) return DSA_ERR_UNSUPPORTED;
+    if (rope->num_axes < 0 || rope->num_axes > 3) return DSA_ERR_UNSUPPORTED;
+    int64_t pairs = 0;
+    for (int i = 0; i < rope->num_axes; ++i) {
+        if (rope->sections[i] < 0) return DSA_ERR_INVALID_ARG;
+        pairs += rope->sections[i];
+    }
+    if (2 * pairs > cache->head_dim) return DSA_ERR_INVALID_ARG;
+    if (pairs % 8 != 0) return DSA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return DSA_OK;
+    if ((pairs > 0 && (!rope->inv_freq || !positions)) || !slots) return DSA_ERR_INVALID_ARG;
+    const int dim = cache->head_dim;
+    if (!row_ok(k, k_stride, cache->num_kv_heads, dim) ||
+        !row_ok(v, v_stride, cache->num_kv_heads, dim))
+        return DSA_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (!row_ok(q, q_stride, num_q_heads, dim) ||
+                            !row_ok(q_out, q_out_stride, num_q_heads, dim)))
+        return DSA_ERR_INVALID_ARG;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(launch_rope_append(num_tokens, *cache, (int)format, *rope, positions, slots,
+                                          num_q_heads, q, q_stride, k, k_stride, v, v_stride, q_out,
+                                          q_out_stride, dev_status, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,263 @@
+// rope_append.cu -- rotary positions on queries and keys, and the write of keys
+// and values into the paged cache, in one pass.
+//
+// Pair i of a head is turned by positions[axis(i), t] * inv_freq[i]:
+//   (x, y) -> (x cos - y sin, y cos + x sin).
+// Positions reach 2^20 and beyond, where a 32-bit angle is off by 1/16 of a
+// radian, so the angle is reduced in fixed point: inv_freq / 2 pi as a fraction
+// of a turn in 64 bits, times the position, modulo 2^64, is the fraction of the
+// turn (the product wraps exactly; the rate is off by less than 2^-53 turns per
+// unit of position).  Its upper 32 bits go to sincospi.  Two double-precision
+// operations per pair, none per value.
+//
+// Memory bound: every value is read and written once.  A CTA takes kTokens
+// tokens; its threads first form the pairs' cosines and sines in shared memory,
+// once for all heads of a token, then move units of 16 values (two 16-byte
+// loads: the two halves of eight pairs, or 16 consecutive values).
+#include "common.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = 4;
+constexpr int kMaxPairs = 128;  // head_dim / 2
+
+struct RopeArgs {
+    int32_t num_tokens, q_heads, kv_heads, interleaved, pairs;
+    int32_t end0, end1;  // first pair of the second and of the third section
+    int64_t slot_end;
+    const double* inv_freq;
+    const int32_t* positions;
+    const int64_t* slots;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_pages;
+    void* v_pages;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    float k_scale, v_scale;
+    int32_t* status;
+};
+
+template <typename T>
+__device__ __forceinline__ float2 to_float2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 to_float2<__nv_bfloat16>(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v));
+}
+template <>
+__device__ __forceinline__ float2 to_float2<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t from_float2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t from_float2<__nv_bfloat16>(float x, float y) {
+    __nv_bfloat162 r = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t from_float2<__half>(float x, float y) {
+    __half2 r = __floats2half2_rn(x, y);
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = to_float2<T>(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+    uint4 u;
+    u.x = from_float2<T>(x[0], x[1]);
+    u.y = from_float2<T>(x[2], x[3]);
+    u.z = from_float2<T>(x[4], x[5]);
+    u.w = from_float2<T>(x[6], x[7]);
+    *reinterpret_cast<uint4*>(p) = u;
+}
+
+// Eight values as E4M3 codes of x / scale (IEEE division, so that the codes are
+// those of the definition), round to nearest even, saturating.
+__device__ __forceinline__ void store8_fp8(uint8_t* p, const float (&x)[8], float scale) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+            make_float2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)), __NV_SATFINITE,
+            __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)),
+            __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+template <typename T, bool kFp8, int kDim>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
+    __shared__ float2 s_turn[kTokens][kMaxPairs];  // cos, sin
+    constexpr int kUnits = kDim / 16;
+    const int tid = threadIdx.x;
+    const int64_t first = (int64_t)blockIdx.x * kTokens;
+    const int count = (int)min((int64_t)kTokens, a.num_tokens - first);
+    grid_dependents_launch();
+    grid_dependency_wait();
+
+    for (int i = tid; i < count * a.pairs; i += kThreads) {
+        const int j = i / a.pairs, pair = i - j * a.pairs;
+        const int axis = (pair >= a.end0 ? 1 : 0) + (pair >= a.end1 ? 1 : 0);
+        const int pos = __ldg(a.positions + (int64_t)axis * a.num_tokens + first + j);
+        // the fraction of a turn per unit of position, in units of 2^-64
+        double turns = __ldg(a.inv_freq + pair) * 0.15915494309189533577;
+        turns -= floor(turns);
+        const unsigned long long rate = (unsigned long long)(turns * 18446744073709551616.0);
+        const long long angle = (long long)((unsigned long long)(long long)pos * rate);
+        float sn, cs;
+        sincospif((float)(int)(angle >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+        s_turn[j][pair] = make_float2(cs, sn);
+    }
+    __syncthreads();
+
+    const int heads = a.q_heads + 2 * a.kv_heads;
+    const int items = heads * kUnits;
+    const int turned = a.pairs / 8;  // units with pairs; the others are copied
+    for (int i = tid; i < count * items; i += kThreads) {
+        const int j = i / items, rest = i - j * items;
+        const int head = rest / kUnits, unit = rest % kUnits;
+        const int64_t t = first + j;
+        const bool is_q = head < a.q_heads, is_k = !is_q && head < a.q_heads + a.kv_heads;
+        const int h = is_q ? head : is_k ? head - a.q_heads : head - a.q_heads - a.kv_heads;
+        int64_t row = 0;
+        if (!is_q) {
+            const int64_t slot = __ldg(a.slots + t);
+            if (slot < 0) continue;
+            if (slot >= a.slot_end) {
+                record_error(a.status, DSA_ERR_DEVICE_CHECK);
+                continue;
+            }
+            row = ((slot / kPage) * a.kv_heads + h) * kPage + slot % kPage;
+        }
+        const T* src = (is_q ? static_cast<const T*>(a.q) + t * a.q_stride
+                             : is_k ? static_cast<const T*>(a.k) + t * a.k_stride
+                                    : static_cast<const T*>(a.v) + t * a.v_stride) +
+                       h * kDim;
+        const bool turn = (is_q || is_k) && unit < turned;
+        const int at0 = turn && !a.interleaved ? unit * 8 : unit * 16;
+        const int at1 = turn && !a.interleaved ? unit * 8 + a.pairs : unit * 16 + 8;
+        float x[8], y[8];
+        load8(src + at0, x);
+        load8(src + at1, y);
+        if (turn) {
+            const float2* cs = s_turn[j] + unit * 8;
+            if (a.interleaved) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const float2 c0 = cs[p], c1 = cs[4 + p];
+                    const float x0 = x[2 * p], x1 = x[2 * p + 1], y0 = y[2 * p], y1 = y[2 * p + 1];
+                    x[2 * p] = x0 * c0.x - x1 * c0.y;
+                    x[2 * p + 1] = x1 * c0.x + x0 * c0.y;
+                    y[2 * p] = y0 * c1.x - y1 * c1.y;
+                    y[2 * p + 1] = y1 * c1.x + y0 * c1.y;
+                }
+            } else {
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const float2 c = cs[p];
+                    const float x0 = x[p], y0 = y[p];
+                    x[p] = x0 * c.x - y0 * c.y;
+                    y[p] = y0 * c.x + x0 * c.y;
+                }
+            }
+        }
+        if (is_q) {
+            T* dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * kDim;
+            store8(dst + at0, x);
+            store8(dst + at1, y);
+        } else if (kFp8) {
+            uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) + row * kDim;
+            const float scale = is_k ? a.k_scale : a.v_scale;
+            store8_fp8(dst + at0, x, scale);
+            store8_fp8(dst + at1, y, scale);
+        } else {
+            T* dst = static_cast<T*>(is_k ? a.k_pages : a.v_pages) + row * kDim;
+            store8(dst + at0, x);
+            store8(dst + at1, y);
+        }
+    }
+}
+
+template <typename T, bool kFp8>
+cudaError_t launch_dim(const RopeArgs& a, int head_dim, cudaStream_t stream) {
+    const dim3 grid((unsigned)(((int64_t)a.num_tokens + kTokens - 1) / kTokens));
+    switch (head_dim) {
+        case 64:
+            return launch_kernel(rope_append_kernel<T, kFp8, 64>, grid, dim3(kThreads), 0, stream,
+                                 true, 1, a);
+        case 128:
+            return launch_kernel(rope_append_kernel<T, kFp8, 128>, grid, dim3(kThreads), 0, stream,
+                                 true, 1, a);
+        default:
+            return launch_kernel(rope_append_kernel<T, kFp8, 256>, grid, dim3(kThreads), 0, stream,
+                                 true, 1, a);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(int num_tokens, const dsa_kv_cache& cache, int format,
+                               const dsa_rope& rope, const int32_t* positions,
+                               const int64_t* slots, int num_q_heads, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, void* q_out, int64_t q_out_stride,
+                               int32_t* status, cudaStream_t stream) {
+    RopeArgs a;
+    a.num_tokens = num_tokens;
+    a.q_heads = num_q_heads;
+    a.kv_heads = cache.num_kv_heads;
+    a.interleaved = rope.interleaved != 0;
+    a.pairs = 0;
+    int ends[3] = {0, 0, 0};
+    for (int i = 0; i < 3; ++i) {
+        if (i < rope.num_axes) a.pairs += rope.sections[i];
+        ends[i] = a.pairs;
+    }
+    a.end0 = ends[0];
+    a.end1 = ends[1];
+    a.slot_end = (int64_t)cache.num_pages * kPage;
+    a.inv_freq = rope.inv_freq;
+    a.positions = positions;
+    a.slots = slots;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_pages = cache.k_pages;
+    a.v_pages = cache.v_pages;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_scale = cache.k_scale;
+    a.v_scale = cache.v_scale;
+    a.status = status;
+    const bool fp8 = cache.format == DSA_KV_FP8_E4M3;
+    if (format == DSA_FLOAT_BF16)
+        return fp8 ? launch_dim<__nv_bfloat16, true>(a, cache.head_dim, stream)
+                   : launch_dim<__nv_bfloat16, false>(a, cache.head_dim, stream);
+    return fp8 ? launch_dim<__half, true>(a, cache.head_dim, stream)
+               : launch_dim<__half, false>(a, cache.head_dim, stream);
+}
+
+}  // namespace dsa

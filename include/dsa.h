@@ -392,6 +392,122 @@ int32_t dsa_plan_token_shards(const int32_t* seq_lens, const int32_t* q_counts,
                               int32_t num_requests, int32_t world, int32_t rank,
                               dsa_shard_part* parts, int32_t max_parts);
 
+/* ---- dense attention over the same pages ------------------------------------------
+ * No counterpart on the pages: an addition of this library, for the layers of a
+ * model that attend to every cached position (a draft model, a dense layer)
+ * and for building the batch metadata of every other call on the GPU.  The
+ * calls, in the order a step makes them: dsa_build_tables, dsa_rope_append.
+ * They allocate nothing and may be captured into a CUDA graph. */
+
+/* Element type of queries, keys, values and outputs. */
+typedef enum { DSA_FLOAT_BF16 = 0, DSA_FLOAT_F16 = 1 } dsa_float_format;
+
+/* Element type of a key/value cache.  A 16-bit cache holds the type of the
+ * queries; an FP8 cache serves both. */
+typedef enum { DSA_KV_BF16 = 0, DSA_KV_F16 = 1, DSA_KV_FP8_E4M3 = 2 } dsa_kv_format;
+
+/* A paged key/value cache of one layer.  The struct lives in host memory; the
+ * pools are device pointers, 16-byte aligned, each
+ *   [num_pages, num_kv_heads, 64, head_dim] elements of `format`
+ * so that one page of one head is contiguous.  A stored element x stands for
+ * x * k_scale (keys) or x * v_scale (values).
+ * head_dim is 64, 128 or 256; num_pages * num_kv_heads is below 2^31. */
+typedef struct {
+    int32_t num_pages;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    dsa_kv_format format;
+    void* k_pages;
+    void* v_pages;
+    float k_scale;  /* finite and > 0; 1 for 16-bit formats */
+    float v_scale;
+} dsa_kv_cache;
+
+/* Block tables, offsets and cache slots of a step, from the requests' lengths.
+ * Request b has cached_lens[b] tokens in the cache, in the pages
+ * block_table[b, 0 .. held_b), and brings new_lens[b] more.  With
+ *   held_b  = ceil(cached_lens[b] / 64)
+ *   grown_b = ceil((cached_lens[b] + new_lens[b]) / 64) - held_b
+ *   O, F    = the exclusive sums of new_lens and of grown over the requests
+ * the call writes
+ *   block_table[b, held_b + i] = free_pages[F_b + i]   for 0 <= i < grown_b
+ *                                (the other entries are left as they are)
+ *   q_offsets[b] = O_b, q_offsets[B] = the number T of new tokens
+ *   seq_lens[b]  = cached_lens[b] + new_lens[b]
+ *   pages_taken  = sum of grown: the caller drops that many from the front of
+ *                  its free list
+ * and for token j of request b, at t = O_b + j and position p = cached_lens[b] + j,
+ *   slots[t] = block_table[b, p / 64] * 64 + p % 64,  positions[t] = p,
+ *   token_requests[t] = b;
+ *   for T <= t < max_tokens: slots[t] = -1, positions[t] = 0,
+ *   token_requests[t] = -1, so a step of fixed size may have unused rows.
+ * q_offsets, seq_lens and block_table are the device arrays of a dsa_batch.
+ *   cached_lens, new_lens  [B] int32;  free_pages [num_free] int32 page ids
+ *                          (may be NULL when num_free is 0)
+ *   block_table            [B, max_pages] int32, read and written
+ *   q_offsets [B+1], seq_lens [B], pages_taken [1] int32: outputs
+ *   slots [max_tokens] int64, positions, token_requests [max_tokens] int32:
+ *                          outputs, 16-byte aligned, each may be NULL
+ * B is at most 4096 (DSA_ERR_UNSUPPORTED above).  With the inputs unchanged the
+ * call may be repeated: it writes the same values again.  One kernel launch.
+ * Device checks, each recorded as DSA_ERR_DEVICE_CHECK in *dev_status:
+ *   - a page id outside [0, num_pages), or a free list that is too short (the
+ *     table entry and the tokens' slots become -1; pages_taken still is what
+ *     the step needs, so above num_free it tells the shortfall);
+ *   - a request with a negative length, or with more pages than max_pages: it
+ *     takes no pages and its slots are -1 (a negative length counts as 0);
+ *   - more than max_tokens new tokens: offsets stop at max_tokens and the
+ *     tokens beyond are left out.
+ * Nothing outside the arrays is read or written in any of these cases. */
+dsa_status dsa_build_tables(int32_t num_requests, const int32_t* cached_lens,
+                            const int32_t* new_lens, const int32_t* free_pages, int32_t num_free,
+                            int32_t num_pages, int32_t max_pages, int32_t max_tokens,
+                            int32_t* block_table, int32_t* q_offsets, int32_t* seq_lens,
+                            int64_t* slots, int32_t* positions, int32_t* token_requests,
+                            int32_t* pages_taken, int32_t* dev_status, dsa_stream_t stream);
+
+/* Rotary positions.  The struct lives in host memory, inv_freq on the device.
+ * The first R = 2 * (sections[0] + .. + sections[num_axes - 1]) values of a
+ * head are R / 2 pairs; pair i is turned by the angle positions[a, t] *
+ * inv_freq[i], where axis a is the one whose section holds i (sections are
+ * consecutive: with one axis, all pairs).  Values from R on stay.
+ *   interleaved = 0: pair i is (x[i], x[i + R/2]); != 0: (x[2i], x[2i + 1])
+ * R is a multiple of 16 and at most head_dim; num_axes is 0..3, 0 meaning no
+ * turning.  The angle is reduced in 64-bit fixed point: positions anywhere in
+ * int32 lose no accuracy. */
+typedef struct {
+    int32_t num_axes;
+    int32_t sections[3];
+    int32_t interleaved;
+    const double* inv_freq; /* device [R/2]; may be NULL when R is 0 */
+} dsa_rope;
+
+/* Rotary positions on queries and keys, and the write of keys and values into
+ * the paged cache, in one pass.  For each token t and head h:
+ *   q_out[t,h,:] = turn(q[t,h,:])
+ *   cache key   at slots[t] of KV head h = turn(k[t,h,:])
+ *   cache value at slots[t] of KV head h = v[t,h,:]
+ * in fp32, rounded once: to the 16-bit type, or for FP8 E4M3(x / scale), round to
+ * nearest even, saturating (fp32 division).
+ *   q [T, num_q_heads, head_dim], k, v [T, num_kv_heads, head_dim]: heads of a
+ *       token contiguous, tokens *_stride elements apart (a multiple of 8, at
+ *       least a token's elements), so they may be slices of one fused
+ *       projection; 16-byte aligned
+ *   positions [num_axes, T] int32 (may be NULL when R is 0)
+ *   slots     [T] int64, as dsa_build_tables writes them: page * 64 + row.
+ *             Negative: the token's key and value are not stored.  The other
+ *             slots must be distinct.
+ *   q_out     as q, q_out_stride apart; may be q itself with the same stride,
+ *             else it must not overlap the inputs
+ *   num_q_heads may be 0 (q and q_out are then ignored)
+ * A slot at or beyond num_pages * 64 is skipped and recorded as
+ * DSA_ERR_DEVICE_CHECK.  One kernel launch. */
+dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_float_format format,
+                           const dsa_rope* rope, const int32_t* positions, const int64_t* slots,
+                           int32_t num_q_heads, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                           int64_t q_out_stride, int32_t* dev_status, dsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,80 @@
+"""Argument checks of the paged key/value entry points (CPU only: every call
+here is refused before anything is launched)."""
+import ctypes
+
+import pytest
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+FAKE = ctypes.c_void_p(4096)  # never dereferenced
+ODD = ctypes.c_void_p(4100)   # not 16-byte aligned
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dsa_sparse_attention_step_gb300 import _build
+    _build.build()
+    import dsa_sparse_attention_step_gb300 as dsa
+    return dsa.load()
+
+
+def _cache(**kw):
+    import dsa_sparse_attention_step_gb300 as dsa
+    c = dsa._CKvCache(8, 2, 128, 0, 4096, 8192, 1.0, 1.0)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def _tables(lib, requests=2, free=FAKE, num_free=8, pages=64, width=4, cap=16, table=FAKE,
+            slots=FAKE, positions=FAKE, taken=FAKE, cached=FAKE):
+    return lib.dsa_build_tables(requests, cached, FAKE, free, num_free, pages, width, cap, table,
+                                FAKE, FAKE, slots, positions, FAKE, taken, None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(requests=0), INVALID), (dict(requests=4097), UNSUPPORTED), (dict(num_free=-1), INVALID),
+    (dict(free=None), INVALID), (dict(pages=0), INVALID), (dict(width=0), INVALID),
+    (dict(cap=-1), INVALID), (dict(table=None), INVALID), (dict(taken=None), INVALID),
+    (dict(cached=None), INVALID), (dict(slots=ODD), INVALID), (dict(positions=ODD), INVALID)])
+def test_build_tables_refusals(lib, kw, code):
+    assert _tables(lib, **kw) == code
+
+
+def _rope(lib, cache=None, fmt=0, tokens=3, axes=1, sections=(64, 0, 0), freq=4096, positions=FAKE,
+          slots=FAKE, hq=4, q=FAKE, qs=512, k=FAKE, ks=256, v=FAKE, vs=256, out=FAKE, os=512):
+    import dsa_sparse_attention_step_gb300 as dsa
+    r = dsa._CRope(axes, (ctypes.c_int32 * 3)(*sections), 0, freq)
+    c = _cache() if cache is None else cache
+    return lib.dsa_rope_append(tokens, ctypes.byref(c), fmt, ctypes.byref(r), positions, slots, hq,
+                               q, qs, k, ks, v, vs, out, os, None, None)
+
+
+CACHE_REFUSALS = [
+    (dict(head_dim=96), UNSUPPORTED), (dict(format=1), UNSUPPORTED), (dict(format=7), UNSUPPORTED),
+    (dict(num_pages=0), INVALID), (dict(num_kv_heads=0), INVALID),
+    (dict(num_pages=1 << 20, num_kv_heads=1 << 11), INVALID), (dict(k_pages=0), INVALID),
+    (dict(v_pages=8200), INVALID), (dict(k_scale=0.5), INVALID),
+    (dict(format=2, k_scale=0.0), INVALID), (dict(format=2, v_scale=float("inf")), INVALID),
+    (dict(format=2, k_scale=float("nan")), INVALID)]
+
+
+@pytest.mark.parametrize("kw,code", CACHE_REFUSALS)
+def test_cache_refusals_by_rope_append(lib, kw, code):
+    assert _rope(lib, cache=_cache(**kw)) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(fmt=2), UNSUPPORTED), (dict(tokens=-1), INVALID), (dict(axes=4), UNSUPPORTED),
+    (dict(axes=-1), UNSUPPORTED), (dict(sections=(-8, 0, 0)), INVALID),
+    (dict(sections=(72, 0, 0)), INVALID), (dict(sections=(12, 0, 0)), UNSUPPORTED),
+    (dict(freq=0), INVALID), (dict(positions=None), INVALID), (dict(slots=None), INVALID),
+    (dict(q=None), INVALID), (dict(q=ODD), INVALID), (dict(qs=516), INVALID),
+    (dict(qs=504), INVALID), (dict(ks=248), INVALID), (dict(vs=260), INVALID), (dict(k=ODD), INVALID),
+    (dict(out=None), INVALID), (dict(os=500), INVALID), (dict(hq=-1), INVALID),
+    (dict(hq=1 << 15, qs=1 << 22, os=1 << 22), UNSUPPORTED)])
+def test_rope_append_refusals(lib, kw, code):
+    assert _rope(lib, **kw) == code
+
+
+def test_rope_append_of_no_tokens_is_a_no_op(lib):
+    assert _rope(lib, tokens=0) == 0
