@@ -21,7 +21,9 @@ __all__ = ["DsaError", "Batch", "KEYS_FP8", "KEYS_MXFP4", "TOPK", "library_path"
            "LATENT_FP8", "LATENT_NVFP4", "dsa_sparse_mla_ex", "dsa_decode_ex",
            "dsa_indexer_front", "FRONT_QLAT_DIM", "FRONT_HIDDEN_DIM", "PreparedCall",
            "prepare_decode", "prepare_append_cache", "KvCache", "Rope", "dsa_build_tables",
-           "prepare_build_tables", "dsa_rope_append", "prepare_rope_append"]
+           "prepare_build_tables", "dsa_rope_append", "prepare_rope_append",
+           "dsa_paged_attention", "dsa_paged_attention_workspace_size",
+           "prepare_paged_attention"]
 
 KEYS_FP8 = 0
 KEYS_MXFP4 = 1
@@ -119,6 +121,9 @@ _SIGS = {
     "dsa_rope_append": (ctypes.c_int, [_i32, _kp, ctypes.c_int, ctypes.POINTER(_CRope), _vp, _vp,
                                        _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                        _vp]),
+    "dsa_paged_attention_workspace_size": (_sz, [_bp, _kp, _i32]),
+    "dsa_paged_attention": (ctypes.c_int, [_bp, _kp, ctypes.c_int, _i32, _vp, _i64, _f32, _vp, _vp,
+                                           _vp, _sz, _vp, _vp]),
     "dsa_test_sparse_mla_wait_timeout": (ctypes.c_int, [_bp, _vp, _vp, _f32, _f32, _vp, _i32, _vp,
                                                         _vp, _vp, _sz, _vp, _vp]),
 }
@@ -590,3 +595,35 @@ def dsa_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_status=No
     the cache at `slots` (see include/dsa.h).  positions: int32 [axes, tokens];
     q, k, v: [tokens, heads, head_dim], also as slices of a fused projection."""
     prepare_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_status, stream)()
+
+
+def dsa_paged_attention_workspace_size(batch, cache, num_q_heads):
+    return int(load().dsa_paged_attention_workspace_size(batch.ref(), cache.ref(),
+                                                         int(num_q_heads)))
+
+
+def prepare_paged_attention(batch, cache, q, sm_scale, out, lse=None, ws=None, dev_status=None,
+                            stream=None):
+    """dsa_paged_attention as a PreparedCall (same arguments)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    if q.dtype not in _FLOAT_FORMATS:
+        raise TypeError("q has dtype %s" % q.dtype)
+    hq, dim, tokens = q.shape[1], cache.head_dim, batch.total_q
+    qp, qs = _rows(q, hq, dim, q.dtype, "q")
+    if q.shape[0] < tokens:
+        raise ValueError("q has %d tokens, the batch %d" % (q.shape[0], tokens))
+    args = (batch.ref(), cache.ref(), _FLOAT_FORMATS[q.dtype], hq, qp, qs, float(sm_scale),
+            _sized(out, tokens * hq * dim, q.dtype, "out"),
+            _sized(lse, tokens * hq, torch.float32, "lse"), _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(),
+            _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    keep = (batch, cache, q, out, lse, ws, dev_status, stream)
+    return PreparedCall("dsa_paged_attention", load().dsa_paged_attention, args, keep)
+
+
+def dsa_paged_attention(batch, cache, q, sm_scale, out, lse=None, ws=None, dev_status=None,
+                        stream=None):
+    """Attention of the batch's query tokens q [tokens, num_q_heads, head_dim]
+    over every cached position they see (see include/dsa.h)."""
+    prepare_paged_attention(batch, cache, q, sm_scale, out, lse, ws, dev_status, stream)()

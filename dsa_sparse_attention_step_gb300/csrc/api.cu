@@ -59,6 +59,12 @@ cudaError_t launch_rope_append(int num_tokens, const dsa_kv_cache& cache, int fo
                                int64_t v_stride, void* q_out, int64_t q_out_stride,
                                int32_t* status, cudaStream_t stream);
 
+size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim);
+cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cache, int format,
+                                   int num_q_heads, const void* q, int64_t q_stride,
+                                   float sm_scale, void* out, float* lse, void* ws, bool whole,
+                                   int32_t* status, int* launches, cudaStream_t stream);
+
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int32_t> g_batch_invariant{0};  // dsa_set_batch_invariant
 }  // namespace dsa
@@ -69,14 +75,15 @@ namespace {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-dsa_status check_batch(const dsa_batch* bt) {
+// padded: requests may have more query rows than context (or none at all).
+dsa_status check_batch(const dsa_batch* bt, bool padded = false) {
     if (bt == nullptr) return DSA_ERR_INVALID_ARG;
     if (bt->page_size != kPage) return DSA_ERR_UNSUPPORTED;
     if (bt->num_requests < 1 || bt->total_q < 0 || bt->max_q_per_request < 0 ||
-        bt->max_seq_len < 1 || bt->num_pages < 1 || bt->max_pages < 1)
+        bt->max_seq_len < (padded ? 0 : 1) || bt->num_pages < 1 || bt->max_pages < 1)
         return DSA_ERR_INVALID_ARG;
     if ((int64_t)bt->max_pages * kPage < bt->max_seq_len) return DSA_ERR_INVALID_ARG;
-    if (bt->max_q_per_request > bt->max_seq_len) return DSA_ERR_INVALID_ARG;
+    if (!padded && bt->max_q_per_request > bt->max_seq_len) return DSA_ERR_INVALID_ARG;
     if ((int64_t)bt->total_q > (int64_t)bt->num_requests * bt->max_q_per_request)
         return DSA_ERR_INVALID_ARG;
     if (!bt->q_offsets || !bt->seq_lens || !bt->block_table) return DSA_ERR_INVALID_ARG;
@@ -477,6 +484,47 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
     return cuda_status(launch_rope_append(num_tokens, *cache, (int)format, *rope, positions, slots,
                                           num_q_heads, q, q_stride, k, k_stride, v, v_stride, q_out,
                                           q_out_stride, dev_status, (cudaStream_t)stream));
+}
+
+size_t dsa_paged_attention_workspace_size(const dsa_batch* batch, const dsa_kv_cache* cache,
+                                          int32_t num_q_heads) {
+    if (check_batch(batch, true) != DSA_OK || cache == nullptr || cache->num_kv_heads < 1 ||
+        num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0 ||
+        (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256))
+        return 0;
+    return paged_attention_workspace_bytes(
+        (int64_t)batch->max_q_per_request * (num_q_heads / cache->num_kv_heads), cache->head_dim);
+}
+
+dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache,
+                               dsa_float_format format, int32_t num_q_heads, const void* q,
+                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream) {
+    dsa_status st = check_batch(batch, true);
+    if (st != DSA_OK) return st;
+    st = check_kv_cache(cache, format);
+    if (st != DSA_OK) return st;
+    if (num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0 ||
+        batch->num_pages != cache->num_pages)
+        return DSA_ERR_INVALID_ARG;
+    const int group = num_q_heads / cache->num_kv_heads;
+    if (num_q_heads > kMaxHeads || (int64_t)batch->max_q_per_request * group > (1 << 30))
+        return DSA_ERR_UNSUPPORTED;
+    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+    if (batch->total_q == 0) return DSA_OK;
+    if (!row_ok(q, q_stride, num_q_heads, cache->head_dim) || !out || !aligned16(out))
+        return DSA_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) ||
+        ws_bytes < dsa_paged_attention_workspace_size(batch, cache, num_q_heads))
+        return DSA_ERR_WORKSPACE;
+    const bool whole = g_batch_invariant.load(std::memory_order_relaxed) != 0;
+    int launches = 0;
+    const dsa_status rc = cuda_status(
+        launch_paged_attention(to_args(batch), *cache, (int)format, num_q_heads, q, q_stride,
+                               sm_scale, out, lse, ws, whole, dev_status, &launches,
+                               (cudaStream_t)stream));
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    return rc;
 }
 
 }  // extern "C"

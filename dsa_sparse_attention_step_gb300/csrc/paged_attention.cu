@@ -1,0 +1,1022 @@
+// paged_attention.cu -- attention of new tokens over every cached position they
+// see, keys and values in 64-token pages, G query heads to a KV head.
+//
+//   z[s] = sm_scale q . k_s,  out = sum_s e^(z[s] - m) v_s / sum_s e^(z[s] - m)
+//
+// One pass over the cache with a running maximum m and sum per row (a row is
+// one query token's one head).  The G n_b rows of a request that share a KV head
+// form row tiles of 16, 32 or 64, so the cache is read once per row tile: at
+// decode (at most 64 rows) 2 G n_b / element size flop per byte, below what the
+// tensor cores need to keep up with HBM.  The kernel is bound by the reads.
+//
+// Work is counted in key tiles (one page of one KV head against one row tile)
+// over all requests, and every CTA of a resident grid takes an equal, contiguous
+// run of that list: short and long requests share the SMs evenly without the
+// host knowing their lengths, and the copies of the next request run while the
+// last one is finished.  A (request, row tile, KV head) cut by a CTA's border
+// leaves unnormalised pieces in the workspace, which a second kernel joins
+// (launched early, it waits for the first): piece order is fixed, so results do
+// not change from run to run.
+//
+// One warp per CTA issues the copies (TMA, 128-byte swizzled page tiles into a
+// ring of stages); each consumer warp takes 16 rows and a share of a tile's
+// tokens with a softmax of its own, so the warps meet only when a row tile is
+// done.  m16n8k16 MMAs with fp32 accumulation: at 16 rows a tcgen05 tile of 128
+// rows would be seven eighths empty, and the fragments' register layout lets P
+// go from scores to operand without leaving the registers.  FP8 keys and values
+// are lifted to f16 exactly; bf16 queries then are scaled by a power of two per
+// row, so that f16 holds them.
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+
+namespace dsa {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+using namespace sm100;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+    BatchArgs bt;
+    int32_t kv_heads, group;
+    int32_t min_tiles;  // least tiles of a CTA
+    int32_t whole;      // every (request, row tile, KV head) by one CTA
+    int64_t q_stride;
+    const void* q;
+    void* out;
+    float* lse;
+    float score_scale;  // sm_scale * k_scale * log2 e
+    float v_scale;
+    float* part_o;    // [2 * CTAs][rows][dim] unnormalised pieces
+    float* part_ml;   // [2 * CTAs][rows][2]: maximum (log2 units), sum
+    int32_t* joins;   // [CTAs][8]
+    int32_t* status;
+};
+
+// What a joining block needs to know of the row tile whose first piece a CTA wrote.
+enum { kJoinPieces, kJoinToken, kJoinRow, kJoinRows, kJoinHead, kJoinInts = 8 };
+
+template <int kD, bool kKvFp8, int kWM_, int kWN_>
+struct AttnCfg {
+    static constexpr int kDim = kD;
+    static constexpr bool kFp8 = kKvFp8;
+    static constexpr int kWM = kWM_;  // warps along the rows, 16 rows each
+    static constexpr int kWN = kWN_;  // warps along a tile's tokens
+    static constexpr int kRows = 16 * kWM;
+    static constexpr int kConsumers = kWM * kWN;
+    static constexpr int kThreads = 32 * (kConsumers + 1);
+    static constexpr int kRowBytes = kD * (kKvFp8 ? 1 : 2);
+    static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;
+    static constexpr int kBoxes = kRowBytes / kBoxBytes;
+    static constexpr int kTileBytes = kPage * kRowBytes;  // keys or values of one page
+    static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kCtas = kConsumers <= 4 && kD < 256 ? 2 : 1;
+    static constexpr int kRing = kCtas == 2 ? 98304 : kStageBytes <= 32768 ? 163840 : 196608;
+    static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
+    static constexpr int kTokens = kPage / kWN;                 // of a tile, per warp
+    static constexpr int kSub = kD == 256 || kTokens < 32 ? 16 : 32;  // softmax step
+    static constexpr int kPairs = kRowBytes / 32;               // pairs of 16-byte chunks in a row
+    static constexpr int kTilesD = kD / 8;                      // accumulator tiles along the dims
+    static constexpr bool kQSmem = kD == 256;  // 64 registers of Q fragments do not fit beside 128 of O
+    static constexpr int kQBytes = kQSmem ? kWM * (kD / 16) * 512 : 0;
+    static constexpr int kMergeBytes = kWN > 1 ? (kWN / 2) * kRows * 64 * 4 : 0;
+    static constexpr int kMlBytes = kWN * kRows * 8;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kQBytes + kMergeBytes + kMlBytes;
+};
+
+// ---- the list of key tiles ----------------------------------------------------
+
+// One request as the schedule sees it; rows = 0 when it brings no tokens or its
+// metadata contradict the host sizes.  Unlike the other kernels' check this
+// takes seq < n_b (rows that see nothing).
+struct Request {
+    int q0, nb, seq, rows;
+};
+
+__device__ __forceinline__ Request request_at(const AttnParams& p, int b, int32_t* status) {
+    Request r;
+    r.q0 = __ldg(p.bt.q_offsets + b);
+    const int q1 = __ldg(p.bt.q_offsets + b + 1);
+    r.seq = __ldg(p.bt.seq_lens + b);
+    const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= p.bt.total_q && q1 - r.q0 <= p.bt.max_q &&
+                    r.seq >= 0 && r.seq <= p.bt.max_seq;
+    if (!ok) record_error(status, DSA_ERR_DEVICE_CHECK);
+    r.nb = ok ? q1 - r.q0 : 0;
+    r.rows = r.nb * p.group;
+    return r;
+}
+
+// Key tiles that row tile rt of a request needs: pages up to the last position
+// its last row sees.
+template <int kRows>
+__device__ __forceinline__ int tiles_of(const AttnParams& p, const Request& r, int rt) {
+    const int last = min(r.rows, (rt + 1) * kRows) - 1;
+    const int vis = r.seq - r.nb + last / p.group + 1;
+    return vis > 0 ? (vis + kPage - 1) / kPage : 0;
+}
+
+// A place in the list.  Units run over requests, row tiles, KV heads; a unit
+// without key tiles counts as one, so that somebody writes its empty rows.
+template <int kRows>
+struct Cursor {
+    int b, rt, h, tiles;
+    Request r;
+
+    __device__ __forceinline__ int cost() const { return tiles > 0 ? tiles : 1; }
+    __device__ __forceinline__ void enter(const AttnParams& p) {
+        r = request_at(p, b, nullptr);
+        while (r.rows == 0 && b + 1 < p.bt.num_requests) r = request_at(p, ++b, nullptr);
+        tiles = tiles_of<kRows>(p, r, rt);
+    }
+    __device__ __forceinline__ void next(const AttnParams& p) {
+        if (++h < p.kv_heads) return;
+        h = 0;
+        if (++rt * kRows >= r.rows) {
+            rt = 0;
+            if (++b >= p.bt.num_requests) return;  // the end of the list
+            enter(p);
+        } else {
+            tiles = tiles_of<kRows>(p, r, rt);
+        }
+    }
+};
+
+struct Share {
+    long long begin, end, per;  // this CTA's run of the list
+    int b, rt, h, tile;         // where it begins
+};
+
+// Whole CTA: this CTA's share of the list.  Each thread adds up a run of
+// requests; a scan over the threads places the runs, and the thread whose run
+// holds the CTA's first tile looks it up.
+template <typename C>
+__device__ void find_share(const AttnParams& p, Share* s, long long* s_warp) {
+    constexpr int kWarps = C::kThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = p.bt.num_requests;
+    const int each = (n + C::kThreads - 1) / C::kThreads;
+    long long sum = 0;
+    for (int i = 0; i < each; ++i) {
+        const int b = tid * each + i;
+        if (b >= n) break;
+        const Request r = request_at(p, b, blockIdx.x == 0 ? p.status : nullptr);
+        long long t = 0;
+        for (int rt = 0; rt * C::kRows < r.rows; ++rt)
+            t += max(1, tiles_of<C::kRows>(p, r, rt));
+        sum += t * p.kv_heads;
+    }
+    long long before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
+    }
+    if (lane == 31) s_warp[warp] = before;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+    before -= sum;
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    per = max(per, (long long)p.min_tiles);
+    const long long begin = min(total, per * blockIdx.x);
+    if (tid == 0) {
+        s->begin = begin;
+        s->end = min(total, begin + per);
+        s->per = per;
+    }
+    if (begin < total && before <= begin && begin < before + sum) {
+        for (int b = tid * each;; ++b) {
+            const Request r = request_at(p, b, nullptr);
+            for (int rt = 0; rt * C::kRows < r.rows; ++rt) {
+                const int cost = max(1, tiles_of<C::kRows>(p, r, rt));
+                const long long unit = (long long)cost * p.kv_heads;
+                if (begin < before + unit) {
+                    s->b = b;
+                    s->rt = rt;
+                    s->h = (int)((begin - before) / cost);
+                    s->tile = (int)((begin - before) % cost);
+                    b = n;  // found
+                    break;
+                }
+                before += unit;
+            }
+            if (b >= n) break;
+        }
+    }
+    __syncthreads();
+}
+
+// ---- fragments -----------------------------------------------------------------
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    if (kBf16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes (low 16 bits) as two f16, exact.
+__device__ __forceinline__ uint32_t lift(uint32_t codes) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if (kBf16) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __half2 r = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// A maximum as a subtrahend: 0 for a row that has seen nothing yet.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// 3-D tiled TMA load of one box at (x, y, z).
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, int x, int y, int z,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+template <int kCount>
+__device__ __forceinline__ void consumer_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kCount) : "memory");
+}
+
+// ---- the kernel ----------------------------------------------------------------
+
+template <typename C, bool kQBf16>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas)
+paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
+    // operands of the MMAs: the cache's own type, or f16 lifted from FP8
+    constexpr bool kBf16 = kQBf16 && !C::kFp8;
+    constexpr int kD = C::kDim;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];
+    __shared__ int s_valid[C::kStages];
+    __shared__ long long s_warp[C::kThreads / 32];
+    __shared__ Share s_share;
+    __shared__ int s_abort;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                               ~(uintptr_t)1023);
+    uint8_t* tail = ring + C::kStages * C::kStageBytes;
+    uint4* s_q = reinterpret_cast<uint4*>(tail);
+    float4* s_merge = reinterpret_cast<float4*>(tail + C::kQBytes);
+    float2* s_ml = reinterpret_cast<float2*>(tail + C::kQBytes + C::kMergeBytes);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], C::kConsumers);
+        }
+        fence_mbar_init();
+        s_abort = 0;
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    grid_dependents_launch();
+    grid_dependency_wait();
+    find_share<C>(p, &s_share, s_warp);
+    volatile int* abort_flag = &s_abort;
+
+    const long long end = s_share.end;
+    long long pos = s_share.begin;
+    if (pos >= end) {
+        if (tid == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = 0;
+        return;
+    }
+    Cursor<C::kRows> u;
+    u.b = s_share.b;
+    u.rt = s_share.rt;
+    u.h = s_share.h;
+    u.enter(p);
+    int tile = s_share.tile;
+    if (p.whole && tile != 0) {  // begun by the CTA before, which finishes it
+        pos += u.cost() - tile;
+        tile = 0;
+        u.next(p);
+    }
+
+    if (warp == C::kConsumers) {
+        // copies: the warp holds the next 32 table entries, its first lane issues
+        int n = 0;  // tiles issued
+        int pieces = 0;
+        bool ok = true;
+        while (ok && pos < end) {
+            const int take =
+                p.whole ? u.cost() : (int)min((long long)(u.cost() - tile), end - pos);
+            const int last = min(u.tiles, tile + take);
+            const int32_t* row = p.bt.block_table + (int64_t)u.b * p.bt.max_pages;
+            int ahead = tile + lane < last ? __ldg(row + tile + lane) : -1;
+            for (int t = tile; ok && t < last; ++t) {
+                const int i = (t - tile) & 31;
+                if (i == 0 && t != tile) ahead = t + lane < last ? __ldg(row + t + lane) : -1;
+                const int page = __shfl_sync(0xffffffffu, ahead, i);
+                const int st = n % C::kStages;
+                int go = 1;
+                if (lane == 0) {
+                    go = n < C::kStages ||
+                         mbar_wait(&s_empty[st], ((n / C::kStages) - 1) & 1, abort_flag);
+                    if (go) {
+                        const bool valid = page >= 0 && page < p.bt.num_pages;
+                        s_valid[st] = valid;
+                        if (valid) {
+                            mbar_arrive_expect_tx(&s_full[st], C::kStageBytes);
+                            uint8_t* dst = ring + st * C::kStageBytes;
+                            const int z = page * p.kv_heads + u.h;
+#pragma unroll
+                            for (int x = 0; x < C::kBoxes; ++x)
+                                tma_load_3d(dst + x * (kPage * C::kBoxBytes), &tm_k,
+                                            x * C::kBoxBytes, 0, z, &s_full[st]);
+#pragma unroll
+                            for (int x = 0; x < C::kBoxes; ++x)
+                                tma_load_3d(dst + C::kTileBytes + x * (kPage * C::kBoxBytes), &tm_v,
+                                            x * C::kBoxBytes, 0, z, &s_full[st]);
+                        } else {
+                            record_error(p.status, DSA_ERR_DEVICE_CHECK);
+                            mbar_arrive(&s_full[st]);
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+                if (ok) ++n;
+            }
+            if (lane == 0 && tile == 0 && take < u.cost()) {
+                // first piece of a row tile that other CTAs finish
+                int32_t* j = p.joins + blockIdx.x * kJoinInts;
+                pieces = 1 + (int)((u.cost() - take + s_share.per - 1) / s_share.per);
+                j[kJoinToken] = u.r.q0;
+                j[kJoinRow] = u.rt * C::kRows;
+                j[kJoinRows] = min(C::kRows, u.r.rows - u.rt * C::kRows);
+                j[kJoinHead] = u.h * p.group;
+            }
+            pos += take;
+            tile = 0;
+            u.next(p);
+        }
+        if (lane == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
+        if (lane == 0 && *abort_flag) {
+            // an unwinding CTA must not exit under copies in flight
+            for (int i = max(0, n - C::kStages); i < n; ++i)
+                mbar_drain(&s_full[i % C::kStages], (i / C::kStages) & 1);
+            record_error(p.status, DSA_ERR_TIMEOUT);
+        }
+        return;
+    }
+
+    const int wm = warp % C::kWM, wn = warp / C::kWM;
+    const int g = lane >> 2, c = lane & 3;
+    const int sw = C::kBoxBytes == 128 ? lane & 7 : (lane >> 1) & 3;
+    // ldmatrix rows and chunks of this lane: keys by token halves and chunk,
+    // values (transposed) by chunk and token halves
+    const int k_row = wn * C::kTokens + ((lane >> 4) << 3) + (lane & 7), k_chunk = (lane >> 3) & 1;
+    const int v_row = wn * C::kTokens + (((lane >> 3) & 1) << 3) + (lane & 7), v_chunk = lane >> 4;
+    const uint32_t ring_u32 = smem_u32(ring);
+    auto chunk_at = [&](int row, int chunk) -> uint32_t {
+        if (C::kBoxBytes == 128)
+            return (uint32_t)((chunk >> 3) * (kPage * 128) + row * 128 + (((chunk & 7) ^ sw) << 4));
+        return (uint32_t)(row * C::kBoxBytes + ((chunk ^ sw) << 4));
+    };
+    int n = 0;  // tiles consumed
+    bool dead = false;
+
+    while (pos < end) {
+        const int take = p.whole ? u.cost() : (int)min((long long)(u.cost() - tile), end - pos);
+        const int row0 = u.rt * C::kRows + wm * 16;
+        // this thread's rows: g and g + 8 of the warp's 16
+        const int rows_left = u.r.rows - row0;
+        const bool in0 = g < rows_left, in1 = g + 8 < rows_left;
+        const int j0 = (row0 + g) / p.group, j1 = (row0 + g + 8) / p.group;
+        const int h0 = u.h * p.group + (row0 + g) % p.group;
+        const int h1 = u.h * p.group + (row0 + g + 8) % p.group;
+        const int vis0 = in0 ? u.r.seq - u.r.nb + j0 + 1 : 0;
+        const int vis1 = in1 ? u.r.seq - u.r.nb + j1 + 1 : 0;
+        const int vis_first = u.r.seq - u.r.nb + row0 / p.group + 1;
+
+        // queries as A fragments; for FP8 the columns of a 16-value group are taken
+        // in the order in which the lifted keys come, 4 c .. 4 c + 3
+        float f0 = p.score_scale, f1 = p.score_scale;
+        uint32_t qf[C::kQSmem ? 1 : kD / 16][4];
+        if (!C::kQSmem || wn == 0) {
+            const uint16_t* q0 = static_cast<const uint16_t*>(p.q) +
+                                 (int64_t)(u.r.q0 + j0) * p.q_stride + (int64_t)h0 * kD;
+            const uint16_t* q1 = static_cast<const uint16_t*>(p.q) +
+                                 (int64_t)(u.r.q0 + j1) * p.q_stride + (int64_t)h1 * kD;
+            auto fragment = [&](int ks, uint32_t (&a)[4]) {
+                if (C::kFp8) {
+                    const uint2 x = in0 ? *reinterpret_cast<const uint2*>(q0 + ks * 16 + 4 * c)
+                                        : make_uint2(0, 0);
+                    const uint2 y = in1 ? *reinterpret_cast<const uint2*>(q1 + ks * 16 + 4 * c)
+                                        : make_uint2(0, 0);
+                    a[0] = x.x;
+                    a[1] = y.x;
+                    a[2] = x.y;
+                    a[3] = y.y;
+                } else {
+                    const int at = ks * 16 + 2 * c;
+                    a[0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + at) : 0;
+                    a[1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + at) : 0;
+                    a[2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + at + 8) : 0;
+                    a[3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + at + 8) : 0;
+                }
+            };
+            float up0 = 1.f, up1 = 1.f;
+            if (C::kFp8 && kQBf16) {
+                // bf16 to f16: scale the row by a power of two that brings its
+                // largest value to 1..2 (what then falls below f16's range is
+                // below 2^-25 of that value), and undo it in the score factor
+                uint32_t top0 = 0, top1 = 0;
+                for (int ks = 0; ks < kD / 16; ++ks) {
+                    uint32_t a[4];
+                    fragment(ks, a);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t x = max(a[i] & 0x7fffu, (a[i] >> 16) & 0x7fffu);
+                        if (i & 1) top1 = max(top1, x);
+                        else top0 = max(top0, x);
+                    }
+                }
+                top0 = max(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
+                top0 = max(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
+                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
+                // biased exponents; zero, infinite and NaN rows stay unscaled
+                const uint32_t e0 = top0 >> 7, e1 = top1 >> 7;
+                if (e0 != 0 && e0 < 254) {
+                    up0 = __uint_as_float((254 - e0) << 23);
+                    f0 *= __uint_as_float(e0 << 23);
+                }
+                if (e1 != 0 && e1 < 254) {
+                    up1 = __uint_as_float((254 - e1) << 23);
+                    f1 *= __uint_as_float(e1 << 23);
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                uint32_t a[4];
+                fragment(ks, a);
+                if (C::kFp8 && kQBf16) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float up = (i & 1) ? up1 : up0;
+                        a[i] = pack2<false>(__uint_as_float(a[i] << 16) * up,
+                                            __uint_as_float(a[i] & 0xffff0000u) * up);
+                    }
+                }
+                if (C::kQSmem) {
+                    s_q[(wm * (kD / 16) + ks) * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qf[C::kQSmem ? 0 : ks][i] = a[i];
+                }
+            }
+            if (C::kQSmem && C::kFp8 && c == 0) {
+                s_ml[wm * 16 + g] = make_float2(f0, 0.f);
+                s_ml[wm * 16 + g + 8] = make_float2(f1, 0.f);
+            }
+        }
+        if (C::kQSmem) {
+            consumer_sync<32 * C::kConsumers>();
+            if (C::kFp8) {
+                f0 = s_ml[wm * 16 + g].x;
+                f1 = s_ml[wm * 16 + g + 8].x;
+                consumer_sync<32 * C::kConsumers>();
+            }
+        }
+
+        float o[C::kTilesD][4];
+#pragma unroll
+        for (int i = 0; i < C::kTilesD; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+        const int last = min(u.tiles, tile + take);
+        for (int t = tile; t < last; ++t, ++n) {
+            const int st = n % C::kStages;
+            if (!dead) dead = !mbar_wait(&s_full[st], (n / C::kStages) & 1, abort_flag);
+            dead = __any_sync(0xffffffffu, dead);
+            if (dead) continue;
+            if (s_valid[st]) {
+                const uint32_t ks = ring_u32 + st * C::kStageBytes, vs = ks + C::kTileBytes;
+                const int first = t * kPage + wn * C::kTokens;  // this warp's first position
+                if (first + C::kTokens > u.r.seq) {
+                    // stale rows past the context may hold anything: p is 0 there, but
+                    // 0 * NaN is not
+                    const int keep = max(0, u.r.seq - first);
+                    uint8_t* v = ring + st * C::kStageBytes + C::kTileBytes;
+                    for (int i = lane; i < (C::kTokens - keep) * (C::kRowBytes / 16); i += 32) {
+                        const int r = wn * C::kTokens + keep + i / (C::kRowBytes / 16);
+                        const int x = i % (C::kRowBytes / 16), per = C::kBoxBytes / 16;
+                        *reinterpret_cast<uint4*>(v + (x / per) * (kPage * C::kBoxBytes) +
+                                                  r * C::kBoxBytes + (x % per) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();  // the next copy into this stage comes after
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int sub = 0; sub < C::kTokens; sub += C::kSub) {
+                    constexpr int kNt = C::kSub / 8;
+                    float s[kNt][4];
+#pragma unroll
+                    for (int i = 0; i < kNt; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < C::kPairs; ++j) {
+                        uint32_t qa[4], qb[4];
+                        if (C::kFp8) {  // 32 values: two MMA steps
+                            if (C::kQSmem) {
+                                const uint4 x = s_q[(wm * (kD / 16) + 2 * j) * 32 + lane];
+                                const uint4 y = s_q[(wm * (kD / 16) + 2 * j + 1) * 32 + lane];
+                                qa[0] = x.x, qa[1] = x.y, qa[2] = x.z, qa[3] = x.w;
+                                qb[0] = y.x, qb[1] = y.y, qb[2] = y.z, qb[3] = y.w;
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    qa[i] = qf[C::kQSmem ? 0 : 2 * j][i];
+                                    qb[i] = qf[C::kQSmem ? 0 : 2 * j + 1][i];
+                                }
+                            }
+                        } else if (C::kQSmem) {
+                            const uint4 x = s_q[(wm * (kD / 16) + j) * 32 + lane];
+                            qa[0] = x.x, qa[1] = x.y, qa[2] = x.z, qa[3] = x.w;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) qa[i] = qf[C::kQSmem ? 0 : j][i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < C::kSub / 16; ++i) {
+                            uint32_t k[4];
+                            ldmatrix4(k, ks + chunk_at(k_row + sub + 16 * i, 2 * j + k_chunk));
+                            if (C::kFp8) {
+                                mma16816<false>(s[2 * i], qa, lift(k[0]), lift(k[0] >> 16));
+                                mma16816<false>(s[2 * i + 1], qa, lift(k[2]), lift(k[2] >> 16));
+                                mma16816<false>(s[2 * i], qb, lift(k[1]), lift(k[1] >> 16));
+                                mma16816<false>(s[2 * i + 1], qb, lift(k[3]), lift(k[3] >> 16));
+                            } else {
+                                mma16816<kBf16>(s[2 * i], qa, k[0], k[1]);
+                                mma16816<kBf16>(s[2 * i + 1], qa, k[2], k[3]);
+                            }
+                        }
+                    }
+                    if (t * kPage + kPage > vis_first) {
+#pragma unroll
+                        for (int i = 0; i < kNt; ++i) {
+                            const int at = first + sub + 8 * i + 2 * c;
+                            if (at >= vis0) s[i][0] = -INFINITY;
+                            if (at + 1 >= vis0) s[i][1] = -INFINITY;
+                            if (at >= vis1) s[i][2] = -INFINITY;
+                            if (at + 1 >= vis1) s[i][3] = -INFINITY;
+                        }
+                    }
+                    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < kNt; ++i) {
+                        x0 = fmaxf(x0, fmaxf(s[i][0], s[i][1]));
+                        x1 = fmaxf(x1, fmaxf(s[i][2], s[i][3]));
+                    }
+                    x0 = fmaxf(m0, quad_max(x0) * f0);
+                    x1 = fmaxf(m1, quad_max(x1) * f1);
+                    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+                        const float a0 = ex2(m0 - base_of(x0)), a1 = ex2(m1 - base_of(x1));
+                        l0 *= a0;
+                        l1 *= a1;
+#pragma unroll
+                        for (int i = 0; i < C::kTilesD; ++i) {
+                            o[i][0] *= a0;
+                            o[i][1] *= a0;
+                            o[i][2] *= a1;
+                            o[i][3] *= a1;
+                        }
+                        m0 = x0;
+                        m1 = x1;
+                    }
+                    const float b0 = base_of(m0), b1 = base_of(m1);
+#pragma unroll
+                    for (int i = 0; i < kNt; ++i) {
+                        s[i][0] = ex2(fmaf(s[i][0], f0, -b0));
+                        s[i][1] = ex2(fmaf(s[i][1], f0, -b0));
+                        s[i][2] = ex2(fmaf(s[i][2], f1, -b1));
+                        s[i][3] = ex2(fmaf(s[i][3], f1, -b1));
+                        l0 += s[i][0] + s[i][1];
+                        l1 += s[i][2] + s[i][3];
+                    }
+                    // P rounded to the operand type (the sums above are of the unrounded
+                    // values): half a step per probability, which averages out as the
+                    // output's own rounding does
+#pragma unroll
+                    for (int i = 0; i < C::kSub / 16; ++i) {
+                        const uint32_t pf[4] = {pack2<kBf16>(s[2 * i][0], s[2 * i][1]),
+                                                pack2<kBf16>(s[2 * i][2], s[2 * i][3]),
+                                                pack2<kBf16>(s[2 * i + 1][0], s[2 * i + 1][1]),
+                                                pack2<kBf16>(s[2 * i + 1][2], s[2 * i + 1][3])};
+#pragma unroll
+                        for (int j = 0; j < C::kPairs; ++j) {
+                            uint32_t v[4];
+                            ldmatrix4_t(v, vs + chunk_at(v_row + sub + 16 * i, 2 * j + v_chunk));
+                            if (C::kFp8) {
+                                // each register: two tokens by two dims; split by dim
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const uint32_t lo = __byte_perm(v[2 * x], 0, 0x3120);
+                                    const uint32_t hi = __byte_perm(v[2 * x + 1], 0, 0x3120);
+                                    mma16816<false>(o[C::kFp8 ? 4 * j + 2 * x : 0], pf, lift(lo),
+                                                    lift(hi));
+                                    mma16816<false>(o[C::kFp8 ? 4 * j + 2 * x + 1 : 0], pf,
+                                                    lift(lo >> 16), lift(hi >> 16));
+                                }
+                            } else {
+                                mma16816<kBf16>(o[C::kFp8 ? 0 : 2 * j], pf, v[0], v[1]);
+                                mma16816<kBf16>(o[C::kFp8 ? 0 : 2 * j + 1], pf, v[2], v[3]);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[st]);
+        }
+
+        // join the warps that share rows
+        l0 = quad_sum(l0);
+        l1 = quad_sum(l1);
+        if (C::kWN > 1) {
+            if (c == 0) {
+                s_ml[wn * C::kRows + wm * 16 + g] = make_float2(m0, l0);
+                s_ml[wn * C::kRows + wm * 16 + g + 8] = make_float2(m1, l1);
+            }
+            consumer_sync<32 * C::kConsumers>();
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < C::kWN; ++w) {
+                t0 = fmaxf(t0, s_ml[w * C::kRows + wm * 16 + g].x);
+                t1 = fmaxf(t1, s_ml[w * C::kRows + wm * 16 + g + 8].x);
+            }
+            const float b0 = base_of(t0), b1 = base_of(t1);
+            l0 = l1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < C::kWN; ++w) {
+                const float2 x = s_ml[w * C::kRows + wm * 16 + g];
+                const float2 y = s_ml[w * C::kRows + wm * 16 + g + 8];
+                l0 += x.y * ex2(x.x - b0);
+                l1 += y.y * ex2(y.x - b1);
+            }
+            const float a0 = ex2(m0 - b0), a1 = ex2(m1 - b1);
+            m0 = t0;
+            m1 = t1;
+#pragma unroll
+            for (int i = 0; i < C::kTilesD; ++i) {
+                o[i][0] *= a0;
+                o[i][1] *= a0;
+                o[i][2] *= a1;
+                o[i][3] *= a1;
+            }
+            // halve the warps, 64 dims at a time through the merge buffer
+#pragma unroll
+            for (int half = C::kWN / 2; half >= 1; half /= 2) {
+#pragma unroll
+                for (int d0 = 0; d0 < C::kTilesD; d0 += 8) {
+                    if (wn >= half && wn < 2 * half) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            s_merge[(((wn - half) * C::kWM + wm) * 8 + i) * 32 + lane] =
+                                make_float4(o[d0 + i][0], o[d0 + i][1], o[d0 + i][2], o[d0 + i][3]);
+                    }
+                    consumer_sync<32 * C::kConsumers>();
+                    if (wn < half) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 x = s_merge[((wn * C::kWM + wm) * 8 + i) * 32 + lane];
+                            o[d0 + i][0] += x.x;
+                            o[d0 + i][1] += x.y;
+                            o[d0 + i][2] += x.z;
+                            o[d0 + i][3] += x.w;
+                        }
+                    }
+                    consumer_sync<32 * C::kConsumers>();
+                }
+            }
+        }
+        if (wn == 0) {
+            const bool complete = tile == 0 && take == u.cost();
+            const int64_t r0 = (int64_t)(u.r.q0 + j0) * (p.kv_heads * p.group) + h0;
+            const int64_t r1 = (int64_t)(u.r.q0 + j1) * (p.kv_heads * p.group) + h1;
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0);
+            const int64_t s0 = slot * C::kRows + wm * 16 + g, s1 = s0 + 8;
+            if (complete) {
+                const float i0 = l0 == 0.f ? 0.f : p.v_scale / l0;
+                const float i1 = l1 == 0.f ? 0.f : p.v_scale / l1;
+#pragma unroll
+                for (int i = 0; i < C::kTilesD; ++i) {
+                    o[i][0] *= i0;
+                    o[i][1] *= i0;
+                    o[i][2] *= i1;
+                    o[i][3] *= i1;
+                }
+                if (p.lse && c == 0) {
+                    if (in0) p.lse[r0] = l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * kLn2;
+                    if (in1) p.lse[r1] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * kLn2;
+                }
+            } else if (c == 0) {
+                *reinterpret_cast<float2*>(p.part_ml + 2 * s0) = make_float2(m0, l0);
+                *reinterpret_cast<float2*>(p.part_ml + 2 * s1) = make_float2(m1, l1);
+            }
+            uint16_t* out = static_cast<uint16_t*>(p.out);
+            if (C::kFp8) {
+#pragma unroll
+                for (int i = 0; i < C::kTilesD / 2; ++i) {
+                    const int d = 16 * i + 4 * c;
+                    const float(&e)[4] = o[2 * i];
+                    const float(&f)[4] = o[2 * i + 1];
+                    if (complete) {
+                        if (in0)
+                            *reinterpret_cast<uint2*>(out + r0 * kD + d) =
+                                make_uint2(pack2<kQBf16>(e[0], f[0]), pack2<kQBf16>(e[1], f[1]));
+                        if (in1)
+                            *reinterpret_cast<uint2*>(out + r1 * kD + d) =
+                                make_uint2(pack2<kQBf16>(e[2], f[2]), pack2<kQBf16>(e[3], f[3]));
+                    } else {
+                        *reinterpret_cast<float4*>(p.part_o + s0 * kD + d) =
+                            make_float4(e[0], f[0], e[1], f[1]);
+                        *reinterpret_cast<float4*>(p.part_o + s1 * kD + d) =
+                            make_float4(e[2], f[2], e[3], f[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::kTilesD; ++i) {
+                    const int d = 8 * i + 2 * c;
+                    if (complete) {
+                        if (in0)
+                            *reinterpret_cast<uint32_t*>(out + r0 * kD + d) =
+                                pack2<kQBf16>(o[i][0], o[i][1]);
+                        if (in1)
+                            *reinterpret_cast<uint32_t*>(out + r1 * kD + d) =
+                                pack2<kQBf16>(o[i][2], o[i][3]);
+                    } else {
+                        *reinterpret_cast<float2*>(p.part_o + s0 * kD + d) =
+                            make_float2(o[i][0], o[i][1]);
+                        *reinterpret_cast<float2*>(p.part_o + s1 * kD + d) =
+                            make_float2(o[i][2], o[i][3]);
+                    }
+                }
+            }
+        }
+        pos += take;
+        tile = 0;
+        u.next(p);
+    }
+    if (dead && lane == 0) record_error(p.status, DSA_ERR_TIMEOUT);
+}
+
+// Joins the pieces of a row tile: block (CTA that wrote the first piece, row).
+// Groups of kDim / 4 threads take every kGroups-th piece with a running maximum
+// each, then the groups are added in order.
+constexpr int kJoinThreads = 128;
+
+template <int kDim, bool kQBf16>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnParams p, int rows) {
+    constexpr int kLanes = kDim / 4, kGroups = kJoinThreads / kLanes;
+    __shared__ float4 s_o[kGroups][kLanes];
+    __shared__ float2 s_ml[kGroups];
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int cta = blockIdx.x, row = blockIdx.y;
+    const int32_t* j = p.joins + cta * kJoinInts;
+    const int pieces = __ldcg(j + kJoinPieces);
+    if (pieces == 0 || row >= __ldcg(j + kJoinRows)) return;
+    const int x = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < pieces; i += kGroups) {
+        const int64_t at = (2 * (int64_t)(cta + i) + (i == 0 ? 1 : 0)) * rows + row;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kDim) + x);
+        const float top = fmaxf(m, ml.x), base = base_of(top);
+        const float a = ex2(m - base), b = ex2(ml.x - base);
+        m = top;
+        l = l * a + ml.y * b;
+        o.x = o.x * a + v.x * b;
+        o.y = o.y * a + v.y * b;
+        o.z = o.z * a + v.z * b;
+        o.w = o.w * a + v.w * b;
+    }
+    s_o[grp][x] = o;
+    if (x == 0) s_ml[grp] = make_float2(m, l);
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float2 ml = s_ml[i];
+        const float4 v = s_o[i][x];
+        const float top = fmaxf(m, ml.x), base = base_of(top);
+        const float a = ex2(m - base), b = ex2(ml.x - base);
+        m = top;
+        l = l * a + ml.y * b;
+        o.x = o.x * a + v.x * b;
+        o.y = o.y * a + v.y * b;
+        o.z = o.z * a + v.z * b;
+        o.w = o.w * a + v.w * b;
+    }
+    const int r = __ldcg(j + kJoinRow) + row;
+    const int64_t at = (int64_t)(__ldcg(j + kJoinToken) + r / p.group) * (p.kv_heads * p.group) +
+                       __ldcg(j + kJoinHead) + r % p.group;
+    const float inv = l == 0.f ? 0.f : p.v_scale / l;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * kDim + 4 * x) =
+        make_uint2(pack2<kQBf16>(o.x * inv, o.y * inv), pack2<kQBf16>(o.z * inv, o.w * inv));
+    if (p.lse && x == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ---- launch --------------------------------------------------------------------
+
+// A pool as [pages x KV heads][64 tokens][row bytes], boxes of 64 tokens by up to 128
+// bytes, swizzled so that eight rows' chunks of one column fall into all banks.
+bool encode_pool(CUtensorMap* tm, const void* base, const dsa_kv_cache& c, int row_bytes) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int box_bytes = row_bytes < 128 ? row_bytes : 128;
+    cuuint64_t dims[3] = {(cuuint64_t)row_bytes, kPage, (cuuint64_t)c.num_pages * c.num_kv_heads};
+    cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)row_bytes * kPage};
+    cuuint32_t box[3] = {(cuuint32_t)box_bytes, kPage, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxCtas = 2 * 152;  // pieces are kept for this many CTAs
+constexpr int kMinTiles = 2;
+
+// Rows of a tile for requests of up to max_rows rows: the smallest that holds
+// them, so that the cache is read once, but 16 when every request runs whole
+// (a row's arithmetic must not depend on the other requests' row counts).
+int row_tile(int64_t max_rows, bool whole) {
+    return whole || max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
+}
+
+struct WsLayout {
+    size_t ml, joins, total;
+};
+WsLayout ws_layout(int dim, int rows) {
+    WsLayout w;
+    w.ml = (size_t)2 * kMaxCtas * rows * dim * sizeof(float);
+    w.joins = w.ml + (size_t)2 * kMaxCtas * rows * 2 * sizeof(float);
+    w.total = w.joins + (size_t)kMaxCtas * kJoinInts * sizeof(int32_t);
+    return w;
+}
+
+template <typename C, bool kQBf16>
+cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
+                       cudaStream_t stream) {
+    CUtensorMap tm_k, tm_v;
+    if (!encode_pool(&tm_k, cache.k_pages, cache, C::kRowBytes) ||
+        !encode_pool(&tm_v, cache.v_pages, cache, C::kRowBytes))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<C, kQBf16>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return e;
+    // no more CTAs than the longest list that these host sizes allow has work for
+    const int64_t tiles = ((int64_t)p.bt.max_seq + kPage - 1) / kPage;
+    const int64_t row_tiles = ((int64_t)p.bt.max_q * p.group + C::kRows - 1) / C::kRows;
+    const double most = (double)p.bt.num_requests * row_tiles * p.kv_heads * tiles;
+    int ctas = sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas;
+    if (most < (double)ctas * p.min_tiles)
+        ctas = (int)((most + p.min_tiles - 1) / p.min_tiles);
+    if (ctas < 1) ctas = 1;
+    e = launch_kernel(paged_attention_kernel<C, kQBf16>, dim3((unsigned)ctas), dim3(C::kThreads),
+                      (size_t)C::kSmem, stream, true, 1, tm_k, tm_v, p);
+    if (e != cudaSuccess || p.whole || ctas == 1) return e;
+    *launches = 2;
+    const int64_t rows = (int64_t)p.bt.max_q * p.group;
+    const dim3 grid((unsigned)ctas, (unsigned)(rows < C::kRows ? rows : C::kRows));
+    return launch_kernel(paged_join_kernel<C::kDim, kQBf16>, grid, dim3(kJoinThreads), 0, stream,
+                         true, 1, p, (int)C::kRows);
+}
+
+template <int kD, bool kFp8, bool kQBf16>
+cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* launches,
+                        cudaStream_t stream) {
+    // D = 256: 128 accumulator registers a thread leave room for four consumer
+    // warps, not eight
+    constexpr bool kWide = kD == 256;
+    switch (row_tile((int64_t)p.bt.max_q * p.group, p.whole != 0)) {
+        case 16:
+            return launch_cfg<AttnCfg<kD, kFp8, 1, 4>, kQBf16>(p, cache, launches, stream);
+        case 32:
+            return launch_cfg<AttnCfg<kD, kFp8, 2, kWide ? 2 : 4>, kQBf16>(p, cache, launches,
+                                                                           stream);
+        default:
+            return launch_cfg<AttnCfg<kD, kFp8, 4, kWide ? 1 : 2>, kQBf16>(p, cache, launches,
+                                                                           stream);
+    }
+}
+
+template <int kD>
+cudaError_t launch_dim(const AttnParams& p, const dsa_kv_cache& cache, int format, int* launches,
+                       cudaStream_t stream) {
+    const bool fp8 = cache.format == DSA_KV_FP8_E4M3;
+    if (format == DSA_FLOAT_BF16)
+        return fp8 ? launch_rows<kD, true, true>(p, cache, launches, stream)
+                   : launch_rows<kD, false, true>(p, cache, launches, stream);
+    return fp8 ? launch_rows<kD, true, false>(p, cache, launches, stream)
+               : launch_rows<kD, false, false>(p, cache, launches, stream);
+}
+
+}  // namespace
+
+// Of the default plan, which needs more than the whole one.
+size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim) {
+    return ws_layout(head_dim, row_tile(max_rows, false)).total;
+}
+
+cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cache, int format,
+                                   int num_q_heads, const void* q, int64_t q_stride,
+                                   float sm_scale, void* out, float* lse, void* ws, bool whole,
+                                   int32_t* status, int* launches, cudaStream_t stream) {
+    AttnParams p;
+    p.bt = bt;
+    p.kv_heads = cache.num_kv_heads;
+    p.group = num_q_heads / cache.num_kv_heads;
+    p.min_tiles = kMinTiles;
+    p.whole = whole;
+    p.q_stride = q_stride;
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.score_scale = sm_scale * cache.k_scale * kLog2e;
+    p.v_scale = cache.v_scale;
+    const WsLayout w = ws_layout(cache.head_dim, row_tile((int64_t)bt.max_q * p.group, false));
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(base);
+    p.part_ml = reinterpret_cast<float*>(base + w.ml);
+    p.joins = reinterpret_cast<int32_t*>(base + w.joins);
+    p.status = status;
+    *launches = 1;
+    switch (cache.head_dim) {
+        case 64: return launch_dim<64>(p, cache, format, launches, stream);
+        case 128: return launch_dim<128>(p, cache, format, launches, stream);
+        default: return launch_dim<256>(p, cache, format, launches, stream);
+    }
+}
+
+}  // namespace dsa

@@ -396,8 +396,9 @@ int32_t dsa_plan_token_shards(const int32_t* seq_lens, const int32_t* q_counts,
  * No counterpart on the pages: an addition of this library, for the layers of a
  * model that attend to every cached position (a draft model, a dense layer)
  * and for building the batch metadata of every other call on the GPU.  The
- * calls, in the order a step makes them: dsa_build_tables, dsa_rope_append.
- * They allocate nothing and may be captured into a CUDA graph. */
+ * calls, in the order a step makes them: dsa_build_tables, dsa_rope_append,
+ * dsa_paged_attention.  They allocate nothing and may be captured into a CUDA
+ * graph. */
 
 /* Element type of queries, keys, values and outputs. */
 typedef enum { DSA_FLOAT_BF16 = 0, DSA_FLOAT_F16 = 1 } dsa_float_format;
@@ -507,6 +508,39 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
                            int32_t num_q_heads, const void* q, int64_t q_stride, const void* k,
                            int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
                            int64_t q_out_stride, int32_t* dev_status, dsa_stream_t stream);
+
+/* Attention of the batch's query tokens over every cached position they see.
+ * num_q_heads / num_kv_heads = G query heads share a KV head: query head i
+ * reads KV head i / G.  For token t, at place j of request b's n_b, and head i:
+ *   z[s] = sm_scale * q[t,i,:] . key(s)       for s <= seq_lens[b] - n_b + j
+ *   out[t,i,:] = sum_s softmax_s(z[s]) * value(s)
+ *   lse[t,i]   = log sum_s exp(z[s])          (natural log)
+ * The new tokens' own keys and values must be in the cache already.  Any n_b
+ * is taken; the kernel is made for decode and verification steps (a few
+ * tokens per request).
+ *   q    [T, num_q_heads, head_dim] of `format`, tokens q_stride elements apart
+ *        (a multiple of 8), 16-byte aligned
+ *   out  [T, num_q_heads, head_dim] of `format`, contiguous, 16-byte aligned
+ *   lse  [T, num_q_heads] fp32 (may be NULL)
+ *   ws   device scratch of dsa_paged_attention_workspace_size() bytes, 16-byte
+ *        aligned; its contents need not be kept between calls
+ * Unlike the other calls this one takes seq_lens[b] < n_b: tokens before
+ * position 0 see nothing, so a padding request has seq_lens[b] = 0 and any
+ * n_b.  A token that sees nothing gives out = 0 and lse = -inf.
+ * Cache contents at positions at or beyond seq_lens[b] never reach a result,
+ * whatever they hold.
+ * Device checks: a table entry outside [0, num_pages) is recorded as
+ * DSA_ERR_DEVICE_CHECK and its positions are left out; a request whose arrays
+ * contradict the host sizes is recorded too and its rows are not written.
+ * batch->num_pages must equal cache->num_pages.  Under
+ * dsa_set_batch_invariant each (request, KV head) runs whole, as a token does in
+ * dsa_sparse_mla.  One or two kernel launches. */
+size_t dsa_paged_attention_workspace_size(const dsa_batch* batch, const dsa_kv_cache* cache,
+                                          int32_t num_q_heads);
+dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache,
+                               dsa_float_format format, int32_t num_q_heads, const void* q,
+                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -64,13 +64,18 @@ def turn_reference(x, positions, inv_freq, sections, interleaved):
 
 def attention_reference(q, k_pages, v_pages, k_scale, v_scale, sm_scale, offsets, lens, table,
                         num_pages):
-    """float64 (out, lse) of [T, Hq, D] queries, one request and KV head at a
-    time; positions of pages outside the pool are left out."""
+    """In float64, one request and KV head at a time, for [T, Hq, D] queries:
+      out, lse   the definition; positions of pages outside the pool are left out
+      mean_abs   sum_s softmax_s |v_s|, what a relative error of p costs
+      max_abs    the largest |v| seen, and
+      terms      the largest sm_scale sum_d |q_d k_d| seen, of each row."""
     T, hq, d = q.shape
     hkv = k_pages.shape[1]
     g = hq // hkv
-    out = torch.zeros(T, hq, d, dtype=torch.float64, device=q.device)
-    lse = torch.full((T, hq), -float("inf"), dtype=torch.float64, device=q.device)
+    f64 = dict(dtype=torch.float64, device=q.device)
+    r = dict(out=torch.zeros(T, hq, d, **f64), lse=torch.full((T, hq), -float("inf"), **f64),
+             mean_abs=torch.zeros(T, hq, d, **f64), max_abs=torch.zeros(T, hq, **f64),
+             terms=torch.zeros(T, hq, **f64))
     for b in range(len(lens)):
         q0, n, length = offsets[b], offsets[b + 1] - offsets[b], lens[b]
         if n == 0 or length == 0:
@@ -82,18 +87,23 @@ def attention_reference(q, k_pages, v_pages, k_scale, v_scale, sm_scale, offsets
         pages = pages.clamp(0, num_pages - 1)
         pos = torch.arange(length, device=q.device)[there]
         last = torch.arange(length - n, length, device=q.device)
-        hidden = pos[None, :] > last[:, None]
+        hidden = (pos[None, :] > last[:, None])[:, None, :]
         for h in range(hkv):
             k = k_pages[pages, h].double().flatten(0, 1)[:length][there] * k_scale
             v = v_pages[pages, h].double().flatten(0, 1)[:length][there] * v_scale
-            heads = slice(h * g, (h + 1) * g)
-            z = torch.einsum("tgd,sd->tgs", q[q0:q0 + n, heads].double(), k) * sm_scale
-            z = z.masked_fill(hidden[:, None, :], -float("inf"))
+            rows, heads = slice(q0, q0 + n), slice(h * g, (h + 1) * g)
+            x = q[rows, heads].double() * sm_scale
+            z = torch.einsum("tgd,sd->tgs", x, k).masked_fill(hidden, -float("inf"))
+            sizes = torch.einsum("tgd,sd->tgs", x.abs(), k.abs()).masked_fill(hidden, 0.0)
             top = z.amax(-1, keepdim=True)
             seen = torch.isfinite(top)
-            p = torch.where(seen, torch.exp(z - torch.where(seen, top, torch.zeros_like(top))),
-                            torch.zeros_like(z))
+            p = torch.where(seen, torch.exp(z - torch.where(seen, top, 0.0)), 0.0)
             total = p.sum(-1)
-            out[q0:q0 + n, heads] = torch.einsum("tgs,sd->tgd", p, v) / total.clamp_min(1e-300)[..., None]
-            lse[q0:q0 + n, heads] = torch.where(seen[..., 0], top[..., 0] + torch.log(total), lse[q0:q0 + n, heads])
-    return out, lse
+            p = p / total.clamp_min(1e-300)[..., None]
+            r["out"][rows, heads] = torch.einsum("tgs,sd->tgd", p, v)
+            r["mean_abs"][rows, heads] = torch.einsum("tgs,sd->tgd", p, v.abs())
+            r["max_abs"][rows, heads] = torch.where(hidden, 0.0, v.abs().amax(-1)).amax(-1)
+            r["terms"][rows, heads] = sizes.amax(-1)
+            r["lse"][rows, heads] = torch.where(seen[..., 0], top[..., 0] + torch.log(total),
+                                                -float("inf"))
+    return r

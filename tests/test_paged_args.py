@@ -78,3 +78,47 @@ def test_rope_append_refusals(lib, kw, code):
 
 def test_rope_append_of_no_tokens_is_a_no_op(lib):
     assert _rope(lib, tokens=0) == 0
+
+
+def _attention(lib, batch=None, cache=None, fmt=0, hq=4, q=FAKE, qs=512, sm=0.1, out=FAKE, ws=FAKE,
+               ws_bytes=1 << 40):
+    import dsa_sparse_attention_step_gb300 as dsa
+    b = dsa._CBatch(1, 1, 1, 4096, 8, 64, 64, 16, 32, 48)
+    for k, v in (batch or {}).items():
+        setattr(b, k, v)
+    c = _cache() if cache is None else cache
+    return lib.dsa_paged_attention(ctypes.byref(b), ctypes.byref(c), fmt, hq, q, qs, sm, out, None,
+                                   ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("kw,code", CACHE_REFUSALS)
+def test_cache_refusals_by_paged_attention(lib, kw, code):
+    assert _attention(lib, cache=_cache(**kw)) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=dict(page_size=32)), UNSUPPORTED), (dict(batch=dict(max_pages=10)), INVALID),
+    (dict(batch=dict(num_pages=9)), INVALID), (dict(fmt=1), UNSUPPORTED), (dict(hq=0), INVALID),
+    (dict(hq=5), INVALID), (dict(hq=1 << 15, qs=1 << 22), UNSUPPORTED), (dict(q=None), INVALID),
+    (dict(q=ODD), INVALID), (dict(qs=500), INVALID), (dict(sm=0.0), INVALID),
+    (dict(sm=float("nan")), INVALID), (dict(sm=float("inf")), INVALID), (dict(out=None), INVALID),
+    (dict(out=ODD), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=ODD), WORKSPACE),
+    (dict(ws_bytes=1000), WORKSPACE)])
+def test_paged_attention_refusals(lib, kw, code):
+    assert _attention(lib, **kw) == code
+
+
+def test_paged_attention_of_no_tokens_is_a_no_op(lib):
+    assert _attention(lib, batch=dict(total_q=0), q=None, out=None, ws=None) == 0
+
+
+def test_paged_attention_workspace_follows_rows_and_head_dim(lib):
+    import dsa_sparse_attention_step_gb300 as dsa
+    b = dsa._CBatch(4, 4, 1, 4096, 8, 64, 64, 16, 32, 48)
+
+    def size(hq, **kw):
+        c = _cache(**kw)
+        return lib.dsa_paged_attention_workspace_size(ctypes.byref(b), ctypes.byref(c), hq)
+    assert 0 < size(4) == size(32) < size(64) < size(128) == size(256)
+    assert size(4, head_dim=256) > size(4) > size(4, head_dim=64)
+    assert size(5) == 0 and size(0) == 0 and size(4, head_dim=96) == 0
