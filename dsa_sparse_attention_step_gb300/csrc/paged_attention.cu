@@ -62,33 +62,52 @@ struct AttnParams {
 // What a joining block needs to know of the row tile whose first piece a CTA wrote.
 enum { kJoinPieces, kJoinToken, kJoinRow, kJoinRows, kJoinHead, kJoinInts = 8 };
 
-template <int kD, bool kKvFp8, int kWM_, int kWN_>
+// Eight consumer warps: kNG groups, each taking every kNG-th page of the CTA's run;
+// within a group kWM warps along the rows (kMT tiles of 16 rows each) by kWN warps
+// along the page's tokens.
+template <int kD, bool kKvFp8, int kMT_, int kWM_, int kWN_, int kNG_>
 struct AttnCfg {
     static constexpr int kDim = kD;
     static constexpr bool kFp8 = kKvFp8;
-    static constexpr int kWM = kWM_;  // warps along the rows, 16 rows each
-    static constexpr int kWN = kWN_;  // warps along a tile's tokens
-    static constexpr int kRows = 16 * kWM;
-    static constexpr int kConsumers = kWM * kWN;
-    static constexpr int kThreads = 32 * (kConsumers + 1);
+    static constexpr int kMT = kMT_, kWM = kWM_, kWN = kWN_, kNG = kNG_;
+    static constexpr int kRows = 16 * kMT * kWM;
+    static constexpr int kConsumers = kWM * kWN * kNG;
+    static constexpr int kTokenWarps = kWN * kNG;  // warps that share a row
+    static constexpr int kThreads = 32 * (kConsumers + 4);
     static constexpr int kRowBytes = kD * (kKvFp8 ? 1 : 2);
     static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;
     static constexpr int kBoxes = kRowBytes / kBoxBytes;
     static constexpr int kTileBytes = kPage * kRowBytes;  // keys or values of one page
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kCtas = kConsumers <= 4 && kD < 256 ? 2 : 1;
-    static constexpr int kRing = kCtas == 2 ? 98304 : kStageBytes <= 32768 ? 163840 : 196608;
-    static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
-    static constexpr int kTokens = kPage / kWN;                 // of a tile, per warp
+    static constexpr int kTokens = kPage / kWN;                       // of a page, per warp
     static constexpr int kSub = kD == 256 || kTokens < 32 ? 16 : 32;  // softmax step
-    static constexpr int kPairs = kRowBytes / 32;               // pairs of 16-byte chunks in a row
-    static constexpr int kTilesD = kD / 8;                      // accumulator tiles along the dims
-    static constexpr bool kQSmem = kD == 256;  // 64 registers of Q fragments do not fit beside 128 of O
-    static constexpr int kQBytes = kQSmem ? kWM * (kD / 16) * 512 : 0;
-    static constexpr int kMergeBytes = kWN > 1 ? (kWN / 2) * kRows * 64 * 4 : 0;
-    static constexpr int kMlBytes = kWN * kRows * 8;
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kQBytes + kMergeBytes + kMlBytes;
+    static constexpr int kPairs = kRowBytes / 32;  // pairs of 16-byte chunks in a row
+    static constexpr int kTilesD = kD / 8;         // accumulator tiles along the dims
+    // Q fragments of one row tile fit the registers beside 64 or fewer accumulators
+    static constexpr bool kQSmem = kMT > 1 || kD == 256;
+    static constexpr int kQBytes = kQSmem ? kRows * kD * 2 : 0;
+    static constexpr int kMergeDims = kKvFp8 && kRows == 16 ? 64 : 32;  // joined at a time
+    static constexpr int kMergeLd = kMergeDims + 8;    // floats; keeps fragment stores apart
+    static constexpr int kMergeBytes = kTokenWarps * kRows * kMergeLd * 4;
+    static constexpr int kMlBytes = (kTokenWarps + 1) * kRows * 8 + kRows * 4;
+    static constexpr int kFixed = 1024 + kQBytes + kMergeBytes + kMlBytes;
+    static constexpr int kFit = (226 * 1024 - kFixed) / kStageBytes;
+    static constexpr int kStages = kFit < 12 ? kFit : 12;
+    static constexpr int kSmem = kFixed + kStages * kStageBytes;
+    // Page n of a CTA's run lands in stage n mod kStages but signals full barrier
+    // n mod kFull, a multiple of kNG: a barrier then belongs to one group, which sees
+    // each of its phases.  (Copies may finish out of order; a group that waited on a
+    // barrier another group's page still has to complete would take the phase before
+    // for its own.)  kFull >= kStages: by the time a barrier is armed again, its page
+    // has been released.
+    static constexpr int kFull = (kStages + kNG - 1) / kNG * kNG;
+    static_assert(kConsumers == 8 && kStages >= 2, "");
 };
+
+// The launch gives every thread 168 registers (launch bounds); the copying
+// warpgroup then hands most of its share to the consumers.
+constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 232;
+static_assert(128 * kProducerRegs + 256 * kConsumerRegs <= 384 * kLaunchRegs, "");
 
 // ---- the list of key tiles ----------------------------------------------------
 
@@ -245,11 +264,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 codes (low 16 bits) as two f16, exact.
-__device__ __forceinline__ uint32_t lift(uint32_t codes) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four E4M3 codes as two pairs of f16, exact.
+__device__ __forceinline__ void lift(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
 }
 
 template <bool kBf16>
@@ -299,14 +319,14 @@ __device__ __forceinline__ void consumer_sync() {
 // ---- the kernel ----------------------------------------------------------------
 
 template <typename C, bool kQBf16>
-__global__ void __launch_bounds__(C::kThreads, C::kCtas)
+__global__ void __launch_bounds__(C::kThreads, 1)
 paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
     // operands of the MMAs: the cache's own type, or f16 lifted from FP8
     constexpr bool kBf16 = kQBf16 && !C::kFp8;
-    constexpr int kD = C::kDim;
+    constexpr int kD = C::kDim, kMT = C::kMT;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];
+    __shared__ uint64_t s_full[C::kFull], s_empty[C::kStages];
     __shared__ int s_valid[C::kStages];
     __shared__ long long s_warp[C::kThreads / 32];
     __shared__ Share s_share;
@@ -315,15 +335,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                ~(uintptr_t)1023);
     uint8_t* tail = ring + C::kStages * C::kStageBytes;
     uint4* s_q = reinterpret_cast<uint4*>(tail);
-    float4* s_merge = reinterpret_cast<float4*>(tail + C::kQBytes);
+    float* s_merge = reinterpret_cast<float*>(tail + C::kQBytes);
     float2* s_ml = reinterpret_cast<float2*>(tail + C::kQBytes + C::kMergeBytes);
+    float2* s_row = s_ml + C::kTokenWarps * C::kRows;  // maximum and sum of a row
+    float* s_factor = reinterpret_cast<float*>(s_row + C::kRows);  // score factor of a row
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], C::kConsumers);
-        }
+        for (int i = 0; i < C::kFull; ++i) mbar_init(&s_full[i], 1);
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&s_empty[i], C::kWM * C::kWN);
         fence_mbar_init();
         s_abort = 0;
         tma_prefetch_desc(&tm_k);
@@ -352,7 +372,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         u.next(p);
     }
 
-    if (warp == C::kConsumers) {
+    if (warp >= C::kConsumers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        if (warp > C::kConsumers) return;
         // copies: the warp holds the next 32 table entries, its first lane issues
         int n = 0;  // tiles issued
         int pieces = 0;
@@ -368,6 +390,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (i == 0 && t != tile) ahead = t + lane < last ? __ldg(row + t + lane) : -1;
                 const int page = __shfl_sync(0xffffffffu, ahead, i);
                 const int st = n % C::kStages;
+                uint64_t* full = &s_full[n % C::kFull];
                 int go = 1;
                 if (lane == 0) {
                     go = n < C::kStages ||
@@ -376,20 +399,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const bool valid = page >= 0 && page < p.bt.num_pages;
                         s_valid[st] = valid;
                         if (valid) {
-                            mbar_arrive_expect_tx(&s_full[st], C::kStageBytes);
+                            mbar_arrive_expect_tx(full, C::kStageBytes);
                             uint8_t* dst = ring + st * C::kStageBytes;
                             const int z = page * p.kv_heads + u.h;
 #pragma unroll
                             for (int x = 0; x < C::kBoxes; ++x)
                                 tma_load_3d(dst + x * (kPage * C::kBoxBytes), &tm_k,
-                                            x * C::kBoxBytes, 0, z, &s_full[st]);
+                                            x * C::kBoxBytes, 0, z, full);
 #pragma unroll
                             for (int x = 0; x < C::kBoxes; ++x)
                                 tma_load_3d(dst + C::kTileBytes + x * (kPage * C::kBoxBytes), &tm_v,
-                                            x * C::kBoxBytes, 0, z, &s_full[st]);
+                                            x * C::kBoxBytes, 0, z, full);
                         } else {
                             record_error(p.status, DSA_ERR_DEVICE_CHECK);
-                            mbar_arrive(&s_full[st]);
+                            mbar_arrive(full);
                         }
                     }
                 }
@@ -413,145 +436,166 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (lane == 0 && *abort_flag) {
             // an unwinding CTA must not exit under copies in flight
             for (int i = max(0, n - C::kStages); i < n; ++i)
-                mbar_drain(&s_full[i % C::kStages], (i / C::kStages) & 1);
+                mbar_drain(&s_full[i % C::kFull], (i / C::kFull) & 1);
             record_error(p.status, DSA_ERR_TIMEOUT);
         }
         return;
     }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
 
-    const int wm = warp % C::kWM, wn = warp / C::kWM;
+    const int grp = warp / (C::kWM * C::kWN);
+    const int wn = warp / C::kWM % C::kWN, wm = warp % C::kWM;
+    const int tw = grp * C::kWN + wn;  // of the warps that share rows
     const int g = lane >> 2, c = lane & 3;
-    const int sw = C::kBoxBytes == 128 ? lane & 7 : (lane >> 1) & 3;
-    // ldmatrix rows and chunks of this lane: keys by token halves and chunk,
-    // values (transposed) by chunk and token halves
-    const int k_row = wn * C::kTokens + ((lane >> 4) << 3) + (lane & 7), k_chunk = (lane >> 3) & 1;
-    const int v_row = wn * C::kTokens + (((lane >> 3) & 1) << 3) + (lane & 7), v_chunk = lane >> 4;
-    const uint32_t ring_u32 = smem_u32(ring);
-    auto chunk_at = [&](int row, int chunk) -> uint32_t {
-        if (C::kBoxBytes == 128)
-            return (uint32_t)((chunk >> 3) * (kPage * 128) + row * 128 + (((chunk & 7) ^ sw) << 4));
-        return (uint32_t)(row * C::kBoxBytes + ((chunk ^ sw) << 4));
+    // ldmatrix addresses of this lane: for keys the matrices are token halves by
+    // chunk of a pair, for values (transposed) chunks by token halves.  The swizzle
+    // XORs a row's low bits into the chunk number, so the pairs of a 128-byte row
+    // have up to four different offsets and the rest is an immediate.
+    constexpr int kPairsBox = C::kBoxBytes / 32;
+    uint32_t k_at[kPairsBox], v_at[kPairsBox];
+    {
+        const int sw = C::kBoxBytes == 128 ? lane & 7 : (lane >> 1) & 3;
+        const int k_row = wn * C::kTokens + ((lane >> 4) << 3) + (lane & 7);
+        const int v_row = wn * C::kTokens + (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+        for (int j = 0; j < kPairsBox; ++j) {
+            k_at[j] = k_row * C::kBoxBytes + (((2 * j + ((lane >> 3) & 1)) ^ sw) << 4);
+            v_at[j] = C::kTileBytes + v_row * C::kBoxBytes + (((2 * j + (lane >> 4)) ^ sw) << 4);
+        }
+    }
+    constexpr auto pair_offset = [](int j, int token) {
+        return (uint32_t)(j / kPairsBox * (kPage * C::kBoxBytes) + token * C::kBoxBytes);
     };
-    int n = 0;  // tiles consumed
+    const uint32_t ring_u32 = smem_u32(ring);
+    int n = 0;  // pages of the CTA's run before the current unit
     bool dead = false;
 
     while (pos < end) {
         const int take = p.whole ? u.cost() : (int)min((long long)(u.cost() - tile), end - pos);
-        const int row0 = u.rt * C::kRows + wm * 16;
-        // this thread's rows: g and g + 8 of the warp's 16
-        const int rows_left = u.r.rows - row0;
-        const bool in0 = g < rows_left, in1 = g + 8 < rows_left;
-        const int j0 = (row0 + g) / p.group, j1 = (row0 + g + 8) / p.group;
-        const int h0 = u.h * p.group + (row0 + g) % p.group;
-        const int h1 = u.h * p.group + (row0 + g + 8) % p.group;
-        const int vis0 = in0 ? u.r.seq - u.r.nb + j0 + 1 : 0;
-        const int vis1 = in1 ? u.r.seq - u.r.nb + j1 + 1 : 0;
-        const int vis_first = u.r.seq - u.r.nb + row0 / p.group + 1;
+        const int tile_row = u.rt * C::kRows;  // first row of the row tile in its request
 
-        // queries as A fragments; for FP8 the columns of a 16-value group are taken
-        // in the order in which the lifted keys come, 4 c .. 4 c + 3
-        float f0 = p.score_scale, f1 = p.score_scale;
-        uint32_t qf[C::kQSmem ? 1 : kD / 16][4];
-        if (!C::kQSmem || wn == 0) {
-            const uint16_t* q0 = static_cast<const uint16_t*>(p.q) +
-                                 (int64_t)(u.r.q0 + j0) * p.q_stride + (int64_t)h0 * kD;
-            const uint16_t* q1 = static_cast<const uint16_t*>(p.q) +
-                                 (int64_t)(u.r.q0 + j1) * p.q_stride + (int64_t)h1 * kD;
-            auto fragment = [&](int ks, uint32_t (&a)[4]) {
-                if (C::kFp8) {
-                    const uint2 x = in0 ? *reinterpret_cast<const uint2*>(q0 + ks * 16 + 4 * c)
-                                        : make_uint2(0, 0);
-                    const uint2 y = in1 ? *reinterpret_cast<const uint2*>(q1 + ks * 16 + 4 * c)
-                                        : make_uint2(0, 0);
-                    a[0] = x.x;
-                    a[1] = y.x;
-                    a[2] = x.y;
-                    a[3] = y.y;
-                } else {
-                    const int at = ks * 16 + 2 * c;
-                    a[0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + at) : 0;
-                    a[1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + at) : 0;
-                    a[2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + at + 8) : 0;
-                    a[3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + at + 8) : 0;
+        // Queries of 16 rows as A fragments, with their score factors.  For FP8 the
+        // columns of a 16-value group are taken in the order in which the lifted
+        // keys come, 4 c .. 4 c + 3.
+        auto load_q = [&](int row0, float (&f)[2], auto&& put) {
+            bool in[2];
+            const uint16_t* q[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = row0 + g + 8 * x;
+                in[x] = r < u.r.rows;
+                q[x] = static_cast<const uint16_t*>(p.q) +
+                       (int64_t)(u.r.q0 + r / p.group) * p.q_stride +
+                       (int64_t)(u.h * p.group + r % p.group) * kD;
+                f[x] = p.score_scale;
+            }
+            uint32_t a[kD / 16][4];  // all loads in flight at once
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (C::kFp8) {
+                        const uint2 v = in[x] ? *reinterpret_cast<const uint2*>(q[x] + ks * 16 + 4 * c)
+                                              : make_uint2(0, 0);
+                        a[ks][x] = v.x;
+                        a[ks][2 + x] = v.y;
+                    } else {
+                        const int at = ks * 16 + 2 * c;
+                        a[ks][x] = in[x] ? *reinterpret_cast<const uint32_t*>(q[x] + at) : 0;
+                        a[ks][2 + x] = in[x] ? *reinterpret_cast<const uint32_t*>(q[x] + at + 8) : 0;
+                    }
                 }
-            };
-            float up0 = 1.f, up1 = 1.f;
             if (C::kFp8 && kQBf16) {
                 // bf16 to f16: scale the row by a power of two that brings its
                 // largest value to 1..2 (what then falls below f16's range is
                 // below 2^-25 of that value), and undo it in the score factor
-                uint32_t top0 = 0, top1 = 0;
-                for (int ks = 0; ks < kD / 16; ++ks) {
-                    uint32_t a[4];
-                    fragment(ks, a);
+                float up[2] = {1.f, 1.f};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t x = max(a[i] & 0x7fffu, (a[i] >> 16) & 0x7fffu);
-                        if (i & 1) top1 = max(top1, x);
-                        else top0 = max(top0, x);
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int ks = 0; ks < kD / 16; ++ks) {
+                        top = max(top, max(a[ks][x] & 0x7fffu, (a[ks][x] >> 16) & 0x7fffu));
+                        top = max(top, max(a[ks][2 + x] & 0x7fffu, (a[ks][2 + x] >> 16) & 0x7fffu));
+                    }
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // biased exponent; zero, infinite and NaN rows stay unscaled
+                    const uint32_t e = top >> 7;
+                    if (e != 0 && e < 254) {
+                        up[x] = __uint_as_float((254 - e) << 23);
+                        f[x] *= __uint_as_float(e << 23);
                     }
                 }
-                top0 = max(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
-                top0 = max(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
-                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-                // biased exponents; zero, infinite and NaN rows stay unscaled
-                const uint32_t e0 = top0 >> 7, e1 = top1 >> 7;
-                if (e0 != 0 && e0 < 254) {
-                    up0 = __uint_as_float((254 - e0) << 23);
-                    f0 *= __uint_as_float(e0 << 23);
-                }
-                if (e1 != 0 && e1 < 254) {
-                    up1 = __uint_as_float((254 - e1) << 23);
-                    f1 *= __uint_as_float(e1 << 23);
-                }
+#pragma unroll
+                for (int ks = 0; ks < kD / 16; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        a[ks][i] = pack2<false>(__uint_as_float(a[ks][i] << 16) * up[i & 1],
+                                                __uint_as_float(a[ks][i] & 0xffff0000u) * up[i & 1]);
             }
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
-                uint32_t a[4];
-                fragment(ks, a);
-                if (C::kFp8 && kQBf16) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float up = (i & 1) ? up1 : up0;
-                        a[i] = pack2<false>(__uint_as_float(a[i] << 16) * up,
-                                            __uint_as_float(a[i] & 0xffff0000u) * up);
-                    }
-                }
-                if (C::kQSmem) {
-                    s_q[(wm * (kD / 16) + ks) * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) qf[C::kQSmem ? 0 : ks][i] = a[i];
-                }
-            }
-            if (C::kQSmem && C::kFp8 && c == 0) {
-                s_ml[wm * 16 + g] = make_float2(f0, 0.f);
-                s_ml[wm * 16 + g + 8] = make_float2(f1, 0.f);
-            }
-        }
+            for (int ks = 0; ks < kD / 16; ++ks) put(ks, a[ks]);
+        };
+        float f[kMT][2];
+        uint32_t qf[C::kQSmem ? 1 : kD / 16][4];
         if (C::kQSmem) {
-            consumer_sync<32 * C::kConsumers>();
-            if (C::kFp8) {
-                f0 = s_ml[wm * 16 + g].x;
-                f1 = s_ml[wm * 16 + g + 8].x;
-                consumer_sync<32 * C::kConsumers>();
+            for (int mi = warp; mi < C::kWM * kMT; mi += C::kConsumers) {
+                float own[2];
+                load_q(tile_row + 16 * mi, own, [&](int ks, const uint32_t (&a)[4]) {
+                    s_q[(mi * (kD / 16) + ks) * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
+                });
+                if (c == 0) {
+                    s_factor[16 * mi + g] = own[0];
+                    s_factor[16 * mi + g + 8] = own[1];
+                }
             }
+            consumer_sync<32 * C::kConsumers>();
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+                f[mt][0] = s_factor[16 * (wm * kMT + mt) + g];
+                f[mt][1] = s_factor[16 * (wm * kMT + mt) + g + 8];
+            }
+        } else {
+            load_q(tile_row + 16 * wm, f[0], [&](int ks, const uint32_t (&a)[4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qf[C::kQSmem ? 0 : ks][i] = a[i];
+            });
         }
 
-        float o[C::kTilesD][4];
+        // this thread's rows: g and g + 8 of each 16; what they see
+        int vis[kMT][2];
 #pragma unroll
-        for (int i = 0; i < C::kTilesD; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = tile_row + 16 * (wm * kMT + mt) + g + 8 * x;
+                vis[mt][x] = r < u.r.rows ? u.r.seq - u.r.nb + r / p.group + 1 : 0;
+            }
+        const int vis_first =
+            u.r.seq - u.r.nb + (tile_row + 16 * wm * kMT) / p.group + 1;
+
+        float o[kMT][C::kTilesD][4];
+        float m[kMT][2], l[kMT][2];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+            for (int i = 0; i < C::kTilesD; ++i)
+                o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
+            m[mt][0] = m[mt][1] = -INFINITY;
+            l[mt][0] = l[mt][1] = 0.f;
+        }
 
         const int last = min(u.tiles, tile + take);
-        for (int t = tile; t < last; ++t, ++n) {
-            const int st = n % C::kStages;
-            if (!dead) dead = !mbar_wait(&s_full[st], (n / C::kStages) & 1, abort_flag);
+        // this group's pages: those whose number in the run is grp modulo kNG
+        for (int t = tile + (grp + C::kNG - n % C::kNG) % C::kNG; t < last; t += C::kNG) {
+            const int i_run = n + (t - tile), st = i_run % C::kStages;
+            if (!dead)
+                dead = !mbar_wait(&s_full[i_run % C::kFull], (i_run / C::kFull) & 1, abort_flag);
             dead = __any_sync(0xffffffffu, dead);
-            if (dead) continue;
+            if (dead) break;
             if (s_valid[st]) {
-                const uint32_t ks = ring_u32 + st * C::kStageBytes, vs = ks + C::kTileBytes;
+                const uint32_t stage = ring_u32 + st * C::kStageBytes;
                 const int first = t * kPage + wn * C::kTokens;  // this warp's first position
                 if (first + C::kTokens > u.r.seq) {
                     // stale rows past the context may hold anything: p is 0 there, but
@@ -571,116 +615,147 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                 for (int sub = 0; sub < C::kTokens; sub += C::kSub) {
                     constexpr int kNt = C::kSub / 8;
-                    float s[kNt][4];
+                    float s[kMT][kNt][4];
 #pragma unroll
-                    for (int i = 0; i < kNt; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+                    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < kNt; ++i)
+                            s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
+                    constexpr int kSteps = C::kFp8 ? 2 : 1;  // MMA steps in a chunk pair
 #pragma unroll
                     for (int j = 0; j < C::kPairs; ++j) {
-                        uint32_t qa[4], qb[4];
-                        if (C::kFp8) {  // 32 values: two MMA steps
-                            if (C::kQSmem) {
-                                const uint4 x = s_q[(wm * (kD / 16) + 2 * j) * 32 + lane];
-                                const uint4 y = s_q[(wm * (kD / 16) + 2 * j + 1) * 32 + lane];
-                                qa[0] = x.x, qa[1] = x.y, qa[2] = x.z, qa[3] = x.w;
-                                qb[0] = y.x, qb[1] = y.y, qb[2] = y.z, qb[3] = y.w;
-                            } else {
+                        uint32_t qa[kMT][kSteps][4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    qa[i] = qf[C::kQSmem ? 0 : 2 * j][i];
-                                    qb[i] = qf[C::kQSmem ? 0 : 2 * j + 1][i];
+                        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                            for (int x = 0; x < kSteps; ++x) {
+                                if (C::kQSmem) {
+                                    const uint4 w =
+                                        s_q[((wm * kMT + mt) * (kD / 16) + kSteps * j + x) * 32 + lane];
+                                    qa[mt][x][0] = w.x;
+                                    qa[mt][x][1] = w.y;
+                                    qa[mt][x][2] = w.z;
+                                    qa[mt][x][3] = w.w;
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        qa[mt][x][i] = qf[C::kQSmem ? 0 : kSteps * j + x][i];
                                 }
                             }
-                        } else if (C::kQSmem) {
-                            const uint4 x = s_q[(wm * (kD / 16) + j) * 32 + lane];
-                            qa[0] = x.x, qa[1] = x.y, qa[2] = x.z, qa[3] = x.w;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) qa[i] = qf[C::kQSmem ? 0 : j][i];
-                        }
 #pragma unroll
                         for (int i = 0; i < C::kSub / 16; ++i) {
                             uint32_t k[4];
-                            ldmatrix4(k, ks + chunk_at(k_row + sub + 16 * i, 2 * j + k_chunk));
+                            ldmatrix4(k, stage + k_at[j % kPairsBox] + pair_offset(j, sub + 16 * i));
                             if (C::kFp8) {
-                                mma16816<false>(s[2 * i], qa, lift(k[0]), lift(k[0] >> 16));
-                                mma16816<false>(s[2 * i + 1], qa, lift(k[2]), lift(k[2] >> 16));
-                                mma16816<false>(s[2 * i], qb, lift(k[1]), lift(k[1] >> 16));
-                                mma16816<false>(s[2 * i + 1], qb, lift(k[3]), lift(k[3] >> 16));
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    uint32_t k0, k1, k2, k3;
+                                    lift(k[x], k0, k1);
+                                    lift(k[2 + x], k2, k3);
+#pragma unroll
+                                    for (int mt = 0; mt < kMT; ++mt) {
+                                        mma16816<false>(s[mt][2 * i], qa[mt][x % kSteps], k0, k1);
+                                        mma16816<false>(s[mt][2 * i + 1], qa[mt][x % kSteps], k2, k3);
+                                    }
+                                }
                             } else {
-                                mma16816<kBf16>(s[2 * i], qa, k[0], k[1]);
-                                mma16816<kBf16>(s[2 * i + 1], qa, k[2], k[3]);
+#pragma unroll
+                                for (int mt = 0; mt < kMT; ++mt) {
+                                    mma16816<kBf16>(s[mt][2 * i], qa[mt][0], k[0], k[1]);
+                                    mma16816<kBf16>(s[mt][2 * i + 1], qa[mt][0], k[2], k[3]);
+                                }
                             }
                         }
                     }
                     if (t * kPage + kPage > vis_first) {
 #pragma unroll
-                        for (int i = 0; i < kNt; ++i) {
-                            const int at = first + sub + 8 * i + 2 * c;
-                            if (at >= vis0) s[i][0] = -INFINITY;
-                            if (at + 1 >= vis0) s[i][1] = -INFINITY;
-                            if (at >= vis1) s[i][2] = -INFINITY;
-                            if (at + 1 >= vis1) s[i][3] = -INFINITY;
+                        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                            for (int i = 0; i < kNt; ++i)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    if (first + sub + 8 * i + 2 * c + (x & 1) >= vis[mt][x >> 1])
+                                        s[mt][i][x] = -INFINITY;
+                    }
+                    float top[kMT][2];
+                    bool grew = false;
+#pragma unroll
+                    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float y = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < kNt; ++i)
+                                y = fmaxf(y, fmaxf(s[mt][i][2 * x], s[mt][i][2 * x + 1]));
+                            top[mt][x] = fmaxf(m[mt][x], quad_max(y) * f[mt][x]);
+                            grew |= top[mt][x] > m[mt][x];
+                        }
+                    if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                        for (int mt = 0; mt < kMT; ++mt) {
+                            const float a0 = ex2(m[mt][0] - base_of(top[mt][0]));
+                            const float a1 = ex2(m[mt][1] - base_of(top[mt][1]));
+                            l[mt][0] *= a0;
+                            l[mt][1] *= a1;
+#pragma unroll
+                            for (int i = 0; i < C::kTilesD; ++i) {
+                                o[mt][i][0] *= a0;
+                                o[mt][i][1] *= a0;
+                                o[mt][i][2] *= a1;
+                                o[mt][i][3] *= a1;
+                            }
+                            m[mt][0] = top[mt][0];
+                            m[mt][1] = top[mt][1];
                         }
                     }
-                    float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < kNt; ++i) {
-                        x0 = fmaxf(x0, fmaxf(s[i][0], s[i][1]));
-                        x1 = fmaxf(x1, fmaxf(s[i][2], s[i][3]));
-                    }
-                    x0 = fmaxf(m0, quad_max(x0) * f0);
-                    x1 = fmaxf(m1, quad_max(x1) * f1);
-                    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-                        const float a0 = ex2(m0 - base_of(x0)), a1 = ex2(m1 - base_of(x1));
-                        l0 *= a0;
-                        l1 *= a1;
-#pragma unroll
-                        for (int i = 0; i < C::kTilesD; ++i) {
-                            o[i][0] *= a0;
-                            o[i][1] *= a0;
-                            o[i][2] *= a1;
-                            o[i][3] *= a1;
-                        }
-                        m0 = x0;
-                        m1 = x1;
-                    }
-                    const float b0 = base_of(m0), b1 = base_of(m1);
-#pragma unroll
-                    for (int i = 0; i < kNt; ++i) {
-                        s[i][0] = ex2(fmaf(s[i][0], f0, -b0));
-                        s[i][1] = ex2(fmaf(s[i][1], f0, -b0));
-                        s[i][2] = ex2(fmaf(s[i][2], f1, -b1));
-                        s[i][3] = ex2(fmaf(s[i][3], f1, -b1));
-                        l0 += s[i][0] + s[i][1];
-                        l1 += s[i][2] + s[i][3];
-                    }
-                    // P rounded to the operand type (the sums above are of the unrounded
+                    // P rounded to the operand type (the sums are of the unrounded
                     // values): half a step per probability, which averages out as the
                     // output's own rounding does
+                    uint32_t pf[kMT][C::kSub / 16][4];
+#pragma unroll
+                    for (int mt = 0; mt < kMT; ++mt) {
+                        const float b0 = base_of(m[mt][0]), b1 = base_of(m[mt][1]);
+#pragma unroll
+                        for (int i = 0; i < kNt; ++i) {
+                            const float p0 = ex2(fmaf(s[mt][i][0], f[mt][0], -b0));
+                            const float p1 = ex2(fmaf(s[mt][i][1], f[mt][0], -b0));
+                            const float p2 = ex2(fmaf(s[mt][i][2], f[mt][1], -b1));
+                            const float p3 = ex2(fmaf(s[mt][i][3], f[mt][1], -b1));
+                            l[mt][0] += p0 + p1;
+                            l[mt][1] += p2 + p3;
+                            pf[mt][i / 2][2 * (i & 1)] = pack2<kBf16>(p0, p1);
+                            pf[mt][i / 2][2 * (i & 1) + 1] = pack2<kBf16>(p2, p3);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < C::kSub / 16; ++i) {
-                        const uint32_t pf[4] = {pack2<kBf16>(s[2 * i][0], s[2 * i][1]),
-                                                pack2<kBf16>(s[2 * i][2], s[2 * i][3]),
-                                                pack2<kBf16>(s[2 * i + 1][0], s[2 * i + 1][1]),
-                                                pack2<kBf16>(s[2 * i + 1][2], s[2 * i + 1][3])};
 #pragma unroll
                         for (int j = 0; j < C::kPairs; ++j) {
                             uint32_t v[4];
-                            ldmatrix4_t(v, vs + chunk_at(v_row + sub + 16 * i, 2 * j + v_chunk));
+                            ldmatrix4_t(v, stage + v_at[j % kPairsBox] + pair_offset(j, sub + 16 * i));
                             if (C::kFp8) {
                                 // each register: two tokens by two dims; split by dim
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
-                                    const uint32_t lo = __byte_perm(v[2 * x], 0, 0x3120);
-                                    const uint32_t hi = __byte_perm(v[2 * x + 1], 0, 0x3120);
-                                    mma16816<false>(o[C::kFp8 ? 4 * j + 2 * x : 0], pf, lift(lo),
-                                                    lift(hi));
-                                    mma16816<false>(o[C::kFp8 ? 4 * j + 2 * x + 1 : 0], pf,
-                                                    lift(lo >> 16), lift(hi >> 16));
+                                    uint32_t v0, v1, v2, v3;
+                                    lift(__byte_perm(v[2 * x], 0, 0x3120), v0, v2);
+                                    lift(__byte_perm(v[2 * x + 1], 0, 0x3120), v1, v3);
+                                    constexpr int kStep = C::kFp8 ? 4 : 2;
+#pragma unroll
+                                    for (int mt = 0; mt < kMT; ++mt) {
+                                        mma16816<false>(o[mt][kStep * j + (C::kFp8 ? 2 * x : 0)],
+                                                        pf[mt][i], v0, v1);
+                                        mma16816<false>(o[mt][kStep * j + (C::kFp8 ? 2 * x : 0) + 1],
+                                                        pf[mt][i], v2, v3);
+                                    }
                                 }
                             } else {
-                                mma16816<kBf16>(o[C::kFp8 ? 0 : 2 * j], pf, v[0], v[1]);
-                                mma16816<kBf16>(o[C::kFp8 ? 0 : 2 * j + 1], pf, v[2], v[3]);
+                                constexpr int kStep = C::kFp8 ? 0 : 2;
+#pragma unroll
+                                for (int mt = 0; mt < kMT; ++mt) {
+                                    mma16816<kBf16>(o[mt][kStep * j], pf[mt][i], v[0], v[1]);
+                                    mma16816<kBf16>(o[mt][kStep * j + 1], pf[mt][i], v[2], v[3]);
+                                }
                             }
                         }
                     }
@@ -689,131 +764,103 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[st]);
         }
+        n += max(0, last - tile);
 
-        // join the warps that share rows
-        l0 = quad_sum(l0);
-        l1 = quad_sum(l1);
-        if (C::kWN > 1) {
+        // join the warps that share rows: bring all to the common maximum, then add
+        // 32 dims at a time through shared memory, every thread four values
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+            const int r = 16 * (wm * kMT + mt) + g;
+            l[mt][0] = quad_sum(l[mt][0]);
+            l[mt][1] = quad_sum(l[mt][1]);
             if (c == 0) {
-                s_ml[wn * C::kRows + wm * 16 + g] = make_float2(m0, l0);
-                s_ml[wn * C::kRows + wm * 16 + g + 8] = make_float2(m1, l1);
-            }
-            consumer_sync<32 * C::kConsumers>();
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < C::kWN; ++w) {
-                t0 = fmaxf(t0, s_ml[w * C::kRows + wm * 16 + g].x);
-                t1 = fmaxf(t1, s_ml[w * C::kRows + wm * 16 + g + 8].x);
-            }
-            const float b0 = base_of(t0), b1 = base_of(t1);
-            l0 = l1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < C::kWN; ++w) {
-                const float2 x = s_ml[w * C::kRows + wm * 16 + g];
-                const float2 y = s_ml[w * C::kRows + wm * 16 + g + 8];
-                l0 += x.y * ex2(x.x - b0);
-                l1 += y.y * ex2(y.x - b1);
-            }
-            const float a0 = ex2(m0 - b0), a1 = ex2(m1 - b1);
-            m0 = t0;
-            m1 = t1;
-#pragma unroll
-            for (int i = 0; i < C::kTilesD; ++i) {
-                o[i][0] *= a0;
-                o[i][1] *= a0;
-                o[i][2] *= a1;
-                o[i][3] *= a1;
-            }
-            // halve the warps, 64 dims at a time through the merge buffer
-#pragma unroll
-            for (int half = C::kWN / 2; half >= 1; half /= 2) {
-#pragma unroll
-                for (int d0 = 0; d0 < C::kTilesD; d0 += 8) {
-                    if (wn >= half && wn < 2 * half) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            s_merge[(((wn - half) * C::kWM + wm) * 8 + i) * 32 + lane] =
-                                make_float4(o[d0 + i][0], o[d0 + i][1], o[d0 + i][2], o[d0 + i][3]);
-                    }
-                    consumer_sync<32 * C::kConsumers>();
-                    if (wn < half) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 x = s_merge[((wn * C::kWM + wm) * 8 + i) * 32 + lane];
-                            o[d0 + i][0] += x.x;
-                            o[d0 + i][1] += x.y;
-                            o[d0 + i][2] += x.z;
-                            o[d0 + i][3] += x.w;
-                        }
-                    }
-                    consumer_sync<32 * C::kConsumers>();
-                }
+                s_ml[tw * C::kRows + r] = make_float2(m[mt][0], l[mt][0]);
+                s_ml[tw * C::kRows + r + 8] = make_float2(m[mt][1], l[mt][1]);
             }
         }
-        if (wn == 0) {
-            const bool complete = tile == 0 && take == u.cost();
-            const int64_t r0 = (int64_t)(u.r.q0 + j0) * (p.kv_heads * p.group) + h0;
-            const int64_t r1 = (int64_t)(u.r.q0 + j1) * (p.kv_heads * p.group) + h1;
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0);
-            const int64_t s0 = slot * C::kRows + wm * 16 + g, s1 = s0 + 8;
-            if (complete) {
-                const float i0 = l0 == 0.f ? 0.f : p.v_scale / l0;
-                const float i1 = l1 == 0.f ? 0.f : p.v_scale / l1;
+        consumer_sync<32 * C::kConsumers>();
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = 16 * (wm * kMT + mt) + g + 8 * x;
+                float y = -INFINITY, total = 0.f;
+#pragma unroll
+                for (int w = 0; w < C::kTokenWarps; ++w) y = fmaxf(y, s_ml[w * C::kRows + r].x);
+                if (tw == 0) {
+#pragma unroll
+                    for (int w = 0; w < C::kTokenWarps; ++w) {
+                        const float2 ml = s_ml[w * C::kRows + r];
+                        total += ml.y * ex2(ml.x - base_of(y));
+                    }
+                    if (c == 0) s_row[r] = make_float2(y, total);
+                }
+                const float a = ex2(m[mt][x] - base_of(y));
 #pragma unroll
                 for (int i = 0; i < C::kTilesD; ++i) {
-                    o[i][0] *= i0;
-                    o[i][1] *= i0;
-                    o[i][2] *= i1;
-                    o[i][3] *= i1;
-                }
-                if (p.lse && c == 0) {
-                    if (in0) p.lse[r0] = l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * kLn2;
-                    if (in1) p.lse[r1] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * kLn2;
-                }
-            } else if (c == 0) {
-                *reinterpret_cast<float2*>(p.part_ml + 2 * s0) = make_float2(m0, l0);
-                *reinterpret_cast<float2*>(p.part_ml + 2 * s1) = make_float2(m1, l1);
-            }
-            uint16_t* out = static_cast<uint16_t*>(p.out);
-            if (C::kFp8) {
-#pragma unroll
-                for (int i = 0; i < C::kTilesD / 2; ++i) {
-                    const int d = 16 * i + 4 * c;
-                    const float(&e)[4] = o[2 * i];
-                    const float(&f)[4] = o[2 * i + 1];
-                    if (complete) {
-                        if (in0)
-                            *reinterpret_cast<uint2*>(out + r0 * kD + d) =
-                                make_uint2(pack2<kQBf16>(e[0], f[0]), pack2<kQBf16>(e[1], f[1]));
-                        if (in1)
-                            *reinterpret_cast<uint2*>(out + r1 * kD + d) =
-                                make_uint2(pack2<kQBf16>(e[2], f[2]), pack2<kQBf16>(e[3], f[3]));
-                    } else {
-                        *reinterpret_cast<float4*>(p.part_o + s0 * kD + d) =
-                            make_float4(e[0], f[0], e[1], f[1]);
-                        *reinterpret_cast<float4*>(p.part_o + s1 * kD + d) =
-                            make_float4(e[2], f[2], e[3], f[3]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < C::kTilesD; ++i) {
-                    const int d = 8 * i + 2 * c;
-                    if (complete) {
-                        if (in0)
-                            *reinterpret_cast<uint32_t*>(out + r0 * kD + d) =
-                                pack2<kQBf16>(o[i][0], o[i][1]);
-                        if (in1)
-                            *reinterpret_cast<uint32_t*>(out + r1 * kD + d) =
-                                pack2<kQBf16>(o[i][2], o[i][3]);
-                    } else {
-                        *reinterpret_cast<float2*>(p.part_o + s0 * kD + d) =
-                            make_float2(o[i][0], o[i][1]);
-                        *reinterpret_cast<float2*>(p.part_o + s1 * kD + d) =
-                            make_float2(o[i][2], o[i][3]);
-                    }
+                    o[mt][i][2 * x] *= a;
+                    o[mt][i][2 * x + 1] *= a;
                 }
             }
+        const bool complete = tile == 0 && take == u.cost();
+        const int rows = min(C::kRows, u.r.rows - tile_row);
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0)) * C::kRows;
+#pragma unroll
+        for (int d0 = 0; d0 < kD; d0 += C::kMergeDims) {
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float* dst = s_merge + (tw * C::kRows + 16 * (wm * kMT + mt) + g + 8 * x) *
+                                               C::kMergeLd;
+                    constexpr int kPer = C::kMergeDims / 8;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const float(&e)[4] = o[mt][d0 / 8 + i];
+                        if (C::kFp8) {  // tiles of even and odd dims in turn
+                            if (i % 2 == 0) {
+                                const float(&q)[4] = o[mt][d0 / 8 + (C::kFp8 ? i + 1 : 0)];
+                                *reinterpret_cast<float4*>(dst + 8 * i + 4 * c) = make_float4(
+                                    e[2 * x], q[2 * x], e[2 * x + 1], q[2 * x + 1]);
+                            }
+                        } else {
+                            *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) =
+                                make_float2(e[2 * x], e[2 * x + 1]);
+                        }
+                    }
+                }
+            consumer_sync<32 * C::kConsumers>();
+            for (int i = tid; i < rows * (C::kMergeDims / 4); i += 32 * C::kConsumers) {
+                const int r = i / (C::kMergeDims / 4), d = i % (C::kMergeDims / 4) * 4;
+                const float top = s_row[r].x, total = s_row[r].y;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < C::kTokenWarps; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        s_merge + (w * C::kRows + r) * C::kMergeLd + d);
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                }
+                if (complete) {
+                    const int row = tile_row + r;
+                    const int64_t at = (int64_t)(u.r.q0 + row / p.group) * (p.kv_heads * p.group) +
+                                       u.h * p.group + row % p.group;
+                    const float inv = total == 0.f ? 0.f : p.v_scale / total;
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * kD + d0 + d) =
+                        make_uint2(pack2<kQBf16>(sum.x * inv, sum.y * inv),
+                                   pack2<kQBf16>(sum.z * inv, sum.w * inv));
+                    if (p.lse && d0 + d == 0)
+                        p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + (slot + r) * kD + d0 + d) = sum;
+                    if (d0 + d == 0)
+                        *reinterpret_cast<float2*>(p.part_ml + 2 * (slot + r)) =
+                            make_float2(top, total);
+                }
+            }
+            consumer_sync<32 * C::kConsumers>();
         }
         pos += take;
         tile = 0;
@@ -900,7 +947,7 @@ bool encode_pool(CUtensorMap* tm, const void* base, const dsa_kv_cache& c, int r
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMaxCtas = 2 * 152;  // pieces are kept for this many CTAs
+constexpr int kMaxCtas = 160;  // pieces are kept for this many CTAs
 constexpr int kMinTiles = 2;
 
 // Rows of a tile for requests of up to max_rows rows: the smallest that holds
@@ -931,6 +978,14 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
     cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<C, kQBf16>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    // the consumers would wait forever for registers that the launch did not bring
+    static const int regs = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, paged_attention_kernel<C, kQBf16>) == cudaSuccess
+                   ? a.numRegs
+                   : 0;
+    }();
+    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
@@ -939,7 +994,7 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
     const int64_t tiles = ((int64_t)p.bt.max_seq + kPage - 1) / kPage;
     const int64_t row_tiles = ((int64_t)p.bt.max_q * p.group + C::kRows - 1) / C::kRows;
     const double most = (double)p.bt.num_requests * row_tiles * p.kv_heads * tiles;
-    int ctas = sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas;
+    int ctas = sms < kMaxCtas ? sms : kMaxCtas;
     if (most < (double)ctas * p.min_tiles)
         ctas = (int)((most + p.min_tiles - 1) / p.min_tiles);
     if (ctas < 1) ctas = 1;
@@ -956,18 +1011,18 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
 template <int kD, bool kFp8, bool kQBf16>
 cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* launches,
                         cudaStream_t stream) {
-    // D = 256: 128 accumulator registers a thread leave room for four consumer
-    // warps, not eight
+    // D = 256 has 128 accumulators a thread for 16 rows; the others take 32 rows a
+    // warp, which halves the fragment loads per MMA
     constexpr bool kWide = kD == 256;
     switch (row_tile((int64_t)p.bt.max_q * p.group, p.whole != 0)) {
         case 16:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, 4>, kQBf16>(p, cache, launches, stream);
+            return launch_cfg<AttnCfg<kD, kFp8, 1, 1, 2, 4>, kQBf16>(p, cache, launches, stream);
         case 32:
-            return launch_cfg<AttnCfg<kD, kFp8, 2, kWide ? 2 : 4>, kQBf16>(p, cache, launches,
-                                                                           stream);
+            return launch_cfg<AttnCfg<kD, kFp8, kWide ? 1 : 2, kWide ? 2 : 1, 2, kWide ? 2 : 4>,
+                              kQBf16>(p, cache, launches, stream);
         default:
-            return launch_cfg<AttnCfg<kD, kFp8, 4, kWide ? 1 : 2>, kQBf16>(p, cache, launches,
-                                                                           stream);
+            return launch_cfg<AttnCfg<kD, kFp8, kWide ? 1 : 2, kWide ? 4 : 2, 2, kWide ? 1 : 2>,
+                              kQBf16>(p, cache, launches, stream);
     }
 }
 

@@ -223,6 +223,25 @@ def test_results_do_not_change_from_run_to_run():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("hq,hkv,d,new,kv", [(32, 8, 128, 1, BF16), (16, 4, 128, 6, FP8),
+                                             (8, 8, 64, 1, BF16), (8, 4, 256, 1, BF16)])
+def test_calls_in_a_row_over_a_long_cache(hq, hkv, d, new, kv):
+    """Copies from HBM that finish out of order, passes that follow one another
+    without a wait, the workspace shared."""
+    c = Case([150000, 99000], [new] * 2, hq, hkv, d, BF16, kv, seed=18)
+    want, want_lse = c.run()
+    batch, cache = c.batch(), c.cache()
+    ws = torch.empty(dsa.dsa_paged_attention_workspace_size(batch, cache, hq), dtype=torch.uint8,
+                     device=DEV)
+    outs = [(torch.zeros_like(want), torch.zeros_like(want_lse)) for _ in range(12)]
+    for out, lse in outs:
+        dsa.dsa_paged_attention(batch, cache, c.q, c.sm_scale, out, lse, ws)
+    torch.cuda.synchronize()
+    for out, lse in outs:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    c.check(want, want_lse)
+
+
 def test_batch_invariant_switch():
     """Under the switch a request's results do not depend on its batch."""
     lens, new = [5000, 77, 1300], [1, 2, 5]
