@@ -45,6 +45,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct AttnParams {
     BatchArgs bt;
     int32_t kv_heads, group;
+    float inv_group;
     int32_t min_tiles;  // least tiles of a CTA
     int32_t whole;      // every (request, row tile, KV head) by one CTA
     int64_t q_stride;
@@ -62,9 +63,11 @@ struct AttnParams {
 // What a joining block needs to know of the row tile whose first piece a CTA wrote.
 enum { kJoinPieces, kJoinToken, kJoinRow, kJoinRows, kJoinHead, kJoinInts = 8 };
 
-// Eight consumer warps: kNG groups, each taking every kNG-th page of the CTA's run;
+// The consumer warps: kNG groups, each taking every kNG-th page of the CTA's run;
 // within a group kWM warps along the rows (kMT tiles of 16 rows each) by kWN warps
-// along the page's tokens.
+// along the page's tokens.  8, 12 or 16 warps, as many as the accumulators' registers
+// allow: a warp's softmax is a chain of dependent instructions, and only other
+// warps fill its gaps.
 template <int kD, bool kKvFp8, int kMT_, int kWM_, int kWN_, int kNG_>
 struct AttnCfg {
     static constexpr int kDim = kD;
@@ -80,16 +83,20 @@ struct AttnCfg {
     static constexpr int kTileBytes = kPage * kRowBytes;  // keys or values of one page
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kTokens = kPage / kWN;                       // of a page, per warp
-    static constexpr int kSub = kD == 256 || kTokens < 32 ? 16 : 32;  // softmax step
+    static constexpr int kSub =
+        kD == 256 || kTokens < 32 || (kD == 128 && kConsumers > 8) ? 16 : 32;  // softmax step
     static constexpr int kPairs = kRowBytes / 32;  // pairs of 16-byte chunks in a row
     static constexpr int kTilesD = kD / 8;         // accumulator tiles along the dims
     // Q fragments of one row tile fit the registers beside 64 or fewer accumulators
-    static constexpr bool kQSmem = kMT > 1 || kD == 256;
-    static constexpr int kQBytes = kQSmem ? kRows * kD * 2 : 0;
-    static constexpr int kMergeDims = kKvFp8 && kRows == 16 ? 64 : 32;  // joined at a time
+    static constexpr bool kQSmem = kMT > 1 || kD == 256 || (kD == 128 && kConsumers == 16);
+    static constexpr int kQBytes = kRows * kD * 2;
+    static constexpr int kMergeDims = 32;            // joined at a time
+    // two buffers save a barrier a pass, where they take less than a stage or two
+    static constexpr int kMergeBuffers =
+        kTokenWarps * kRows > 128 || (kD == 256 && !kKvFp8) ? 1 : 2;
     static constexpr int kMergeLd = kMergeDims + 8;    // floats; keeps fragment stores apart
-    static constexpr int kMergeBytes = kTokenWarps * kRows * kMergeLd * 4;
-    static constexpr int kMlBytes = (kTokenWarps + 1) * kRows * 8 + kRows * 4;
+    static constexpr int kMergeBytes = kMergeBuffers * kTokenWarps * kRows * kMergeLd * 4;
+    static constexpr int kMlBytes = kTokenWarps * kRows * 8 + kRows * 4;
     static constexpr int kFixed = 1024 + kQBytes + kMergeBytes + kMlBytes;
     static constexpr int kFit = (226 * 1024 - kFixed) / kStageBytes;
     static constexpr int kStages = kFit < 12 ? kFit : 12;
@@ -101,15 +108,34 @@ struct AttnCfg {
     // for its own.)  kFull >= kStages: by the time a barrier is armed again, its page
     // has been released.
     static constexpr int kFull = (kStages + kNG - 1) / kNG * kNG;
-    static_assert(kConsumers == 8 && kStages >= 2, "");
+    // The launch gives every thread kLaunchRegs registers (launch bounds); the copying
+    // warpgroup then hands most of its share to the consumers.
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kProducerRegs = kConsumers == 12 ? 56 : 40;
+    static constexpr int kConsumerRegs = kConsumers == 8 ? 232 : kConsumers == 12 ? 152 : 104;
+    static_assert(128 * kProducerRegs + 32 * kConsumers * kConsumerRegs <= kThreads * kLaunchRegs,
+                  "setmaxnreg.inc would wait forever");
+    static_assert(kConsumers == 8 || kConsumers == 12 || kConsumers == 16, "");
+    static_assert(kStages >= 2, "");
 };
 
-// The launch gives every thread 168 registers (launch bounds); the copying
-// warpgroup then hands most of its share to the consumers.
-constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 232;
-static_assert(128 * kProducerRegs + 256 * kConsumerRegs <= 384 * kLaunchRegs, "");
-
 // ---- the list of key tiles ----------------------------------------------------
+
+// Row number / group: the token of a row within its request.
+__device__ __forceinline__ int token_of(const AttnParams& p, int row) {
+    if (row >= 1 << 24) return row / p.group;
+    int t = (int)((float)row * p.inv_group);  // off by one at most
+    const int rest = row - t * p.group;
+    t += rest >= p.group;
+    t -= rest < 0;
+    return t;
+}
+
+// 64-bit division, in 32 bits where both fit.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
 
 // One request as the schedule sees it; rows = 0 when it brings no tokens or its
 // metadata contradict the host sizes.  Unlike the other kernels' check this
@@ -118,17 +144,21 @@ struct Request {
     int q0, nb, seq, rows;
 };
 
-__device__ __forceinline__ Request request_at(const AttnParams& p, int b, int32_t* status) {
-    Request r;
-    r.q0 = __ldg(p.bt.q_offsets + b);
-    const int q1 = __ldg(p.bt.q_offsets + b + 1);
-    r.seq = __ldg(p.bt.seq_lens + b);
-    const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= p.bt.total_q && q1 - r.q0 <= p.bt.max_q &&
-                    r.seq >= 0 && r.seq <= p.bt.max_seq;
+struct RawRequest {
+    int q0, q1, seq;
+};
+
+__device__ __forceinline__ RawRequest raw_request(const AttnParams& p, int b) {
+    return {__ldg(p.bt.q_offsets + b), __ldg(p.bt.q_offsets + b + 1), __ldg(p.bt.seq_lens + b)};
+}
+
+__device__ __forceinline__ Request request_of(const AttnParams& p, const RawRequest& x,
+                                              int32_t* status) {
+    const bool ok = x.q0 >= 0 && x.q1 >= x.q0 && x.q1 <= p.bt.total_q &&
+                    x.q1 - x.q0 <= p.bt.max_q && x.seq >= 0 && x.seq <= p.bt.max_seq;
     if (!ok) record_error(status, DSA_ERR_DEVICE_CHECK);
-    r.nb = ok ? q1 - r.q0 : 0;
-    r.rows = r.nb * p.group;
-    return r;
+    const int nb = ok ? x.q1 - x.q0 : 0;
+    return {x.q0, nb, x.seq, nb * p.group};
 }
 
 // Key tiles that row tile rt of a request needs: pages up to the last position
@@ -136,46 +166,52 @@ __device__ __forceinline__ Request request_at(const AttnParams& p, int b, int32_
 template <int kRows>
 __device__ __forceinline__ int tiles_of(const AttnParams& p, const Request& r, int rt) {
     const int last = min(r.rows, (rt + 1) * kRows) - 1;
-    const int vis = r.seq - r.nb + last / p.group + 1;
+    const int vis = last == r.rows - 1 ? r.seq : r.seq - r.nb + token_of(p, last) + 1;
     return vis > 0 ? (vis + kPage - 1) / kPage : 0;
 }
 
 // A place in the list.  Units run over requests, row tiles, KV heads; a unit
-// without key tiles counts as one, so that somebody writes its empty rows.
+// without key tiles counts as one, so that somebody writes its empty rows.  The
+// next request's metadata are loaded one request ahead.
 template <int kRows>
 struct Cursor {
     int b, rt, h, tiles;
     Request r;
+    RawRequest ahead;
 
     __device__ __forceinline__ int cost() const { return tiles > 0 ? tiles : 1; }
-    __device__ __forceinline__ void enter(const AttnParams& p) {
-        r = request_at(p, b, nullptr);
-        while (r.rows == 0 && b + 1 < p.bt.num_requests) r = request_at(p, ++b, nullptr);
-        tiles = tiles_of<kRows>(p, r, rt);
+    __device__ __forceinline__ void look_ahead(const AttnParams& p) {
+        ahead = raw_request(p, min(b + 1, p.bt.num_requests - 1));
     }
     __device__ __forceinline__ void next(const AttnParams& p) {
         if (++h < p.kv_heads) return;
         h = 0;
-        if (++rt * kRows >= r.rows) {
-            rt = 0;
-            if (++b >= p.bt.num_requests) return;  // the end of the list
-            enter(p);
+        if ((rt + 1) * kRows < r.rows) {
+            ++rt;
         } else {
-            tiles = tiles_of<kRows>(p, r, rt);
+            rt = 0;
+            do {
+                if (++b >= p.bt.num_requests) return;  // the end of the list
+                r = request_of(p, ahead, nullptr);
+                look_ahead(p);
+            } while (r.rows == 0);
         }
+        tiles = tiles_of<kRows>(p, r, rt);
     }
 };
 
+template <int kRows>
 struct Share {
     long long begin, end, per;  // this CTA's run of the list
-    int b, rt, h, tile;         // where it begins
+    int tile;                   // its first tile, in the unit at
+    Cursor<kRows> at;
 };
 
 // Whole CTA: this CTA's share of the list.  Each thread adds up a run of
 // requests; a scan over the threads places the runs, and the thread whose run
 // holds the CTA's first tile looks it up.
 template <typename C>
-__device__ void find_share(const AttnParams& p, Share* s, long long* s_warp) {
+__device__ void find_share(const AttnParams& p, Share<C::kRows>* s, long long* s_warp) {
     constexpr int kWarps = C::kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = p.bt.num_requests;
@@ -184,7 +220,8 @@ __device__ void find_share(const AttnParams& p, Share* s, long long* s_warp) {
     for (int i = 0; i < each; ++i) {
         const int b = tid * each + i;
         if (b >= n) break;
-        const Request r = request_at(p, b, blockIdx.x == 0 ? p.status : nullptr);
+        const Request r =
+            request_of(p, raw_request(p, b), blockIdx.x == 0 ? p.status : nullptr);
         long long t = 0;
         for (int rt = 0; rt * C::kRows < r.rows; ++rt)
             t += max(1, tiles_of<C::kRows>(p, r, rt));
@@ -205,8 +242,7 @@ __device__ void find_share(const AttnParams& p, Share* s, long long* s_warp) {
         total += s_warp[w];
     }
     before -= sum;
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    per = max(per, (long long)p.min_tiles);
+    const long long per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)p.min_tiles);
     const long long begin = min(total, per * blockIdx.x);
     if (tid == 0) {
         s->begin = begin;
@@ -215,15 +251,20 @@ __device__ void find_share(const AttnParams& p, Share* s, long long* s_warp) {
     }
     if (begin < total && before <= begin && begin < before + sum) {
         for (int b = tid * each;; ++b) {
-            const Request r = request_at(p, b, nullptr);
+            const Request r = request_of(p, raw_request(p, b), nullptr);
             for (int rt = 0; rt * C::kRows < r.rows; ++rt) {
-                const int cost = max(1, tiles_of<C::kRows>(p, r, rt));
+                const int tiles = tiles_of<C::kRows>(p, r, rt), cost = max(1, tiles);
                 const long long unit = (long long)cost * p.kv_heads;
                 if (begin < before + unit) {
-                    s->b = b;
-                    s->rt = rt;
-                    s->h = (int)((begin - before) / cost);
-                    s->tile = (int)((begin - before) % cost);
+                    Cursor<C::kRows> u;
+                    u.b = b;
+                    u.rt = rt;
+                    u.h = (int)divide(begin - before, cost);
+                    u.tiles = tiles;
+                    u.r = r;
+                    u.look_ahead(p);
+                    s->tile = (int)(begin - before - (long long)u.h * cost);
+                    s->at = u;
                     b = n;  // found
                     break;
                 }
@@ -329,7 +370,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     __shared__ uint64_t s_full[C::kFull], s_empty[C::kStages];
     __shared__ int s_valid[C::kStages];
     __shared__ long long s_warp[C::kThreads / 32];
-    __shared__ Share s_share;
+    __shared__ Share<C::kRows> s_share;
     __shared__ int s_abort;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                ~(uintptr_t)1023);
@@ -337,8 +378,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint4* s_q = reinterpret_cast<uint4*>(tail);
     float* s_merge = reinterpret_cast<float*>(tail + C::kQBytes);
     float2* s_ml = reinterpret_cast<float2*>(tail + C::kQBytes + C::kMergeBytes);
-    float2* s_row = s_ml + C::kTokenWarps * C::kRows;  // maximum and sum of a row
-    float* s_factor = reinterpret_cast<float*>(s_row + C::kRows);  // score factor of a row
+    float* s_factor = reinterpret_cast<float*>(s_ml + C::kTokenWarps * C::kRows);  // of a row
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -360,11 +400,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (tid == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = 0;
         return;
     }
-    Cursor<C::kRows> u;
-    u.b = s_share.b;
-    u.rt = s_share.rt;
-    u.h = s_share.h;
-    u.enter(p);
+    Cursor<C::kRows> u = s_share.at;
     int tile = s_share.tile;
     if (p.whole && tile != 0) {  // begun by the CTA before, which finishes it
         pos += u.cost() - tile;
@@ -373,56 +409,68 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
 
     if (warp >= C::kConsumers) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kProducerRegs));
         if (warp > C::kConsumers) return;
-        // copies: the warp holds the next 32 table entries, its first lane issues
-        int n = 0;  // tiles issued
+        // copies: the warp holds the next 32 table entries of the unit and the first
+        // 32 of the one after it, its first lane issues
+        auto entries = [&](const Cursor<C::kRows>& x, int t) {
+            return t + lane < x.tiles
+                       ? __ldg(p.bt.block_table + (int64_t)x.b * p.bt.max_pages + t + lane)
+                       : -1;
+        };
         int pieces = 0;
+        // of the first lane: pages issued, and the next one's stage, full barrier and
+        // empty parity (a fresh barrier's phase before the first counts as complete)
+        int n = 0, st = 0, fb = 0;
+        uint32_t parity = 1;
         bool ok = true;
-        while (ok && pos < end) {
+        int ahead = entries(u, tile);
+        while (pos < end) {
             const int take =
                 p.whole ? u.cost() : (int)min((long long)(u.cost() - tile), end - pos);
             const int last = min(u.tiles, tile + take);
-            const int32_t* row = p.bt.block_table + (int64_t)u.b * p.bt.max_pages;
-            int ahead = tile + lane < last ? __ldg(row + tile + lane) : -1;
-            for (int t = tile; ok && t < last; ++t) {
+            Cursor<C::kRows> v = u;
+            int ahead_v = -1;
+            if (pos + take < end) {
+                v.next(p);
+                ahead_v = entries(v, 0);
+            }
+            for (int t = tile; t < last; ++t) {
                 const int i = (t - tile) & 31;
-                if (i == 0 && t != tile) ahead = t + lane < last ? __ldg(row + t + lane) : -1;
+                if (i == 0 && t != tile) ahead = entries(u, t);
                 const int page = __shfl_sync(0xffffffffu, ahead, i);
-                const int st = n % C::kStages;
-                uint64_t* full = &s_full[n % C::kFull];
-                int go = 1;
-                if (lane == 0) {
-                    go = n < C::kStages ||
-                         mbar_wait(&s_empty[st], ((n / C::kStages) - 1) & 1, abort_flag);
-                    if (go) {
-                        const bool valid = page >= 0 && page < p.bt.num_pages;
-                        s_valid[st] = valid;
-                        if (valid) {
-                            mbar_arrive_expect_tx(full, C::kStageBytes);
-                            uint8_t* dst = ring + st * C::kStageBytes;
-                            const int z = page * p.kv_heads + u.h;
+                if (lane == 0 && ok && (ok = mbar_wait(&s_empty[st], parity, abort_flag))) {
+                    const bool valid = page >= 0 && page < p.bt.num_pages;
+                    s_valid[st] = valid;
+                    if (valid) {
+                        mbar_arrive_expect_tx(&s_full[fb], C::kStageBytes);
+                        uint8_t* dst = ring + st * C::kStageBytes;
+                        const int z = page * p.kv_heads + u.h;
 #pragma unroll
-                            for (int x = 0; x < C::kBoxes; ++x)
-                                tma_load_3d(dst + x * (kPage * C::kBoxBytes), &tm_k,
-                                            x * C::kBoxBytes, 0, z, full);
+                        for (int x = 0; x < C::kBoxes; ++x)
+                            tma_load_3d(dst + x * (kPage * C::kBoxBytes), &tm_k, x * C::kBoxBytes,
+                                        0, z, &s_full[fb]);
 #pragma unroll
-                            for (int x = 0; x < C::kBoxes; ++x)
-                                tma_load_3d(dst + C::kTileBytes + x * (kPage * C::kBoxBytes), &tm_v,
-                                            x * C::kBoxBytes, 0, z, full);
-                        } else {
-                            record_error(p.status, DSA_ERR_DEVICE_CHECK);
-                            mbar_arrive(full);
-                        }
+                        for (int x = 0; x < C::kBoxes; ++x)
+                            tma_load_3d(dst + C::kTileBytes + x * (kPage * C::kBoxBytes), &tm_v,
+                                        x * C::kBoxBytes, 0, z, &s_full[fb]);
+                    } else {
+                        record_error(p.status, DSA_ERR_DEVICE_CHECK);
+                        mbar_arrive(&s_full[fb]);
+                    }
+                    ++n;
+                    if (++fb == C::kFull) fb = 0;
+                    if (++st == C::kStages) {
+                        st = 0;
+                        parity ^= 1;
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-                if (ok) ++n;
+                __syncwarp();
             }
             if (lane == 0 && tile == 0 && take < u.cost()) {
                 // first piece of a row tile that other CTAs finish
                 int32_t* j = p.joins + blockIdx.x * kJoinInts;
-                pieces = 1 + (int)((u.cost() - take + s_share.per - 1) / s_share.per);
+                pieces = 1 + (int)divide(u.cost() - take + s_share.per - 1, s_share.per);
                 j[kJoinToken] = u.r.q0;
                 j[kJoinRow] = u.rt * C::kRows;
                 j[kJoinRows] = min(C::kRows, u.r.rows - u.rt * C::kRows);
@@ -430,7 +478,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             pos += take;
             tile = 0;
-            u.next(p);
+            u = v;
+            ahead = ahead_v;
         }
         if (lane == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
         if (lane == 0 && *abort_flag) {
@@ -441,7 +490,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         return;
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kConsumerRegs));
 
     const int grp = warp / (C::kWM * C::kWN);
     const int wn = warp / C::kWM % C::kWN, wm = warp % C::kWM;
@@ -474,93 +523,90 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int take = p.whole ? u.cost() : (int)min((long long)(u.cost() - tile), end - pos);
         const int tile_row = u.rt * C::kRows;  // first row of the row tile in its request
 
-        // Queries of 16 rows as A fragments, with their score factors.  For FP8 the
-        // columns of a 16-value group are taken in the order in which the lifted
-        // keys come, 4 c .. 4 c + 3.
-        auto load_q = [&](int row0, float (&f)[2], auto&& put) {
-            bool in[2];
-            const uint16_t* q[2];
+        // Queries to shared memory as A fragments, a warp per row; a row's score factor
+        // beside them.  For FP8 the columns of a 16-value group are taken in the
+        // order in which the lifted keys come, 4 c .. 4 c + 3.
+        constexpr int kWords = kD / 64;  // pairs of values of a row in a lane
+        constexpr int kRowsWarp = (C::kRows + C::kConsumers - 1) / C::kConsumers;
+        uint32_t qw[kRowsWarp][kWords];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = row0 + g + 8 * x;
-                in[x] = r < u.r.rows;
-                q[x] = static_cast<const uint16_t*>(p.q) +
-                       (int64_t)(u.r.q0 + r / p.group) * p.q_stride +
-                       (int64_t)(u.h * p.group + r % p.group) * kD;
-                f[x] = p.score_scale;
-            }
-            uint32_t a[kD / 16][4];  // all loads in flight at once
+        for (int x = 0; x < kRowsWarp; ++x) {
+            const int r = tile_row + warp + x * C::kConsumers;
+            const int j = token_of(p, r);
+            const uint16_t* q = static_cast<const uint16_t*>(p.q) +
+                                (int64_t)(u.r.q0 + j) * p.q_stride +
+                                (int64_t)(u.h * p.group + r - j * p.group) * kD;
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (C::kFp8) {
-                        const uint2 v = in[x] ? *reinterpret_cast<const uint2*>(q[x] + ks * 16 + 4 * c)
-                                              : make_uint2(0, 0);
-                        a[ks][x] = v.x;
-                        a[ks][2 + x] = v.y;
-                    } else {
-                        const int at = ks * 16 + 2 * c;
-                        a[ks][x] = in[x] ? *reinterpret_cast<const uint32_t*>(q[x] + at) : 0;
-                        a[ks][2 + x] = in[x] ? *reinterpret_cast<const uint32_t*>(q[x] + at + 8) : 0;
-                    }
+            for (int i = 0; i < kWords; ++i) qw[x][i] = 0;
+            if (warp + x * C::kConsumers < C::kRows && r < u.r.rows) {
+                if (kWords == 1) {
+                    qw[x][0] = *(reinterpret_cast<const uint32_t*>(q) + lane);
+                } else if (kWords == 2) {
+                    const uint2 w = *(reinterpret_cast<const uint2*>(q) + lane);
+                    qw[x][0] = w.x;
+                    qw[x][kWords > 1 ? 1 : 0] = w.y;
+                } else {
+                    const uint4 w = *(reinterpret_cast<const uint4*>(q) + lane);
+                    qw[x][0] = w.x;
+                    qw[x][kWords > 1 ? 1 : 0] = w.y;
+                    qw[x][kWords > 2 ? 2 : 0] = w.z;
+                    qw[x][kWords > 2 ? 3 : 0] = w.w;
                 }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kRowsWarp; ++x) {
+            const int r = warp + x * C::kConsumers;
+            if (r >= C::kRows) break;
+            float factor = p.score_scale;
             if (C::kFp8 && kQBf16) {
                 // bf16 to f16: scale the row by a power of two that brings its
                 // largest value to 1..2 (what then falls below f16's range is
                 // below 2^-25 of that value), and undo it in the score factor
-                float up[2] = {1.f, 1.f};
+                uint32_t top = 0;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int ks = 0; ks < kD / 16; ++ks) {
-                        top = max(top, max(a[ks][x] & 0x7fffu, (a[ks][x] >> 16) & 0x7fffu));
-                        top = max(top, max(a[ks][2 + x] & 0x7fffu, (a[ks][2 + x] >> 16) & 0x7fffu));
-                    }
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // biased exponent; zero, infinite and NaN rows stay unscaled
-                    const uint32_t e = top >> 7;
-                    if (e != 0 && e < 254) {
-                        up[x] = __uint_as_float((254 - e) << 23);
-                        f[x] *= __uint_as_float(e << 23);
-                    }
+                for (int i = 0; i < kWords; ++i)
+                    top = max(top, max(qw[x][i] & 0x7fffu, (qw[x][i] >> 16) & 0x7fffu));
+                top = __reduce_max_sync(0xffffffffu, top);
+                // biased exponent; zero, infinite and NaN rows stay unscaled
+                const uint32_t e = top >> 7;
+                float up = 1.f;
+                if (e != 0 && e < 254) {
+                    up = __uint_as_float((254 - e) << 23);
+                    factor *= __uint_as_float(e << 23);
                 }
 #pragma unroll
-                for (int ks = 0; ks < kD / 16; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        a[ks][i] = pack2<false>(__uint_as_float(a[ks][i] << 16) * up[i & 1],
-                                                __uint_as_float(a[ks][i] & 0xffff0000u) * up[i & 1]);
+                for (int i = 0; i < kWords; ++i)
+                    qw[x][i] = pack2<false>(__uint_as_float(qw[x][i] << 16) * up,
+                                            __uint_as_float(qw[x][i] & 0xffff0000u) * up);
             }
+            if (lane == 0) s_factor[r] = factor;
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) put(ks, a[ks]);
-        };
+            for (int i = 0; i < kWords; ++i) {
+                const int pair = lane * kWords + i, at = pair & 7;
+                const int column = C::kFp8 ? at >> 1 : at & 3, half = C::kFp8 ? at & 1 : at >> 2;
+                reinterpret_cast<uint32_t*>(
+                    s_q)[(((r >> 4) * (kD / 16) + (pair >> 3)) * 32 + (r & 7) * 4 + column) * 4 +
+                         2 * half + ((r >> 3) & 1)] = qw[x][i];
+            }
+        }
+        consumer_sync<32 * C::kConsumers>();
         float f[kMT][2];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+            f[mt][0] = s_factor[16 * (wm * kMT + mt) + g];
+            f[mt][1] = s_factor[16 * (wm * kMT + mt) + g + 8];
+        }
         uint32_t qf[C::kQSmem ? 1 : kD / 16][4];
-        if (C::kQSmem) {
-            for (int mi = warp; mi < C::kWM * kMT; mi += C::kConsumers) {
-                float own[2];
-                load_q(tile_row + 16 * mi, own, [&](int ks, const uint32_t (&a)[4]) {
-                    s_q[(mi * (kD / 16) + ks) * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
-                });
-                if (c == 0) {
-                    s_factor[16 * mi + g] = own[0];
-                    s_factor[16 * mi + g + 8] = own[1];
-                }
-            }
-            consumer_sync<32 * C::kConsumers>();
+        if (!C::kQSmem) {
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-                f[mt][0] = s_factor[16 * (wm * kMT + mt) + g];
-                f[mt][1] = s_factor[16 * (wm * kMT + mt) + g + 8];
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                const uint4 w = s_q[(wm * (kD / 16) + ks) * 32 + lane];
+                qf[C::kQSmem ? 0 : ks][0] = w.x;
+                qf[C::kQSmem ? 0 : ks][1] = w.y;
+                qf[C::kQSmem ? 0 : ks][2] = w.z;
+                qf[C::kQSmem ? 0 : ks][3] = w.w;
             }
-        } else {
-            load_q(tile_row + 16 * wm, f[0], [&](int ks, const uint32_t (&a)[4]) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qf[C::kQSmem ? 0 : ks][i] = a[i];
-            });
         }
 
         // this thread's rows: g and g + 8 of each 16; what they see
@@ -570,10 +616,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int r = tile_row + 16 * (wm * kMT + mt) + g + 8 * x;
-                vis[mt][x] = r < u.r.rows ? u.r.seq - u.r.nb + r / p.group + 1 : 0;
+                vis[mt][x] = r < u.r.rows ? u.r.seq - u.r.nb + token_of(p, r) + 1 : 0;
             }
-        const int vis_first =
-            u.r.seq - u.r.nb + (tile_row + 16 * wm * kMT) / p.group + 1;
+        const int vis_first = u.r.seq - u.r.nb + token_of(p, tile_row + 16 * wm * kMT) + 1;
 
         float o[kMT][C::kTilesD][4];
         float m[kMT][2], l[kMT][2];
@@ -766,8 +811,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         n += max(0, last - tile);
 
-        // join the warps that share rows: bring all to the common maximum, then add
-        // 32 dims at a time through shared memory, every thread four values
+        // Join the warps that share rows, 32 dims at a time through shared memory: each
+        // thread adds four dims of a row over the warps, weighted by what their
+        // maxima lack to the common one.
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
             const int r = 16 * (wm * kMT + mt) + g;
@@ -778,41 +824,24 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 s_ml[tw * C::kRows + r + 8] = make_float2(m[mt][1], l[mt][1]);
             }
         }
-        consumer_sync<32 * C::kConsumers>();
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = 16 * (wm * kMT + mt) + g + 8 * x;
-                float y = -INFINITY, total = 0.f;
-#pragma unroll
-                for (int w = 0; w < C::kTokenWarps; ++w) y = fmaxf(y, s_ml[w * C::kRows + r].x);
-                if (tw == 0) {
-#pragma unroll
-                    for (int w = 0; w < C::kTokenWarps; ++w) {
-                        const float2 ml = s_ml[w * C::kRows + r];
-                        total += ml.y * ex2(ml.x - base_of(y));
-                    }
-                    if (c == 0) s_row[r] = make_float2(y, total);
-                }
-                const float a = ex2(m[mt][x] - base_of(y));
-#pragma unroll
-                for (int i = 0; i < C::kTilesD; ++i) {
-                    o[mt][i][2 * x] *= a;
-                    o[mt][i][2 * x + 1] *= a;
-                }
-            }
         const bool complete = tile == 0 && take == u.cost();
         const int rows = min(C::kRows, u.r.rows - tile_row);
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0)) * C::kRows;
+        constexpr int kQuads = C::kMergeDims / 4;
+        constexpr int kItems = (C::kRows * kQuads + 32 * C::kConsumers - 1) / (32 * C::kConsumers);  // rows of a thread
+        const int quad = tid % kQuads * 4;
+        float weight[kItems][C::kTokenWarps];
+        int64_t at[kItems];  // output row, or row of the piece
+        float inv[kItems];
 #pragma unroll
         for (int d0 = 0; d0 < kD; d0 += C::kMergeDims) {
+            float* buffer = s_merge + d0 / C::kMergeDims % C::kMergeBuffers *
+                                          (C::kTokenWarps * C::kRows * C::kMergeLd);
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float* dst = s_merge + (tw * C::kRows + 16 * (wm * kMT + mt) + g + 8 * x) *
-                                               C::kMergeLd;
+                    float* dst = buffer + (tw * C::kRows + 16 * (wm * kMT + mt) + g + 8 * x) *
+                                              C::kMergeLd;
                     constexpr int kPer = C::kMergeDims / 8;
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
@@ -830,37 +859,58 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                 }
             consumer_sync<32 * C::kConsumers>();
-            for (int i = tid; i < rows * (C::kMergeDims / 4); i += 32 * C::kConsumers) {
-                const int r = i / (C::kMergeDims / 4), d = i % (C::kMergeDims / 4) * 4;
-                const float top = s_row[r].x, total = s_row[r].y;
+#pragma unroll
+            for (int x = 0; x < kItems; ++x) {
+                const int r = (tid + 32 * C::kConsumers * x) / kQuads;
+                if (r >= rows) continue;
+                if (d0 == 0) {
+                    float top = -INFINITY, total = 0.f;
+#pragma unroll
+                    for (int w = 0; w < C::kTokenWarps; ++w)
+                        top = fmaxf(top, s_ml[w * C::kRows + r].x);
+                    const float base = base_of(top);
+#pragma unroll
+                    for (int w = 0; w < C::kTokenWarps; ++w) {
+                        const float2 ml = s_ml[w * C::kRows + r];
+                        weight[x][w] = ex2(ml.x - base);
+                        total += ml.y * weight[x][w];
+                    }
+                    if (complete) {
+                        const int j = token_of(p, tile_row + r);
+                        at[x] = (int64_t)(u.r.q0 + j) * (p.kv_heads * p.group) + u.h * p.group +
+                                tile_row + r - j * p.group;
+                        inv[x] = total == 0.f ? 0.f : p.v_scale / total;
+                        if (p.lse && quad == 0)
+                            p.lse[at[x]] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+                    } else {
+                        at[x] = (2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0)) * C::kRows + r;
+                        inv[x] = 1.f;
+                        if (quad == 0)
+                            *reinterpret_cast<float2*>(p.part_ml + 2 * at[x]) =
+                                make_float2(top, total);
+                    }
+                }
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < C::kTokenWarps; ++w) {
                     const float4 v = *reinterpret_cast<const float4*>(
-                        s_merge + (w * C::kRows + r) * C::kMergeLd + d);
-                    sum.x += v.x;
-                    sum.y += v.y;
-                    sum.z += v.z;
-                    sum.w += v.w;
+                        buffer + (w * C::kRows + r) * C::kMergeLd + quad);
+                    sum.x += weight[x][w] * v.x;
+                    sum.y += weight[x][w] * v.y;
+                    sum.z += weight[x][w] * v.z;
+                    sum.w += weight[x][w] * v.w;
                 }
-                if (complete) {
-                    const int row = tile_row + r;
-                    const int64_t at = (int64_t)(u.r.q0 + row / p.group) * (p.kv_heads * p.group) +
-                                       u.h * p.group + row % p.group;
-                    const float inv = total == 0.f ? 0.f : p.v_scale / total;
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * kD + d0 + d) =
-                        make_uint2(pack2<kQBf16>(sum.x * inv, sum.y * inv),
-                                   pack2<kQBf16>(sum.z * inv, sum.w * inv));
-                    if (p.lse && d0 + d == 0)
-                        p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
-                } else {
-                    *reinterpret_cast<float4*>(p.part_o + (slot + r) * kD + d0 + d) = sum;
-                    if (d0 + d == 0)
-                        *reinterpret_cast<float2*>(p.part_ml + 2 * (slot + r)) =
-                            make_float2(top, total);
-                }
+                if (complete)
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at[x] * kD + d0 +
+                                              quad) =
+                        make_uint2(pack2<kQBf16>(sum.x * inv[x], sum.y * inv[x]),
+                                   pack2<kQBf16>(sum.z * inv[x], sum.w * inv[x]));
+                else
+                    *reinterpret_cast<float4*>(p.part_o + at[x] * kD + d0 + quad) = sum;
             }
-            consumer_sync<32 * C::kConsumers>();
+            // the next pass writes the other buffer (where there are two); the next
+            // unit's barriers keep it from overtaking the last reads of this one
+            if (C::kMergeBuffers == 1) consumer_sync<32 * C::kConsumers>();
         }
         pos += take;
         tile = 0;
@@ -954,7 +1004,7 @@ constexpr int kMinTiles = 2;
 // them, so that the cache is read once, but 16 when every request runs whole
 // (a row's arithmetic must not depend on the other requests' row counts).
 int row_tile(int64_t max_rows, bool whole) {
-    return whole || max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
+    return whole || max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 48 ? 48 : 64;
 }
 
 struct WsLayout {
@@ -985,7 +1035,7 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
                    ? a.numRegs
                    : 0;
     }();
-    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if (regs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
@@ -1011,18 +1061,21 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
 template <int kD, bool kFp8, bool kQBf16>
 cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* launches,
                         cudaStream_t stream) {
-    // D = 256 has 128 accumulators a thread for 16 rows; the others take 32 rows a
-    // warp, which halves the fragment loads per MMA
-    constexpr bool kWide = kD == 256;
+    // D = 256 has 128 accumulators a thread for 16 rows and so eight warps, D = 64
+    // has 32 and sixteen
     switch (row_tile((int64_t)p.bt.max_q * p.group, p.whole != 0)) {
         case 16:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, 1, 2, 4>, kQBf16>(p, cache, launches, stream);
+            return launch_cfg<AttnCfg<kD, kFp8, 1, 1, 2, 4>, kQBf16>(
+                p, cache, launches, stream);
         case 32:
-            return launch_cfg<AttnCfg<kD, kFp8, kWide ? 1 : 2, kWide ? 2 : 1, 2, kWide ? 2 : 4>,
-                              kQBf16>(p, cache, launches, stream);
+            return launch_cfg<AttnCfg<kD, kFp8, 1, 2, 2, kD == 256 ? 2 : 3>, kQBf16>(
+                p, cache, launches, stream);
+        case 48:
+            return launch_cfg<AttnCfg<kD, kFp8, 1, kD == 256 ? 4 : 3, 2, kD == 256 ? 1 : 2>, kQBf16>(
+                p, cache, launches, stream);
         default:
-            return launch_cfg<AttnCfg<kD, kFp8, kWide ? 1 : 2, kWide ? 4 : 2, 2, kWide ? 1 : 2>,
-                              kQBf16>(p, cache, launches, stream);
+            return launch_cfg<AttnCfg<kD, kFp8, 1, 4, 2, kD == 256 ? 1 : 2>, kQBf16>(
+                p, cache, launches, stream);
     }
 }
 
@@ -1052,6 +1105,7 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
     p.bt = bt;
     p.kv_heads = cache.num_kv_heads;
     p.group = num_q_heads / cache.num_kv_heads;
+    p.inv_group = 1.0f / (float)p.group;
     p.min_tiles = kMinTiles;
     p.whole = whole;
     p.q_stride = q_stride;
