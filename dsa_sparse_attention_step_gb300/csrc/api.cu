@@ -59,6 +59,7 @@ cudaError_t launch_rope_append(int num_tokens, const dsa_kv_cache& cache, int fo
                                int64_t v_stride, void* q_out, int64_t q_out_stride,
                                int32_t* status, cudaStream_t stream);
 
+bool paged_attention_supported(const BatchArgs& bt, int kv_heads, int group);
 size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim);
 cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
@@ -508,7 +509,8 @@ dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache
         batch->num_pages != cache->num_pages)
         return DSA_ERR_INVALID_ARG;
     const int group = num_q_heads / cache->num_kv_heads;
-    if (num_q_heads > kMaxHeads || (int64_t)batch->max_q_per_request * group > (1 << 30))
+    if (num_q_heads > kMaxHeads || (int64_t)batch->max_q_per_request * group > (1 << 30) ||
+        !paged_attention_supported(to_args(batch), cache->num_kv_heads, group))
         return DSA_ERR_UNSUPPORTED;
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
     if (batch->total_q == 0) return DSA_OK;

@@ -46,7 +46,7 @@ struct AttnParams {
     BatchArgs bt;
     int32_t kv_heads, group;
     float inv_group;
-    int32_t min_tiles;  // least tiles of a CTA
+    int32_t min_length;  // least length of a CTA's run of the list
     int32_t whole;      // every (request, row tile, KV head) by one CTA
     int64_t q_stride;
     const void* q;
@@ -61,11 +61,12 @@ struct AttnParams {
 };
 
 // What a joining block needs to know of the row tile whose first piece a CTA wrote.
+// The first four are read as one vector.
 enum { kJoinPieces, kJoinToken, kJoinRow, kJoinRows, kJoinHead, kJoinInts = 8 };
 
 // The consumer warps: kNG groups, each taking every kNG-th page of the CTA's run;
 // within a group kWM warps along the rows (kMT tiles of 16 rows each) by kWN warps
-// along the page's tokens.  8, 12 or 16 warps, as many as the accumulators' registers
+// along the page's tokens.  8 or 12 warps, as many as the accumulators' registers
 // allow: a warp's softmax is a chain of dependent instructions, and only other
 // warps fill its gaps.
 template <int kD, bool kKvFp8, int kMT_, int kWM_, int kWN_, int kNG_>
@@ -88,7 +89,7 @@ struct AttnCfg {
     static constexpr int kPairs = kRowBytes / 32;  // pairs of 16-byte chunks in a row
     static constexpr int kTilesD = kD / 8;         // accumulator tiles along the dims
     // Q fragments of one row tile fit the registers beside 64 or fewer accumulators
-    static constexpr bool kQSmem = kMT > 1 || kD == 256 || (kD == 128 && kConsumers == 16);
+    static constexpr bool kQSmem = kMT > 1 || kD == 256;
     static constexpr int kQBytes = kRows * kD * 2;
     static constexpr int kMergeDims = 32;            // joined at a time
     // two buffers save a barrier a pass, where they take less than a stage or two
@@ -99,23 +100,39 @@ struct AttnCfg {
     static constexpr int kMlBytes = kTokenWarps * kRows * 8 + kRows * 4;
     static constexpr int kFixed = 1024 + kQBytes + kMergeBytes + kMlBytes;
     static constexpr int kFit = (226 * 1024 - kFixed) / kStageBytes;
-    static constexpr int kStages = kFit < 12 ? kFit : 12;
+    // A copying warp takes about 500 cycles a page (wait, arm, issue).  FP8 pages of
+    // up to 16 KB come faster than that: four warps copy every fourth page each (64
+    // dims: 92.5 -> 55.7 us for 152 requests of 16384; 128: 357 -> 350 us for the
+    // ragged batch of 64).  16-bit pages of 16 KB gain nothing in long requests and
+    // lose 13% in short ones to the shallower ring.  The stages then are a multiple
+    // of four, so that each warp keeps its own, and of kNG, so that full barriers and
+    // stages go together (below).
+    static constexpr int kMost = kFit < 12 ? kFit : 12;
+    static constexpr int kProducers =
+        kKvFp8 && kStageBytes <= 16384 && kMost >= 4 && kMost / 4 * 4 % kNG == 0 ? 4 : 1;
+    static constexpr int kStages = kMost / kProducers * kProducers;
     static constexpr int kSmem = kFixed + kStages * kStageBytes;
     // Page n of a CTA's run lands in stage n mod kStages but signals full barrier
     // n mod kFull, a multiple of kNG: a barrier then belongs to one group, which sees
     // each of its phases.  (Copies may finish out of order; a group that waited on a
     // barrier another group's page still has to complete would take the phase before
-    // for its own.)  kFull >= kStages: by the time a barrier is armed again, its page
-    // has been released.
+    // for its own.)  A barrier may be armed again once its page has been released:
+    // one copying warp has waited for the release of all pages up to n - kStages, so
+    // kFull >= kStages will do; of several each knows its own stage only.
     static constexpr int kFull = (kStages + kNG - 1) / kNG * kNG;
+    static_assert(kProducers == 1 || kFull == kStages, "");
+    // What a unit costs besides its tiles (queries, the join of the warps: about 2000
+    // cycles), in tiles at the rate at which HBM brings them (24 bytes a cycle).
+    static constexpr int kUnitCost = (2000 * 24 + kStageBytes / 2) / kStageBytes;
+    static_assert(kUnitCost <= 8, "");
     // The launch gives every thread kLaunchRegs registers (launch bounds); the copying
     // warpgroup then hands most of its share to the consumers.
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kProducerRegs = kConsumers == 12 ? 56 : 40;
-    static constexpr int kConsumerRegs = kConsumers == 8 ? 232 : kConsumers == 12 ? 152 : 104;
+    static constexpr int kProducerRegs = kConsumers == 12 ? 56 : kD == 256 ? 40 : 72;
+    static constexpr int kConsumerRegs = kConsumers == 12 ? 152 : kD == 256 ? 232 : 208;
     static_assert(128 * kProducerRegs + 32 * kConsumers * kConsumerRegs <= kThreads * kLaunchRegs,
                   "setmaxnreg.inc would wait forever");
-    static_assert(kConsumers == 8 || kConsumers == 12 || kConsumers == 16, "");
+    static_assert(kConsumers == 8 || kConsumers == 12, "");
     static_assert(kStages >= 2, "");
 };
 
@@ -129,12 +146,6 @@ __device__ __forceinline__ int token_of(const AttnParams& p, int row) {
     t += rest >= p.group;
     t -= rest < 0;
     return t;
-}
-
-// 64-bit division, in 32 bits where both fit.
-__device__ __forceinline__ long long divide(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
 }
 
 // One request as the schedule sees it; rows = 0 when it brings no tokens or its
@@ -170,9 +181,9 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, const Request& r, i
     return vis > 0 ? (vis + kPage - 1) / kPage : 0;
 }
 
-// A place in the list.  Units run over requests, row tiles, KV heads; a unit
-// without key tiles counts as one, so that somebody writes its empty rows.  The
-// next request's metadata are loaded one request ahead.
+// A place in the list.  Units run over requests, row tiles, KV heads.  A unit
+// without key tiles counts as one tile, so that somebody writes its empty rows.
+// The next request's metadata are loaded one request ahead.
 template <int kRows>
 struct Cursor {
     int b, rt, h, tiles;
@@ -200,77 +211,118 @@ struct Cursor {
     }
 };
 
+// In the list a unit is as long as its tiles and kUnitCost more in front of them,
+// for what a unit costs a CTA besides its tiles.  Positions are 32-bit: the host
+// refuses longer lists.
 template <int kRows>
 struct Share {
-    long long begin, end, per;  // this CTA's run of the list
-    int tile;                   // its first tile, in the unit at
+    uint32_t begin, end, per;  // this CTA's run of the list
+    uint32_t offset;           // of the first position, in the unit at
     Cursor<kRows> at;
 };
 
-// Whole CTA: this CTA's share of the list.  Each thread adds up a run of
-// requests; a scan over the threads places the runs, and the thread whose run
-// holds the CTA's first tile looks it up.
+// A CTA's way through its run.  Copying and consuming warps each take their own,
+// after they have parted: with the start in shared variables the compiler moves
+// common subexpressions above the fork and spills them in both.
 template <typename C>
-__device__ void find_share(const AttnParams& p, Share<C::kRows>* s, long long* s_warp) {
+struct Walk {
+    uint32_t pos, end, offset;  // offset of pos in u
+    int tile, count;            // of u in this run: first tile, tiles
+    Cursor<C::kRows> u;
+
+    __device__ __forceinline__ Walk(const AttnParams& p, const Share<C::kRows>& s)
+        : pos(s.begin), end(s.end), offset(s.offset), u(s.at) {
+        u.look_ahead(p);
+        settle(p);
+    }
+    // Makes (tile, count) this run's part of u, passing over units of which it has
+    // none.  With `whole` a unit belongs to the run that holds its first position.
+    __device__ __forceinline__ void settle(const AttnParams& p) {
+        while (pos < end) {
+            const uint32_t length = C::kUnitCost + u.cost();
+            const uint32_t stop = p.whole ? length : min(length, offset + (end - pos));
+            tile = max((int)offset - C::kUnitCost, 0);
+            count = max((int)stop - C::kUnitCost, 0) - tile;
+            if (p.whole && offset > 0) count = 0;
+            if (count > 0) return;
+            advance(p);
+        }
+    }
+    __device__ __forceinline__ void advance(const AttnParams& p) {
+        pos += C::kUnitCost + u.cost() - offset;
+        offset = 0;
+        if (pos < end) u.next(p);
+    }
+    __device__ __forceinline__ void next(const AttnParams& p) {
+        advance(p);
+        settle(p);
+    }
+    __device__ __forceinline__ bool complete() const { return count == u.cost(); }
+};
+
+// Whole CTA: this CTA's share of the list.  Each thread adds up a run of
+// requests; sums over the warps place the warps, and in the warp whose run holds
+// the CTA's first position a scan finds the thread, which looks it up.
+template <typename C>
+__device__ void find_share(const AttnParams& p, Share<C::kRows>* s, uint32_t* s_warp) {
     constexpr int kWarps = C::kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = p.bt.num_requests;
     const int each = (n + C::kThreads - 1) / C::kThreads;
-    long long sum = 0;
-    for (int i = 0; i < each; ++i) {
-        const int b = tid * each + i;
-        if (b >= n) break;
-        const Request r =
-            request_of(p, raw_request(p, b), blockIdx.x == 0 ? p.status : nullptr);
-        long long t = 0;
+    const int first = tid * each;
+    uint32_t sum = 0;
+    Request r = {0, 0, 0, 0};
+    for (int b = first; b < min(n, first + each); ++b) {
+        r = request_of(p, raw_request(p, b), blockIdx.x == 0 ? p.status : nullptr);
         for (int rt = 0; rt * C::kRows < r.rows; ++rt)
-            t += max(1, tiles_of<C::kRows>(p, r, rt));
-        sum += t * p.kv_heads;
+            sum += (max(1, tiles_of<C::kRows>(p, r, rt)) + C::kUnitCost) * p.kv_heads;
     }
-    long long before = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += x;
-    }
-    if (lane == 31) s_warp[warp] = before;
+    const uint32_t warp_sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) s_warp[warp] = warp_sum;
     __syncthreads();
-    long long total = 0;
+    uint32_t total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_warp[w];
         total += s_warp[w];
     }
-    before -= sum;
-    const long long per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)p.min_tiles);
-    const long long begin = min(total, per * blockIdx.x);
+    const uint32_t per = max((total + gridDim.x - 1) / gridDim.x, (uint32_t)p.min_length);
+    const uint32_t begin = (uint32_t)min((unsigned long long)per * blockIdx.x,
+                                         (unsigned long long)total);
     if (tid == 0) {
         s->begin = begin;
         s->end = min(total, begin + per);
         s->per = per;
     }
-    if (begin < total && before <= begin && begin < before + sum) {
-        for (int b = tid * each;; ++b) {
-            const Request r = request_of(p, raw_request(p, b), nullptr);
-            for (int rt = 0; rt * C::kRows < r.rows; ++rt) {
-                const int tiles = tiles_of<C::kRows>(p, r, rt), cost = max(1, tiles);
-                const long long unit = (long long)cost * p.kv_heads;
-                if (begin < before + unit) {
-                    Cursor<C::kRows> u;
-                    u.b = b;
-                    u.rt = rt;
-                    u.h = (int)divide(begin - before, cost);
-                    u.tiles = tiles;
-                    u.r = r;
-                    u.look_ahead(p);
-                    s->tile = (int)(begin - before - (long long)u.h * cost);
-                    s->at = u;
-                    b = n;  // found
-                    break;
+    if (begin < total && before <= begin && begin < before + warp_sum) {
+        uint32_t upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        before += upto - sum;
+        if (before <= begin && begin < before + sum) {
+            for (int b = first;; ++b) {
+                if (each > 1) r = request_of(p, raw_request(p, b), nullptr);
+                int rt = 0;
+                for (; rt * C::kRows < r.rows; ++rt) {
+                    const int tiles = tiles_of<C::kRows>(p, r, rt);
+                    const uint32_t length = max(1, tiles) + C::kUnitCost;
+                    if (begin < before + length * p.kv_heads) {
+                        const uint32_t h = (begin - before) / length;
+                        s->offset = begin - before - h * length;
+                        s->at.b = b;
+                        s->at.rt = rt;
+                        s->at.h = (int)h;
+                        s->at.tiles = tiles;
+                        s->at.r = r;
+                        break;
+                    }
+                    before += length * p.kv_heads;
                 }
-                before += unit;
+                if (rt * C::kRows < r.rows) break;  // found
             }
-            if (b >= n) break;
         }
     }
     __syncthreads();
@@ -369,7 +421,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t s_full[C::kFull], s_empty[C::kStages];
     __shared__ int s_valid[C::kStages];
-    __shared__ long long s_warp[C::kThreads / 32];
+    __shared__ uint32_t s_warp[C::kThreads / 32];
     __shared__ Share<C::kRows> s_share;
     __shared__ int s_abort;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
@@ -394,51 +446,45 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     find_share<C>(p, &s_share, s_warp);
     volatile int* abort_flag = &s_abort;
 
-    const long long end = s_share.end;
-    long long pos = s_share.begin;
-    if (pos >= end) {
+    if (s_share.begin >= s_share.end) {
         if (tid == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = 0;
         return;
-    }
-    Cursor<C::kRows> u = s_share.at;
-    int tile = s_share.tile;
-    if (p.whole && tile != 0) {  // begun by the CTA before, which finishes it
-        pos += u.cost() - tile;
-        tile = 0;
-        u.next(p);
     }
 
     if (warp >= C::kConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kProducerRegs));
-        if (warp > C::kConsumers) return;
-        // copies: the warp holds the next 32 table entries of the unit and the first
-        // 32 of the one after it, its first lane issues
+        const int me = warp - C::kConsumers;
+        if (me >= C::kProducers) return;
+        Walk<C> walk(p, s_share);
+        // Copies: every kProducers-th page of the run.  The warp holds 32 table
+        // entries of the unit and the first 32 of the one after it; its first lane
+        // issues.
         auto entries = [&](const Cursor<C::kRows>& x, int t) {
             return t + lane < x.tiles
                        ? __ldg(p.bt.block_table + (int64_t)x.b * p.bt.max_pages + t + lane)
                        : -1;
         };
         int pieces = 0;
-        // of the first lane: pages issued, and the next one's stage, full barrier and
+        // the first lane's next page: its number in the run, stage, full barrier and
         // empty parity (a fresh barrier's phase before the first counts as complete)
-        int n = 0, st = 0, fb = 0;
+        int n = me, st = me, fb = me;
         uint32_t parity = 1;
+        int skip = me;  // pages until this warp's next one
         bool ok = true;
-        int ahead = entries(u, tile);
-        while (pos < end) {
-            const int take =
-                p.whole ? u.cost() : (int)min((long long)(u.cost() - tile), end - pos);
-            const int last = min(u.tiles, tile + take);
-            Cursor<C::kRows> v = u;
-            int ahead_v = -1;
-            if (pos + take < end) {
-                v.next(p);
-                ahead_v = entries(v, 0);
-            }
-            for (int t = tile; t < last; ++t) {
-                const int i = (t - tile) & 31;
-                if (i == 0 && t != tile) ahead = entries(u, t);
-                const int page = __shfl_sync(0xffffffffu, ahead, i);
+        int ahead = walk.pos < walk.end ? entries(walk.u, walk.tile) : -1;
+        while (walk.pos < walk.end) {
+            const Cursor<C::kRows>& u = walk.u;
+            const int tile = walk.tile, count = min(u.tiles, tile + walk.count) - tile;
+            Walk<C> v = walk;
+            v.next(p);
+            const int ahead_v = v.pos < v.end ? entries(v.u, v.tile) : -1;
+            int i = skip, held = 0;
+            for (; i < count; i += C::kProducers) {
+                if (i - held >= 32) {
+                    held = i & ~31;
+                    ahead = entries(u, tile + held);
+                }
+                const int page = __shfl_sync(0xffffffffu, ahead, i & 31);
                 if (lane == 0 && ok && (ok = mbar_wait(&s_empty[st], parity, abort_flag))) {
                     const bool valid = page >= 0 && page < p.bt.num_pages;
                     s_valid[st] = valid;
@@ -458,33 +504,33 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         record_error(p.status, DSA_ERR_DEVICE_CHECK);
                         mbar_arrive(&s_full[fb]);
                     }
-                    ++n;
-                    if (++fb == C::kFull) fb = 0;
-                    if (++st == C::kStages) {
-                        st = 0;
+                    n += C::kProducers;
+                    if ((fb += C::kProducers) >= C::kFull) fb -= C::kFull;
+                    if ((st += C::kProducers) >= C::kStages) {
+                        st -= C::kStages;
                         parity ^= 1;
                     }
                 }
                 __syncwarp();
             }
-            if (lane == 0 && tile == 0 && take < u.cost()) {
+            skip = i - max(count, 0);
+            if (me == 0 && lane == 0 && tile == 0 && !walk.complete()) {
                 // first piece of a row tile that other CTAs finish
                 int32_t* j = p.joins + blockIdx.x * kJoinInts;
-                pieces = 1 + (int)divide(u.cost() - take + s_share.per - 1, s_share.per);
+                pieces = 1 + (int)((u.cost() - walk.count + s_share.per - 1) / s_share.per);
                 j[kJoinToken] = u.r.q0;
                 j[kJoinRow] = u.rt * C::kRows;
                 j[kJoinRows] = min(C::kRows, u.r.rows - u.rt * C::kRows);
                 j[kJoinHead] = u.h * p.group;
             }
-            pos += take;
-            tile = 0;
-            u = v;
+            walk = v;
             ahead = ahead_v;
         }
-        if (lane == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
+        if (me == 0 && lane == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
         if (lane == 0 && *abort_flag) {
             // an unwinding CTA must not exit under copies in flight
-            for (int i = max(0, n - C::kStages); i < n; ++i)
+            for (int i = n - C::kProducers; i >= 0 && i > n - C::kProducers - C::kStages;
+                 i -= C::kProducers)
                 mbar_drain(&s_full[i % C::kFull], (i / C::kFull) & 1);
             record_error(p.status, DSA_ERR_TIMEOUT);
         }
@@ -492,6 +538,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kConsumerRegs));
 
+    Walk<C> walk(p, s_share);
     const int grp = warp / (C::kWM * C::kWN);
     const int wn = warp / C::kWM % C::kWN, wm = warp % C::kWM;
     const int tw = grp * C::kWN + wn;  // of the warps that share rows
@@ -519,19 +566,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     int n = 0;  // pages of the CTA's run before the current unit
     bool dead = false;
 
-    while (pos < end) {
-        const int take = p.whole ? u.cost() : (int)min((long long)(u.cost() - tile), end - pos);
-        const int tile_row = u.rt * C::kRows;  // first row of the row tile in its request
-
-        // Queries to shared memory as A fragments, a warp per row; a row's score factor
-        // beside them.  For FP8 the columns of a 16-value group are taken in the
-        // order in which the lifted keys come, 4 c .. 4 c + 3.
-        constexpr int kWords = kD / 64;  // pairs of values of a row in a lane
-        constexpr int kRowsWarp = (C::kRows + C::kConsumers - 1) / C::kConsumers;
-        uint32_t qw[kRowsWarp][kWords];
+    // Queries of this warp's rows of a row tile, one row a warp at a time.
+    constexpr int kWords = kD / 64;  // pairs of values of a row in a lane
+    constexpr int kRowsWarp = (C::kRows + C::kConsumers - 1) / C::kConsumers;
+    uint32_t qw[kRowsWarp][kWords];
+    auto load_q = [&](const Cursor<C::kRows>& u) {
 #pragma unroll
         for (int x = 0; x < kRowsWarp; ++x) {
-            const int r = tile_row + warp + x * C::kConsumers;
+            const int r = u.rt * C::kRows + warp + x * C::kConsumers;
             const int j = token_of(p, r);
             const uint16_t* q = static_cast<const uint16_t*>(p.q) +
                                 (int64_t)(u.r.q0 + j) * p.q_stride +
@@ -554,6 +596,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
             }
         }
+    };
+    // loaded a unit ahead where the registers allow it
+    constexpr bool kQAhead = kRowsWarp * kWords <= 4;
+    if (kQAhead && walk.pos < walk.end) load_q(walk.u);
+
+    while (walk.pos < walk.end) {
+        const Cursor<C::kRows>& u = walk.u;
+        const int tile = walk.tile;
+        const int tile_row = u.rt * C::kRows;  // first row of the row tile in its request
+
+        if (!kQAhead) load_q(u);
+        // Queries to shared memory as A fragments; a row's score factor beside them.
+        // For FP8 the columns of a 16-value group are taken in the order in which the
+        // lifted keys come, 4 c .. 4 c + 3.
 #pragma unroll
         for (int x = 0; x < kRowsWarp; ++x) {
             const int r = warp + x * C::kConsumers;
@@ -589,6 +645,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     s_q)[(((r >> 4) * (kD / 16) + (pair >> 3)) * 32 + (r & 7) * 4 + column) * 4 +
                          2 * half + ((r >> 3) & 1)] = qw[x][i];
             }
+        }
+        if (kQAhead) {  // the next unit's, for which there is time until this one is done
+            Walk<C> v = walk;
+            v.next(p);
+            if (v.pos < v.end) load_q(v.u);
         }
         consumer_sync<32 * C::kConsumers>();
         float f[kMT][2];
@@ -631,7 +692,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             l[mt][0] = l[mt][1] = 0.f;
         }
 
-        const int last = min(u.tiles, tile + take);
+        const int last = min(u.tiles, tile + walk.count);
         // this group's pages: those whose number in the run is grp modulo kNG
         for (int t = tile + (grp + C::kNG - n % C::kNG) % C::kNG; t < last; t += C::kNG) {
             const int i_run = n + (t - tile), st = i_run % C::kStages;
@@ -824,7 +885,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 s_ml[tw * C::kRows + r + 8] = make_float2(m[mt][1], l[mt][1]);
             }
         }
-        const bool complete = tile == 0 && take == u.cost();
+        const bool complete = walk.complete();
         const int rows = min(C::kRows, u.r.rows - tile_row);
         constexpr int kQuads = C::kMergeDims / 4;
         constexpr int kItems = (C::kRows * kQuads + 32 * C::kConsumers - 1) / (32 * C::kConsumers);  // rows of a thread
@@ -912,9 +973,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             // unit's barriers keep it from overtaking the last reads of this one
             if (C::kMergeBuffers == 1) consumer_sync<32 * C::kConsumers>();
         }
-        pos += take;
-        tile = 0;
-        u.next(p);
+        walk.next(p);
     }
     if (dead && lane == 0) record_error(p.status, DSA_ERR_TIMEOUT);
 }
@@ -932,9 +991,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnPara
     grid_dependents_launch();
     grid_dependency_wait();
     const int cta = blockIdx.x, row = blockIdx.y;
-    const int32_t* j = p.joins + cta * kJoinInts;
-    const int pieces = __ldcg(j + kJoinPieces);
-    if (pieces == 0 || row >= __ldcg(j + kJoinRows)) return;
+    const int4 join = __ldcg(reinterpret_cast<const int4*>(p.joins + cta * kJoinInts));
+    const int join_head = __ldcg(p.joins + cta * kJoinInts + kJoinHead);
+    const int pieces = join.x;
+    if (pieces == 0 || row >= join.w) return;
     const int x = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -969,9 +1029,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnPara
         o.z = o.z * a + v.z * b;
         o.w = o.w * a + v.w * b;
     }
-    const int r = __ldcg(j + kJoinRow) + row;
-    const int64_t at = (int64_t)(__ldcg(j + kJoinToken) + r / p.group) * (p.kv_heads * p.group) +
-                       __ldcg(j + kJoinHead) + r % p.group;
+    const int r = join.z + row, t = token_of(p, r);
+    const int64_t at =
+        (int64_t)(join.y + t) * (p.kv_heads * p.group) + join_head + r - t * p.group;
     const float inv = l == 0.f ? 0.f : p.v_scale / l;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * kDim + 4 * x) =
         make_uint2(pack2<kQBf16>(o.x * inv, o.y * inv), pack2<kQBf16>(o.z * inv, o.w * inv));
@@ -1005,6 +1065,14 @@ constexpr int kMinTiles = 2;
 // (a row's arithmetic must not depend on the other requests' row counts).
 int row_tile(int64_t max_rows, bool whole) {
     return whole || max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 48 ? 48 : 64;
+}
+
+// At most so many units: a request of n_b tokens has n_b group / rows row tiles,
+// and one more for what is left.
+double most_units(const BatchArgs& bt, int kv_heads, int group, int rows) {
+    const double each = (double)(((int64_t)bt.max_q * group + rows - 1) / rows) * bt.num_requests;
+    const double all = (double)bt.total_q * group / rows + bt.num_requests;
+    return (each < all ? each : all) * kv_heads;
 }
 
 struct WsLayout {
@@ -1041,12 +1109,12 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
     // no more CTAs than the longest list that these host sizes allow has work for
+    const double units = most_units(p.bt, p.kv_heads, p.group, C::kRows);
     const int64_t tiles = ((int64_t)p.bt.max_seq + kPage - 1) / kPage;
-    const int64_t row_tiles = ((int64_t)p.bt.max_q * p.group + C::kRows - 1) / C::kRows;
-    const double most = (double)p.bt.num_requests * row_tiles * p.kv_heads * tiles;
+    p.min_length = C::kUnitCost + kMinTiles;
     int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-    if (most < (double)ctas * p.min_tiles)
-        ctas = (int)((most + p.min_tiles - 1) / p.min_tiles);
+    if (units * (tiles + C::kUnitCost) < (double)ctas * p.min_length)
+        ctas = (int)(units * (tiles + C::kUnitCost) / p.min_length) + 1;
     if (ctas < 1) ctas = 1;
     e = launch_kernel(paged_attention_kernel<C, kQBf16>, dim3((unsigned)ctas), dim3(C::kThreads),
                       (size_t)C::kSmem, stream, true, 1, tm_k, tm_v, p);
@@ -1074,7 +1142,7 @@ cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* lau
             return launch_cfg<AttnCfg<kD, kFp8, 1, kD == 256 ? 4 : 3, 2, kD == 256 ? 1 : 2>, kQBf16>(
                 p, cache, launches, stream);
         default:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, 4, 2, kD == 256 ? 1 : 2>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 1, 4, kD == 256 ? 2 : 1, kD == 256 ? 1 : 3>, kQBf16>(
                 p, cache, launches, stream);
     }
 }
@@ -1092,6 +1160,12 @@ cudaError_t launch_dim(const AttnParams& p, const dsa_kv_cache& cache, int forma
 
 }  // namespace
 
+// Positions in the list of key tiles are 32-bit (kUnitCost is at most 8).
+bool paged_attention_supported(const BatchArgs& bt, int kv_heads, int group) {
+    const double tiles = ((double)bt.max_seq + kPage - 1) / kPage;
+    return most_units(bt, kv_heads, group, 16) * (tiles + 1 + 8) < 2147483648.0;
+}
+
 // Of the default plan, which needs more than the whole one.
 size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim) {
     return ws_layout(head_dim, row_tile(max_rows, false)).total;
@@ -1106,7 +1180,6 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
     p.kv_heads = cache.num_kv_heads;
     p.group = num_q_heads / cache.num_kv_heads;
     p.inv_group = 1.0f / (float)p.group;
-    p.min_tiles = kMinTiles;
     p.whole = whole;
     p.q_stride = q_stride;
     p.q = q;

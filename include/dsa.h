@@ -517,7 +517,8 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
  *   lse[t,i]   = log sum_s exp(z[s])          (natural log)
  * The new tokens' own keys and values must be in the cache already.  Any n_b
  * is taken; the kernel is made for decode and verification steps (a few
- * tokens per request).
+ * tokens per request).  DSA_ERR_UNSUPPORTED where the host sizes allow more than
+ * about 2^31 pairs of 16 query rows and a page of keys.
  *   q    [T, num_q_heads, head_dim] of `format`, tokens q_stride elements apart
  *        (a multiple of 8), 16-byte aligned
  *   out  [T, num_q_heads, head_dim] of `format`, contiguous, 16-byte aligned

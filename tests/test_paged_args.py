@@ -103,7 +103,10 @@ def test_cache_refusals_by_paged_attention(lib, kw, code):
     (dict(q=ODD), INVALID), (dict(qs=500), INVALID), (dict(sm=0.0), INVALID),
     (dict(sm=float("nan")), INVALID), (dict(sm=float("inf")), INVALID), (dict(out=None), INVALID),
     (dict(out=ODD), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=ODD), WORKSPACE),
-    (dict(ws_bytes=1000), WORKSPACE)])
+    (dict(ws_bytes=1000), WORKSPACE),
+    # 2^20 new tokens of one request, each over up to 2^20 positions
+    (dict(batch=dict(total_q=1 << 20, max_q_per_request=1 << 20, max_seq_len=1 << 20,
+                     max_pages=1 << 14)), UNSUPPORTED)])
 def test_paged_attention_refusals(lib, kw, code):
     assert _attention(lib, **kw) == code
 
