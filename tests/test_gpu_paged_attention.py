@@ -112,9 +112,12 @@ def spread(seed, requests, top):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("hq,hkv,new", [(1, 1, 1), (8, 8, 1), (12, 1, 1), (32, 8, 5), (40, 2, 1),
                                         (8, 1, 9), (15, 3, 27)])
-def test_formats_and_head_layouts(dtype, kv, d, hq, hkv, new):
-    lens = [max(n, new) for n in spread(d + hq, 5, 1500)]
-    c = Case(lens, [new] * 5, hq, hkv, d, dtype, kv, seed=hq)
+@pytest.mark.parametrize("filler", [0, 170])
+def test_formats_and_head_layouts(dtype, kv, d, hq, hkv, new, filler):
+    """Few requests (a cluster to each KV head), and more than there are SMs (equal
+    shares of one list), most of those of one token."""
+    lens = [max(n, new) for n in spread(d + hq, 5, 1500)] + [1] * filler
+    c = Case(lens, [new] * 5 + [1] * filler, hq, hkv, d, dtype, kv, seed=hq)
     c.check(*c.run())
 
 
@@ -123,6 +126,8 @@ def test_formats_and_head_layouts(dtype, kv, d, hq, hkv, new):
 @pytest.mark.parametrize("new,kv", [(1, BF16), (7, FP8)])
 def test_lengths(length, new, kv):
     c = Case([length, 3 * length], [min(new, length), 1], 4, 2, 128, BF16, kv, seed=length)
+    c.check(*c.run())
+    c = Case([length, 3 * length] * 45, [min(new, length), 1] * 45, 4, 2, 64, BF16, kv, seed=length)
     c.check(*c.run())
 
 
