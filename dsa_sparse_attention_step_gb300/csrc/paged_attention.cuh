@@ -70,13 +70,15 @@ enum { kJoinPieces, kJoinToken, kJoinRow, kJoinRows, kJoinHead, kJoinInts = 8 };
 
 // The consumer warps: kNG groups, each taking every kNG-th page of the CTA's run;
 // within a group kWM warps along the rows (kMT tiles of 16 rows each) by kWN warps
-// along the page's tokens.  8 or 12 warps, as many as the accumulators' registers
+// along the page's tokens.  8 or 12 warps (4 of each of two CTAs), as many as the accumulators' registers
 // allow: a warp's softmax is a chain of dependent instructions, and only other
 // warps fill its gaps.
-template <int kD, bool kKvFp8, int kMT_, int kWM_, int kWN_, int kNG_, bool kDirect_ = false>
+template <int kD, bool kKvFp8, int kMT_, int kWM_, int kWN_, int kNG_, bool kDirect_ = false,
+          int kCtas_ = 1>
 struct AttnCfg {
     static constexpr int kDim = kD;
     static constexpr bool kDirect = kDirect_;  // a cluster to a unit, no list
+    static constexpr int kCtas = kCtas_;       // of an SM
     using Direct = AttnCfg<kD, kKvFp8, kMT_, kWM_, kWN_, kNG_, true>;
     static constexpr bool kFp8 = kKvFp8;
     static constexpr int kMT = kMT_, kWM = kWM_, kWN = kWN_, kNG = kNG_;
@@ -99,15 +101,15 @@ struct AttnCfg {
     // us with both in registers and 16-token steps, 587 so)
     static constexpr bool kQSmem = kMT > 1 || kD == 256 || (kD == 128 && kConsumers == 12);
     static constexpr int kQBytes = kRows * kD * 2;
-    static constexpr int kMergeDims = 32;            // joined at a time
-    // two buffers save a barrier a pass, where they take less than a stage or two
-    static constexpr int kMergeBuffers =
-        kTokenWarps * kRows > 128 || (kD == 256 && !kKvFp8) ? 1 : 2;
-    static constexpr int kMergeLd = kMergeDims + 8;    // floats; keeps fragment stores apart
-    static constexpr int kMergeBytes = kMergeBuffers * kTokenWarps * kRows * kMergeLd * 4;
+    // The join of the warps takes so many dims at a time; 64 keep all threads busy
+    // where the buffer then takes no stage that is needed.
+    static constexpr int kMergeDims =
+        kRows == 16 && (kD < 256 || kKvFp8) ? 64 : 32;
+    static constexpr int kMergeLd = kMergeDims + 8;  // floats; keeps fragment stores apart
+    static constexpr int kMergeBytes = kTokenWarps * kRows * kMergeLd * 4;
     static constexpr int kMlBytes = kTokenWarps * kRows * 8 + kRows * 4;
     static constexpr int kFixed = 1024 + kQBytes + kMergeBytes + kMlBytes;
-    static constexpr int kFit = (226 * 1024 - kFixed) / kStageBytes;
+    static constexpr int kFit = ((kCtas == 1 ? 226 : 111) * 1024 - kFixed) / kStageBytes;
     // A copying warp takes about 500 cycles a page (wait, arm, issue).  FP8 pages of
     // up to 16 KB come faster than that: four warps copy every fourth page each (64
     // dims: 92.5 -> 55.7 us for 152 requests of 16384; 128: 357 -> 350 us for the
@@ -130,17 +132,18 @@ struct AttnCfg {
     static constexpr int kFull = (kStages + kNG - 1) / kNG * kNG;
     static_assert(kProducers == 1 || kFull == kStages, "");
     // What a unit costs besides its tiles (queries, the join of the warps: about 2000
-    // cycles), in tiles at the rate at which HBM brings them (24 bytes a cycle).
-    static constexpr int kUnitCost = (2000 * 24 + kStageBytes / 2) / kStageBytes;
+    // to 5000 cycles), in tiles at the rate at which HBM brings them (24 bytes a cycle).
+    static constexpr int kUnitCost =
+        ((kD == 64 ? 2000 : 5000) * 24 + kStageBytes / 2) / kStageBytes;
     static_assert(kUnitCost <= 8, "");
     // The launch gives every thread kLaunchRegs registers (launch bounds); the copying
     // warpgroup then hands most of its share to the consumers.
-    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kProducerRegs = kConsumers == 12 ? 56 : kD == 256 ? 40 : 72;
+    static constexpr int kLaunchRegs = 65536 / (kThreads * kCtas) / 8 * 8;
+    static constexpr int kProducerRegs = kConsumers == 12 ? 56 : kD == 256 || kConsumers == 4 ? 40 : 72;
     static constexpr int kConsumerRegs = kConsumers == 12 ? 152 : kD == 256 ? 232 : 208;
     static_assert(128 * kProducerRegs + 32 * kConsumers * kConsumerRegs <= kThreads * kLaunchRegs,
                   "setmaxnreg.inc would wait forever");
-    static_assert(kConsumers == 8 || kConsumers == 12, "");
+    static_assert(kConsumers == 4 * (3 - kCtas) || kConsumers == 12, "");
     static_assert(kStages >= 2 && kStages * kStageBytes >= kRows * (kD + 2) * 4, "");
 };
 
@@ -479,7 +482,7 @@ __device__ __forceinline__ void consumer_sync() {
 // ---- the kernel ----------------------------------------------------------------
 
 template <typename C, bool kQBf16>
-__global__ void __launch_bounds__(C::kThreads, 1)
+__global__ void __launch_bounds__(C::kThreads, C::kCtas)
 paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
     // operands of the MMAs: the cache's own type, or f16 lifted from FP8
@@ -940,9 +943,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         n += max(0, last - tile);
 
-        // Join the warps that share rows, 32 dims at a time through shared memory: each
-        // thread adds four dims of a row over the warps, weighted by what their
-        // maxima lack to the common one.
+        // Join the warps that share rows, kMergeDims at a time through shared memory:
+        // each thread adds four dims of a row over the warps, weighted by what their
+        // maxima lack to the common one.  (The next unit's barriers keep its writes
+        // from overtaking the last pass's reads.)
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
             const int r = 16 * (wm * kMT + mt) + g;
@@ -966,13 +970,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         float inv[kItems];
 #pragma unroll
         for (int d0 = 0; d0 < kD; d0 += C::kMergeDims) {
-            float* buffer = s_merge + d0 / C::kMergeDims % C::kMergeBuffers *
-                                          (C::kTokenWarps * C::kRows * C::kMergeLd);
+            if (d0 > 0) consumer_sync<32 * C::kConsumers>();  // the last pass has been read
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float* dst = buffer + (tw * C::kRows + 16 * (wm * kMT + mt) + g + 8 * x) *
+                    float* dst = s_merge + (tw * C::kRows + 16 * (wm * kMT + mt) + g + 8 * x) *
                                               C::kMergeLd;
                     constexpr int kPer = C::kMergeDims / 8;
 #pragma unroll
@@ -1028,7 +1031,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                 for (int w = 0; w < C::kTokenWarps; ++w) {
                     const float4 v = *reinterpret_cast<const float4*>(
-                        buffer + (w * C::kRows + r) * C::kMergeLd + quad);
+                        s_merge + (w * C::kRows + r) * C::kMergeLd + quad);
                     sum.x += weight[x][w] * v.x;
                     sum.y += weight[x][w] * v.y;
                     sum.z += weight[x][w] * v.z;
@@ -1043,9 +1046,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     *reinterpret_cast<float4*>((C::kDirect ? piece_o : p.part_o) + at[x] * kD + d0 +
                                                quad) = sum;
             }
-            // the next pass writes the other buffer (where there are two); the next
-            // unit's barriers keep it from overtaking the last reads of this one
-            if (C::kMergeBuffers == 1) consumer_sync<32 * C::kConsumers>();
         }
         if (C::kDirect && p.cluster > 1) {
             // the cluster's pieces, read from its CTAs' shared memory
@@ -1241,6 +1241,23 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
             return launch_kernel(paged_attention_kernel<D, kQBf16>,
                                  dim3((unsigned)(units * p.cluster)), dim3(D::kThreads),
                                  (size_t)D::kSmem, stream, true, p.cluster, tm_k, tm_v, p);
+        }
+    }
+    // Many short units of a few rows: a CTA to a unit, two to an SM, so that the fixed
+    // costs of one overlap the other's tiles (64 requests of up to 256 positions, 4
+    // heads of 128: 13.8 -> 7.1 us).  The longest unit alone bounds the time where the
+    // list would spread it: the sides meet at 13 to 16 pages of 32 KB, 16 to 30 of
+    // 16 KB and 25 to 35 of 8 KB, for 1 to 7 units an SM.
+    if constexpr (C::kRows == 16 && C::kDim < 256) {
+        if (!p.whole && units > sms && units < (1 << 24) &&
+            tiles * (C::kStageBytes + 8192) <= 524288) {
+            using S = AttnCfg<C::kDim, C::kFp8, 1, 1, 2, 2, true, 2>;
+            p.cluster = 1;
+            p.row_tiles = (int)row_tiles;
+            if ((e = prepare_kernel<S, kQBf16>()) != cudaSuccess) return e;
+            return launch_kernel(paged_attention_kernel<S, kQBf16>, dim3((unsigned)units),
+                                 dim3(S::kThreads), (size_t)S::kSmem, stream, true, 1, tm_k, tm_v,
+                                 p);
         }
     }
     if ((e = prepare_kernel<C, kQBf16>()) != cudaSuccess) return e;

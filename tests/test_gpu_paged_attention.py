@@ -112,11 +112,11 @@ def spread(seed, requests, top):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("hq,hkv,new", [(1, 1, 1), (8, 8, 1), (12, 1, 1), (32, 8, 5), (40, 2, 1),
                                         (8, 1, 9), (15, 3, 27)])
-@pytest.mark.parametrize("filler", [0, 170])
-def test_formats_and_head_layouts(dtype, kv, d, hq, hkv, new, filler):
-    """Few requests (a cluster to each KV head), and more than there are SMs (equal
-    shares of one list), most of those of one token."""
-    lens = [max(n, new) for n in spread(d + hq, 5, 1500)] + [1] * filler
+@pytest.mark.parametrize("filler,top", [(0, 1500), (170, 2100), (170, 300)])
+def test_formats_and_head_layouts(dtype, kv, d, hq, hkv, new, filler, top):
+    """Few requests (a cluster to each KV head), and more than there are SMs, most of
+    one token (equal shares of one list; for short contexts a CTA to a KV head)."""
+    lens = [max(n, new) for n in spread(d + hq, 5, top)] + [1] * filler
     c = Case(lens, [new] * 5 + [1] * filler, hq, hkv, d, dtype, kv, seed=hq)
     c.check(*c.run())
 
@@ -127,8 +127,9 @@ def test_formats_and_head_layouts(dtype, kv, d, hq, hkv, new, filler):
 def test_lengths(length, new, kv):
     c = Case([length, 3 * length], [min(new, length), 1], 4, 2, 128, BF16, kv, seed=length)
     c.check(*c.run())
-    c = Case([length, 3 * length] * 45, [min(new, length), 1] * 45, 4, 2, 64, BF16, kv, seed=length)
-    c.check(*c.run())
+    for d in (64, 256):
+        c = Case([length, 3 * length] * 45, [min(new, length), 1] * 45, 4, 2, d, BF16, kv, seed=length)
+        c.check(*c.run())
 
 
 @pytest.mark.parametrize("hq,hkv,d,length,new", [(4, 1, 128, 70001, 1), (3, 3, 64, 33333, 3),
