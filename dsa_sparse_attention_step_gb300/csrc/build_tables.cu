@@ -7,9 +7,12 @@
 //
 // Every CTA forms both sums over all requests by itself (at most 4096 pairs of
 // lengths, read through L2) and keeps them in shared memory, then fills its own
-// tile of tokens and its share of the new pages by binary search.  That repeats
-// up to 32 KB of reads per CTA but needs one launch and no ordering between
-// CTAs.  The work is bound by latency: the outputs are 16 bytes per token.
+// tiles of tokens and its share of the new pages.  That repeats up to 32 KB of reads
+// per CTA but needs one launch and no ordering between CTAs.  A warp writes 64
+// consecutive tokens, two a lane so that all stores are whole 16-byte words; it
+// looks its request up once where one request holds them all.
+//
+// Bound by latency up to some 100,000 tokens, then by the writes of 16 bytes a token.
 #include "common.cuh"
 
 namespace dsa {
@@ -18,8 +21,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kMaxRequests = 4096;
-constexpr int kTokensPerThread = 4;
-constexpr int kTile = kThreads * kTokensPerThread;
+constexpr int kPerThread = kMaxRequests / kThreads;  // requests summed by one thread
+constexpr int kTile = kThreads * 2;                  // tokens written at a time
+constexpr int kMaxCtas = 2 * 152;                    // resident at once
 
 struct TablesArgs {
     int32_t num_requests, num_free, num_pages, max_pages, max_tokens;
@@ -64,10 +68,9 @@ __device__ __forceinline__ int new_page(const TablesArgs& a, int64_t i) {
     return p >= 0 && p < a.num_pages ? p : -1;
 }
 
-// The last b with sums[b] <= x (sums is non-decreasing, sums[0] = 0): the
-// request whose range holds x, since ranges before the last equal entry are empty.
-__device__ __forceinline__ int owner_of(const int32_t* sums, int n, int x) {
-    int lo = 0, hi = n - 1;
+// The last b in [lo, hi] with sums[b] <= x (sums is non-decreasing, sums[lo] <= x):
+// the request whose range holds x, since ranges before the last equal entry are empty.
+__device__ __forceinline__ int owner_of(const int32_t* sums, int lo, int hi, int x) {
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (sums[mid] <= x) lo = mid;
@@ -76,125 +79,167 @@ __device__ __forceinline__ int owner_of(const int32_t* sums, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) build_tables_kernel(TablesArgs a) {
+// Sums stop at the largest int32 (associative for values of 0 and more).
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+    return min(a + b, (uint32_t)INT32_MAX);
+}
+
+// The cache slot of position pos of request b, whose new pages begin at first_new.
+__device__ __forceinline__ int64_t slot_of(const TablesArgs& a, const Growth& g, int b,
+                                           int first_new, int pos) {
+    if (!g.fits) return -1;
+    const int lp = pos / kPage;
+    int page;
+    if (lp >= g.held) {
+        page = new_page(a, (int64_t)first_new + lp - g.held);
+    } else {  // the page the cached tokens left open
+        page = __ldg(a.block_table + (int64_t)b * a.max_pages + lp);
+        if (page < 0 || page >= a.num_pages) {
+            page = -1;
+            record_error(a.status, DSA_ERR_DEVICE_CHECK);
+        }
+    }
+    return page < 0 ? -1 : (int64_t)page * kPage + pos % kPage;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) build_tables_kernel(TablesArgs a) {
     __shared__ int32_t s_tokens[kMaxRequests];
     __shared__ int32_t s_pages[kMaxRequests];
-    __shared__ int64_t s_warp[2][kThreads / 32];
+    __shared__ uint32_t s_warp[2][kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = a.num_requests;
     grid_dependents_launch();
     grid_dependency_wait();
 
-    // both sums in 64 bits: each thread sums a run of requests, then a scan over
-    // the threads' totals
+    // each thread sums a run of requests, then a scan over the threads' totals
     const int per = (n + kThreads - 1) / kThreads;
-    int64_t tokens = 0, pages = 0;
+    uint32_t added[kPerThread], grown[kPerThread], length[kPerThread];
+    uint32_t tokens = 0, pages = 0;
     bool bad = false;
-    for (int i = 0; i < per; ++i) {
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
         const int b = tid * per + i;
-        if (b < n) {
+        added[i] = grown[i] = length[i] = 0;
+        if (i < per && b < n) {
             const Growth g = growth_of(a, b);
-            tokens += g.added;
-            pages += g.grown;
+            added[i] = g.added;
+            grown[i] = g.grown;
+            length[i] = add(g.cached, g.added);
             bad |= !g.fits;
         }
+        tokens = add(tokens, added[i]);
+        pages = add(pages, grown[i]);
     }
-    int64_t ti = tokens, pi = pages;
+    uint32_t ti = tokens, pi = pages;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, ti, o), y = __shfl_up_sync(0xffffffffu, pi, o);
+        const uint32_t x = __shfl_up_sync(0xffffffffu, ti, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, pi, o);
         if (lane >= o) {
-            ti += x;
-            pi += y;
+            ti = add(ti, x);
+            pi = add(pi, y);
         }
     }
     if (lane == 31) {
         s_warp[0][warp] = ti;
         s_warp[1][warp] = pi;
     }
+    // exclusive within the warp
+    uint32_t t0 = __shfl_up_sync(0xffffffffu, ti, 1), p0 = __shfl_up_sync(0xffffffffu, pi, 1);
+    if (lane == 0) t0 = p0 = 0;
     __syncthreads();
-    int64_t t0 = 0, p0 = 0, all_tokens = 0, all_pages = 0;
+    uint32_t all_tokens = 0, all_pages = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        const int64_t x = s_warp[0][w], y = s_warp[1][w];
+        const uint32_t x = s_warp[0][w], y = s_warp[1][w];
         if (w < warp) {
-            t0 += x;
-            p0 += y;
+            t0 = add(t0, x);
+            p0 = add(p0, y);
         }
-        all_tokens += x;
-        all_pages += y;
+        all_tokens = add(all_tokens, x);
+        all_pages = add(all_pages, y);
     }
-    t0 += ti - tokens;
-    p0 += pi - pages;
-    const bool first = blockIdx.x == 0;
-    for (int i = 0; i < per; ++i) {
+    const uint32_t cap = a.max_tokens;
+    const bool writes = tid % gridDim.x == blockIdx.x;  // the offsets, spread over the CTAs
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
         const int b = tid * per + i;
-        if (b < n) {
-            const Growth g = growth_of(a, b);
-            const int32_t at = (int32_t)min(t0, (int64_t)a.max_tokens);
+        if (i < per && b < n) {
+            const int32_t at = (int32_t)min(t0, cap);
             s_tokens[b] = at;
-            s_pages[b] = (int32_t)min(p0, (int64_t)INT32_MAX);
-            if (first) {
+            s_pages[b] = (int32_t)p0;
+            if (writes) {
                 a.q_offsets[b] = at;
-                a.seq_lens[b] = (int32_t)min((int64_t)g.cached + g.added, (int64_t)INT32_MAX);
+                a.seq_lens[b] = (int32_t)length[i];
             }
-            t0 += g.added;
-            p0 += g.grown;
+            t0 = add(t0, added[i]);
+            p0 = add(p0, grown[i]);
         }
     }
-    const int T = (int)min(all_tokens, (int64_t)a.max_tokens);
-    if (first) {
+    const int T = (int)min(all_tokens, cap);
+    if (blockIdx.x == 0) {
         if (bad) record_error(a.status, DSA_ERR_DEVICE_CHECK);
         if (tid == 0) {
             a.q_offsets[n] = T;
-            *a.pages_taken = (int32_t)min(all_pages, (int64_t)INT32_MAX);
-            if (all_tokens > a.max_tokens || all_pages > a.num_free)
+            *a.pages_taken = (int32_t)all_pages;
+            if (all_tokens > cap || all_pages > (uint32_t)a.num_free)
                 record_error(a.status, DSA_ERR_DEVICE_CHECK);
         }
     }
     __syncthreads();
 
     // new table entries
-    const int64_t step = (int64_t)gridDim.x * kThreads;
-    const int64_t end = min(all_pages, (int64_t)INT32_MAX);
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < end; i += step) {
-        const int b = owner_of(s_pages, n, (int)i);
+    const uint32_t step = gridDim.x * kThreads;
+    for (uint32_t i = blockIdx.x * kThreads + tid; i < all_pages; i += step) {
+        const int b = owner_of(s_pages, 0, n - 1, (int)i);
         const int held = growth_of(a, b).held;
         const int page = new_page(a, i);
         if (page < 0) record_error(a.status, DSA_ERR_DEVICE_CHECK);
-        a.block_table[(int64_t)b * a.max_pages + held + (i - s_pages[b])] = page;
+        a.block_table[(int64_t)b * a.max_pages + held + ((int)i - s_pages[b])] = page;
     }
 
     // tokens
     if (!a.slots && !a.positions && !a.token_requests) return;
-    for (int i = 0; i < kTokensPerThread; ++i) {
-        const int64_t t64 = (int64_t)blockIdx.x * kTile + i * kThreads + tid;
-        if (t64 >= a.max_tokens) break;
-        const int t = (int)t64;
-        int b = -1, pos = 0;
-        int64_t slot = -1;
-        if (t < T) {
-            b = owner_of(s_tokens, n, t);
-            const Growth g = growth_of(a, b);
-            pos = (int)min((int64_t)g.cached + (t - s_tokens[b]), (int64_t)INT32_MAX);
-            if (g.fits) {
-                const int lp = pos / kPage;
-                int page;
-                if (lp >= g.held) {
-                    page = new_page(a, (int64_t)s_pages[b] + lp - g.held);
-                } else {  // the page the cached tokens left open
-                    page = __ldg(a.block_table + (int64_t)b * a.max_pages + lp);
-                    if (page < 0 || page >= a.num_pages) {
-                        page = -1;
-                        record_error(a.status, DSA_ERR_DEVICE_CHECK);
-                    }
-                }
-                if (page >= 0) slot = (int64_t)page * kPage + pos % kPage;
+    for (int64_t tile = (int64_t)blockIdx.x * kTile; tile < a.max_tokens;
+         tile += (int64_t)gridDim.x * kTile) {
+        const int64_t first = tile + warp * 64;  // of the warp's 64 tokens
+        if (first >= a.max_tokens) break;
+        int lo = 0, hi = n - 1;
+        if (first < T) {
+            lo = owner_of(s_tokens, 0, n - 1, (int)first);
+            if (lo == n - 1 || s_tokens[lo + 1] >= first + 64) hi = lo;
+        }
+        const int64_t t = first + 2 * lane;
+        int b[2], pos[2];
+        int64_t slot[2];
+        Growth g = {};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            b[x] = -1;
+            pos[x] = 0;
+            slot[x] = -1;
+            if (t + x < T) {
+                const int tx = (int)t + x;
+                b[x] = owner_of(s_tokens, x ? b[0] : lo, hi, tx);
+                if (x == 0 || b[1] != b[0]) g = growth_of(a, b[x]);
+                pos[x] = (int)add(g.cached, tx - s_tokens[b[x]]);
+                if (x == 1 && b[1] == b[0] && pos[1] % kPage != 0)
+                    slot[1] = slot[0] < 0 ? -1 : slot[0] + 1;  // the same page
+                else
+                    slot[x] = slot_of(a, g, b[x], s_pages[b[x]], pos[x]);
             }
         }
-        if (a.slots) a.slots[t] = slot;
-        if (a.positions) a.positions[t] = pos;
-        if (a.token_requests) a.token_requests[t] = b;
+        if (t + 1 < a.max_tokens) {
+            if (a.slots)
+                *reinterpret_cast<longlong2*>(a.slots + t) = make_longlong2(slot[0], slot[1]);
+            if (a.positions) *reinterpret_cast<int2*>(a.positions + t) = make_int2(pos[0], pos[1]);
+            if (a.token_requests)
+                *reinterpret_cast<int2*>(a.token_requests + t) = make_int2(b[0], b[1]);
+        } else if (t < a.max_tokens) {
+            if (a.slots) a.slots[t] = slot[0];
+            if (a.positions) a.positions[t] = pos[0];
+            if (a.token_requests) a.token_requests[t] = b[0];
+        }
     }
 }
 
@@ -226,9 +271,12 @@ cudaError_t launch_build_tables(int num_requests, const int32_t* cached, const i
     a.pages_taken = pages_taken;
     a.status = status;
     const bool per_token = slots || positions || token_requests;
-    const int64_t grid = per_token ? ((int64_t)max_tokens + kTile - 1) / kTile : 1;
-    return launch_kernel(build_tables_kernel, dim3((unsigned)(grid < 1 ? 1 : grid)), dim3(kThreads),
-                         0, stream, true, 1, a);
+    const int64_t tiles = per_token ? ((int64_t)max_tokens + kTile - 1) / kTile : 1;
+    // every CTA the same number of tiles
+    const int64_t each = (tiles + kMaxCtas - 1) / kMaxCtas;
+    const int64_t grid = tiles > 0 ? (tiles + each - 1) / each : 1;
+    return launch_kernel(build_tables_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, true,
+                         1, a);
 }
 
 }  // namespace dsa

@@ -10,10 +10,14 @@
 // unit of position).  Its upper 32 bits go to sincospi.  Two double-precision
 // operations per pair, none per value.
 //
-// Memory bound: every value is read and written once.  A CTA takes kTokens
-// tokens; its threads first form the pairs' cosines and sines in shared memory,
-// once for all heads of a token, then move units of 16 values (two 16-byte
-// loads: the two halves of eight pairs, or 16 consecutive values).
+// Memory bound: every value is read and written once.  A thread moves units of 16
+// values (two 16-byte loads: the two halves of eight pairs, or 16 consecutive
+// values).  A CTA forms its tokens' cosines and sines, once for all heads, in shared
+// memory.  Below about a million units a CTA takes as few tokens as give its threads
+// four units each, so that they fill the GPU, with two units a thread in flight, the
+// first two during the cosines; above, four tokens and one unit at a time, which
+// leaves the registers for more CTAs (1024 tokens of 48 heads of 128: 6.9 us so, 11.9
+// with the other; 32768 tokens of 40 heads of 256: 214 and 207 us, 6.5 TB/s).
 #include "common.cuh"
 
 namespace dsa {
@@ -21,11 +25,12 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;
-constexpr int kMaxPairs = 128;  // head_dim / 2
+constexpr int kBatch = 2;       // units of a thread in flight, for small calls
+constexpr int kMaxTokens = 16;  // of a CTA
 
 struct RopeArgs {
     int32_t num_tokens, q_heads, kv_heads, interleaved, pairs;
+    int32_t tokens;  // of a CTA
     int32_t end0, end1;  // first pair of the second and of the third section
     int64_t slot_end;
     const double* inv_freq;
@@ -67,8 +72,7 @@ __device__ __forceinline__ uint32_t from_float2<__half>(float x, float y) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -105,16 +109,122 @@ __device__ __forceinline__ void store8_fp8(uint8_t* p, const float (&x)[8], floa
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
+// A unit of work: 16 values of a token's head.
+template <typename T>
+struct Unit {
+    uint4 a, b;        // the values
+    int64_t row;       // of the destination: the token for q, the cache row else
+    int32_t at0, at1;  // first values of a and b in the head
+    int32_t kind;      // -1: nothing to do; 0: q; 1: k; 2: v
+    int32_t token, head, unit;
+};
+
 template <typename T, bool kFp8, int kDim>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
-    __shared__ float2 s_turn[kTokens][kMaxPairs];  // cos, sin
+__device__ __forceinline__ Unit<T> load_unit(const RopeArgs& a, int64_t first, int items, int count,
+                                             int i) {
     constexpr int kUnits = kDim / 16;
+    Unit<T> u;
+    u.kind = -1;
+    if (i >= count * items) return u;
+    const int j = i / items, rest = i - j * items;
+    const int head = rest / kUnits, unit = rest % kUnits;
+    const int64_t t = first + j;
+    u.token = j;
+    u.unit = unit;
+    const int kind = head < a.q_heads ? 0 : head < a.q_heads + a.kv_heads ? 1 : 2;
+    const int h = kind == 0 ? head : head - a.q_heads - (kind == 2 ? a.kv_heads : 0);
+    u.head = h;
+    u.row = t;
+    if (kind != 0) {
+        const int64_t slot = __ldg(a.slots + t);
+        if (slot < 0) return u;
+        if (slot >= a.slot_end) {
+            record_error(a.status, DSA_ERR_DEVICE_CHECK);
+            return u;
+        }
+        u.row = ((slot / kPage) * a.kv_heads + h) * kPage + slot % kPage;
+    }
+    u.kind = kind;
+    const T* src = (kind == 0   ? static_cast<const T*>(a.q) + t * a.q_stride
+                    : kind == 1 ? static_cast<const T*>(a.k) + t * a.k_stride
+                                : static_cast<const T*>(a.v) + t * a.v_stride) +
+                   h * kDim;
+    const bool halves = kind != 2 && unit < a.pairs / 8 && !a.interleaved;
+    u.at0 = halves ? unit * 8 : unit * 16;
+    u.at1 = halves ? unit * 8 + a.pairs : unit * 16 + 8;
+    u.a = *reinterpret_cast<const uint4*>(src + u.at0);
+    u.b = *reinterpret_cast<const uint4*>(src + u.at1);
+    return u;
+}
+
+template <typename T, bool kFp8, int kDim>
+__device__ __forceinline__ void finish_unit(const RopeArgs& a, const Unit<T>& u,
+                                            const float2* turns) {
+    if (u.kind < 0) return;
+    float x[8], y[8];
+    unpack8<T>(u.a, x);
+    unpack8<T>(u.b, y);
+    if (u.kind != 2 && u.unit < a.pairs / 8) {
+        // two (cos, sin) pairs a load
+        const float4* cs = reinterpret_cast<const float4*>(turns + u.token * a.pairs + u.unit * 8);
+        if (a.interleaved) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float4 c = cs[p], d = cs[2 + p];
+                const float x0 = x[4 * p], x1 = x[4 * p + 1], x2 = x[4 * p + 2], x3 = x[4 * p + 3];
+                const float y0 = y[4 * p], y1 = y[4 * p + 1], y2 = y[4 * p + 2], y3 = y[4 * p + 3];
+                x[4 * p] = x0 * c.x - x1 * c.y;
+                x[4 * p + 1] = x1 * c.x + x0 * c.y;
+                x[4 * p + 2] = x2 * c.z - x3 * c.w;
+                x[4 * p + 3] = x3 * c.z + x2 * c.w;
+                y[4 * p] = y0 * d.x - y1 * d.y;
+                y[4 * p + 1] = y1 * d.x + y0 * d.y;
+                y[4 * p + 2] = y2 * d.z - y3 * d.w;
+                y[4 * p + 3] = y3 * d.z + y2 * d.w;
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float4 c = cs[p];
+                const float x0 = x[2 * p], y0 = y[2 * p], x1 = x[2 * p + 1], y1 = y[2 * p + 1];
+                x[2 * p] = x0 * c.x - y0 * c.y;
+                y[2 * p] = y0 * c.x + x0 * c.y;
+                x[2 * p + 1] = x1 * c.z - y1 * c.w;
+                y[2 * p + 1] = y1 * c.z + x1 * c.w;
+            }
+        }
+    }
+    if (u.kind == 0) {
+        T* dst = static_cast<T*>(a.q_out) + u.row * a.q_out_stride + u.head * kDim;
+        store8(dst + u.at0, x);
+        store8(dst + u.at1, y);
+    } else if (kFp8) {
+        uint8_t* dst = static_cast<uint8_t*>(u.kind == 1 ? a.k_pages : a.v_pages) + u.row * kDim;
+        const float scale = u.kind == 1 ? a.k_scale : a.v_scale;
+        store8_fp8(dst + u.at0, x, scale);
+        store8_fp8(dst + u.at1, y, scale);
+    } else {
+        T* dst = static_cast<T*>(u.kind == 1 ? a.k_pages : a.v_pages) + u.row * kDim;
+        store8(dst + u.at0, x);
+        store8(dst + u.at1, y);
+    }
+}
+
+template <typename T, bool kFp8, int kDim, bool kAhead>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
+    extern __shared__ float2 s_turn[];  // [tokens][pairs] (cos, sin)
     const int tid = threadIdx.x;
-    const int64_t first = (int64_t)blockIdx.x * kTokens;
-    const int count = (int)min((int64_t)kTokens, a.num_tokens - first);
+    const int64_t first = (int64_t)blockIdx.x * a.tokens;
+    const int count = (int)min((int64_t)a.tokens, a.num_tokens - first);
+    const int items = (a.q_heads + 2 * a.kv_heads) * (kDim / 16);
     grid_dependents_launch();
     grid_dependency_wait();
 
+    Unit<T> u[kBatch];
+    if (kAhead)
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+            u[x] = load_unit<T, kFp8, kDim>(a, first, items, count, tid + x * kThreads);
     for (int i = tid; i < count * a.pairs; i += kThreads) {
         const int j = i / a.pairs, pair = i - j * a.pairs;
         const int axis = (pair >= a.end0 ? 1 : 0) + (pair >= a.end1 ? 1 : 0);
@@ -126,91 +236,45 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
         const long long angle = (long long)((unsigned long long)(long long)pos * rate);
         float sn, cs;
         sincospif((float)(int)(angle >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
-        s_turn[j][pair] = make_float2(cs, sn);
+        s_turn[i] = make_float2(cs, sn);
     }
     __syncthreads();
-
-    const int heads = a.q_heads + 2 * a.kv_heads;
-    const int items = heads * kUnits;
-    const int turned = a.pairs / 8;  // units with pairs; the others are copied
-    for (int i = tid; i < count * items; i += kThreads) {
-        const int j = i / items, rest = i - j * items;
-        const int head = rest / kUnits, unit = rest % kUnits;
-        const int64_t t = first + j;
-        const bool is_q = head < a.q_heads, is_k = !is_q && head < a.q_heads + a.kv_heads;
-        const int h = is_q ? head : is_k ? head - a.q_heads : head - a.q_heads - a.kv_heads;
-        int64_t row = 0;
-        if (!is_q) {
-            const int64_t slot = __ldg(a.slots + t);
-            if (slot < 0) continue;
-            if (slot >= a.slot_end) {
-                record_error(a.status, DSA_ERR_DEVICE_CHECK);
-                continue;
-            }
-            row = ((slot / kPage) * a.kv_heads + h) * kPage + slot % kPage;
-        }
-        const T* src = (is_q ? static_cast<const T*>(a.q) + t * a.q_stride
-                             : is_k ? static_cast<const T*>(a.k) + t * a.k_stride
-                                    : static_cast<const T*>(a.v) + t * a.v_stride) +
-                       h * kDim;
-        const bool turn = (is_q || is_k) && unit < turned;
-        const int at0 = turn && !a.interleaved ? unit * 8 : unit * 16;
-        const int at1 = turn && !a.interleaved ? unit * 8 + a.pairs : unit * 16 + 8;
-        float x[8], y[8];
-        load8(src + at0, x);
-        load8(src + at1, y);
-        if (turn) {
-            const float2* cs = s_turn[j] + unit * 8;
-            if (a.interleaved) {
+    if (!kAhead) {
+        for (int i = tid; i < count * items; i += kThreads)
+            finish_unit<T, kFp8, kDim>(a, load_unit<T, kFp8, kDim>(a, first, items, count, i),
+                                       s_turn);
+        return;
+    }
+    for (int i = tid; i < count * items;) {
+        i += kBatch * kThreads;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const float2 c0 = cs[p], c1 = cs[4 + p];
-                    const float x0 = x[2 * p], x1 = x[2 * p + 1], y0 = y[2 * p], y1 = y[2 * p + 1];
-                    x[2 * p] = x0 * c0.x - x1 * c0.y;
-                    x[2 * p + 1] = x1 * c0.x + x0 * c0.y;
-                    y[2 * p] = y0 * c1.x - y1 * c1.y;
-                    y[2 * p + 1] = y1 * c1.x + y0 * c1.y;
-                }
-            } else {
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const float2 c = cs[p];
-                    const float x0 = x[p], y0 = y[p];
-                    x[p] = x0 * c.x - y0 * c.y;
-                    y[p] = y0 * c.x + x0 * c.y;
-                }
-            }
-        }
-        if (is_q) {
-            T* dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * kDim;
-            store8(dst + at0, x);
-            store8(dst + at1, y);
-        } else if (kFp8) {
-            uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) + row * kDim;
-            const float scale = is_k ? a.k_scale : a.v_scale;
-            store8_fp8(dst + at0, x, scale);
-            store8_fp8(dst + at1, y, scale);
-        } else {
-            T* dst = static_cast<T*>(is_k ? a.k_pages : a.v_pages) + row * kDim;
-            store8(dst + at0, x);
-            store8(dst + at1, y);
+        for (int x = 0; x < kBatch; ++x) {
+            finish_unit<T, kFp8, kDim>(a, u[x], s_turn);
+            u[x] = load_unit<T, kFp8, kDim>(a, first, items, count, i + x * kThreads);
         }
     }
 }
 
+template <typename T, bool kFp8, int kDim>
+cudaError_t launch_units(RopeArgs a, cudaStream_t stream) {
+    const int items = (a.q_heads + 2 * a.kv_heads) * (kDim / 16);
+    const bool ahead = (int64_t)a.num_tokens * items < (1 << 20);
+    const int few = 4 * kThreads / items;
+    a.tokens = few < 1 ? 1 : few > kMaxTokens ? kMaxTokens : few;
+    if (!ahead && a.tokens < 4) a.tokens = 4;
+    const dim3 grid((unsigned)(((int64_t)a.num_tokens + a.tokens - 1) / a.tokens));
+    const size_t smem = (size_t)a.tokens * a.pairs * sizeof(float2);  // at most 16 KB
+    return launch_kernel(ahead ? rope_append_kernel<T, kFp8, kDim, true>
+                               : rope_append_kernel<T, kFp8, kDim, false>,
+                         grid, dim3(kThreads), smem, stream, true, 1, a);
+}
+
 template <typename T, bool kFp8>
 cudaError_t launch_dim(const RopeArgs& a, int head_dim, cudaStream_t stream) {
-    const dim3 grid((unsigned)(((int64_t)a.num_tokens + kTokens - 1) / kTokens));
     switch (head_dim) {
-        case 64:
-            return launch_kernel(rope_append_kernel<T, kFp8, 64>, grid, dim3(kThreads), 0, stream,
-                                 true, 1, a);
-        case 128:
-            return launch_kernel(rope_append_kernel<T, kFp8, 128>, grid, dim3(kThreads), 0, stream,
-                                 true, 1, a);
-        default:
-            return launch_kernel(rope_append_kernel<T, kFp8, 256>, grid, dim3(kThreads), 0, stream,
-                                 true, 1, a);
+        case 64: return launch_units<T, kFp8, 64>(a, stream);
+        case 128: return launch_units<T, kFp8, 128>(a, stream);
+        default: return launch_units<T, kFp8, 256>(a, stream);
     }
 }
 
