@@ -1243,19 +1243,23 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
                                  (size_t)D::kSmem, stream, true, p.cluster, tm_k, tm_v, p);
         }
     }
-    // Many short units of a few rows: a CTA to a unit, two to an SM, so that the fixed
-    // costs of one overlap the other's tiles (64 requests of up to 256 positions, 4
-    // heads of 128: 13.8 -> 7.1 us).  The longest unit alone bounds the time where the
-    // list would spread it: the sides meet at 13 to 16 pages of 32 KB, 16 to 30 of
-    // 16 KB and 25 to 35 of 8 KB, for 1 to 7 units an SM.
-    if constexpr (C::kRows == 16 && C::kDim < 256) {
-        if (!p.whole && units > sms && units < (1 << 24) &&
+    // Many short units: a CTA to a unit, two to an SM, so that the fixed costs of one
+    // overlap the other's tiles (64 requests of up to 256 positions, 4 heads of 128:
+    // 13.8 -> 7.1 us).  The longest unit alone bounds the time where the list would
+    // spread it: the sides meet at 13 to 16 pages of 32 KB, 16 to 30 of 16 KB and 25
+    // to 35 of 8 KB, for 1 to 7 units an SM.  256 dims need more registers than half
+    // an SM has for them.
+    if constexpr (C::kDim < 256) {
+        constexpr int kWM = C::kRows == 16 ? 1 : C::kRows == 32 ? 2 : 4;
+        using S = AttnCfg<C::kDim, C::kFp8, 1, kWM, kWM == 4 ? 1 : 2, kWM == 1 ? 2 : 1, true, 2>;
+        const int64_t small_tiles = ((int64_t)p.bt.max_q * p.group + S::kRows - 1) / S::kRows;
+        const int64_t small_units = small_tiles * p.bt.num_requests * p.kv_heads;
+        if (!p.whole && small_units > sms && small_units < (1 << 24) &&
             tiles * (C::kStageBytes + 8192) <= 524288) {
-            using S = AttnCfg<C::kDim, C::kFp8, 1, 1, 2, 2, true, 2>;
             p.cluster = 1;
-            p.row_tiles = (int)row_tiles;
+            p.row_tiles = (int)small_tiles;
             if ((e = prepare_kernel<S, kQBf16>()) != cudaSuccess) return e;
-            return launch_kernel(paged_attention_kernel<S, kQBf16>, dim3((unsigned)units),
+            return launch_kernel(paged_attention_kernel<S, kQBf16>, dim3((unsigned)small_units),
                                  dim3(S::kThreads), (size_t)S::kSmem, stream, true, 1, tm_k, tm_v,
                                  p);
         }
