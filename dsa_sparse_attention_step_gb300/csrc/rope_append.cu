@@ -13,11 +13,13 @@
 // Memory bound: every value is read and written once.  A thread moves units of 16
 // values (two 16-byte loads: the two halves of eight pairs, or 16 consecutive
 // values).  A CTA forms its tokens' cosines and sines, once for all heads, in shared
-// memory.  Below about a million units a CTA takes as few tokens as give its threads
-// four units each, so that they fill the GPU, with two units a thread in flight, the
-// first two during the cosines; above, four tokens and one unit at a time, which
-// leaves the registers for more CTAs (1024 tokens of 48 heads of 128: 6.9 us so, 11.9
-// with the other; 32768 tokens of 40 heads of 256: 214 and 207 us, 6.5 TB/s).
+// memory, with its first loads in flight, and then keeps two units a thread in
+// flight.  Below a million units a CTA takes as few tokens as give its threads four
+// units each, so that they fill the GPU, else at least four (1024 tokens of 48 heads
+// of 128: 5.9 us; 2053 of 80: 17.7 us).  From eight million on DRAM is busy anyway and
+// one unit a thread, which leaves registers for a fifth CTA on the SM, is the faster
+// (32768 tokens of 40 heads of 256: 206 us, 6.5 TB/s, with two 213; 4096 tokens of 48
+// such heads: 44.7 and 39.4 us).
 #include "common.cuh"
 
 namespace dsa {
@@ -25,7 +27,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 2;       // units of a thread in flight, for small calls
+constexpr int kBatch = 2;       // units of a thread in flight
 constexpr int kMaxTokens = 16;  // of a CTA
 
 struct RopeArgs {
@@ -165,12 +167,13 @@ __device__ __forceinline__ void finish_unit(const RopeArgs& a, const Unit<T>& u,
     unpack8<T>(u.a, x);
     unpack8<T>(u.b, y);
     if (u.kind != 2 && u.unit < a.pairs / 8) {
-        // two (cos, sin) pairs a load
-        const float4* cs = reinterpret_cast<const float4*>(turns + u.token * a.pairs + u.unit * 8);
+        // two (cos, sin) pairs a load, neighbouring units in neighbouring banks
+        const int units = a.pairs / 8;
+        const float4* cs = reinterpret_cast<const float4*>(turns + u.token * a.pairs) + u.unit;
         if (a.interleaved) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const float4 c = cs[p], d = cs[2 + p];
+                const float4 c = cs[p * units], d = cs[(2 + p) * units];
                 const float x0 = x[4 * p], x1 = x[4 * p + 1], x2 = x[4 * p + 2], x3 = x[4 * p + 3];
                 const float y0 = y[4 * p], y1 = y[4 * p + 1], y2 = y[4 * p + 2], y3 = y[4 * p + 3];
                 x[4 * p] = x0 * c.x - x1 * c.y;
@@ -185,7 +188,7 @@ __device__ __forceinline__ void finish_unit(const RopeArgs& a, const Unit<T>& u,
         } else {
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                const float4 c = cs[p];
+                const float4 c = cs[p * units];
                 const float x0 = x[2 * p], y0 = y[2 * p], x1 = x[2 * p + 1], y1 = y[2 * p + 1];
                 x[2 * p] = x0 * c.x - y0 * c.y;
                 y[2 * p] = y0 * c.x + x0 * c.y;
@@ -212,7 +215,8 @@ __device__ __forceinline__ void finish_unit(const RopeArgs& a, const Unit<T>& u,
 
 template <typename T, bool kFp8, int kDim, bool kAhead>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
-    extern __shared__ float2 s_turn[];  // [tokens][pairs] (cos, sin)
+    // (cos, sin) as [tokens][4][units][2]: pair 8 u + 2 p + e of a token at [p][u][e]
+    extern __shared__ float2 s_turn[];
     const int tid = threadIdx.x;
     const int64_t first = (int64_t)blockIdx.x * a.tokens;
     const int count = (int)min((int64_t)a.tokens, a.num_tokens - first);
@@ -236,7 +240,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
         const long long angle = (long long)((unsigned long long)(long long)pos * rate);
         float sn, cs;
         sincospif((float)(int)(angle >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
-        s_turn[i] = make_float2(cs, sn);
+        s_turn[j * a.pairs + (((pair >> 1 & 3) * (a.pairs >> 3) + (pair >> 3)) << 1) + (pair & 1)] =
+            make_float2(cs, sn);
     }
     __syncthreads();
     if (!kAhead) {
@@ -258,10 +263,11 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
 template <typename T, bool kFp8, int kDim>
 cudaError_t launch_units(RopeArgs a, cudaStream_t stream) {
     const int items = (a.q_heads + 2 * a.kv_heads) * (kDim / 16);
-    const bool ahead = (int64_t)a.num_tokens * items < (1 << 20);
+    const int64_t units = (int64_t)a.num_tokens * items;
+    const bool ahead = units < (1 << 23);
     const int few = 4 * kThreads / items;
     a.tokens = few < 1 ? 1 : few > kMaxTokens ? kMaxTokens : few;
-    if (!ahead && a.tokens < 4) a.tokens = 4;
+    if (units >= (1 << 20) && a.tokens < 4) a.tokens = 4;
     const dim3 grid((unsigned)(((int64_t)a.num_tokens + a.tokens - 1) / a.tokens));
     const size_t smem = (size_t)a.tokens * a.pairs * sizeof(float2);  // at most 16 KB
     return launch_kernel(ahead ? rope_append_kernel<T, kFp8, kDim, true>
