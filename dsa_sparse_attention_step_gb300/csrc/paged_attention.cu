@@ -34,6 +34,7 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
     p.group = num_q_heads / cache.num_kv_heads;
     p.inv_group = 1.0f / (float)p.group;
     p.whole = whole;
+    p.min_length = p.cluster = p.row_tiles = 0;  // set by the launch
     p.q_stride = q_stride;
     p.q = q;
     p.out = out;

@@ -5,27 +5,32 @@
 //
 // One pass over the cache with a running maximum m and sum per row (a row is
 // one query token's one head).  The G n_b rows of a request that share a KV head
-// form row tiles of 16, 32 or 64, so the cache is read once per row tile: at
-// decode (at most 64 rows) 2 G n_b / element size flop per byte, below what the
-// tensor cores need to keep up with HBM.  The kernel is bound by the reads.
+// form row tiles of 16 to 64, so the cache is read once per row tile: at decode (at
+// most 64 rows) 2 G n_b / element size flop per byte, below what the tensor cores
+// need to keep up with HBM.  The kernel is bound by the reads.
 //
 // Work is counted in key tiles (one page of one KV head against one row tile)
 // over all requests, and every CTA of a resident grid takes an equal, contiguous
 // run of that list: short and long requests share the SMs evenly without the
 // host knowing their lengths, and the copies of the next request run while the
-// last one is finished.  A (request, row tile, KV head) cut by a CTA's border
+// last one is finished.  A unit (request, row tile, KV head) cut by a CTA's border
 // leaves unnormalised pieces in the workspace, which a second kernel joins
 // (launched early, it waits for the first): piece order is fixed, so results do
-// not change from run to run.
+// not change from run to run.  Short contexts do without the list: a cluster to a
+// unit where units are few, half-size CTAs where they are many (launch_cfg).
 //
-// One warp per CTA issues the copies (TMA, 128-byte swizzled page tiles into a
-// ring of stages); each consumer warp takes 16 rows and a share of a tile's
-// tokens with a softmax of its own, so the warps meet only when a row tile is
-// done.  m16n8k16 MMAs with fp32 accumulation: at 16 rows a tcgen05 tile of 128
-// rows would be seven eighths empty, and the fragments' register layout lets P
-// go from scores to operand without leaving the registers.  FP8 keys and values
-// are lifted to f16 exactly; bf16 queries then are scaled by a power of two per
-// row, so that f16 holds them.
+// One warp or four per CTA issue the copies (TMA, 128-byte swizzled page tiles into
+// a ring of stages); each consumer warp takes 16 rows and a share of a page's
+// tokens with a softmax of its own, so the warps meet only when a unit is done.
+// m16n8k16 MMAs with fp32 accumulation: at 16 rows a tcgen05 tile of 128 rows would
+// be seven eighths empty, and the fragments' register layout lets P go from scores
+// to operand without leaving the registers.  FP8 keys and values are lifted to f16
+// exactly; bf16 queries then are scaled by a power of two per row, so that f16 holds
+// them.
+//
+// Measured: one token over 2^20 positions of 32/8 heads of 128, bf16, 592 us, 7.25
+// TB/s; 64 ragged FP8 requests, 64/8 heads, 334 us, 6.76 TB/s; five tokens to verify
+// in each of 16 requests of up to 131072, 583 us, 6.78 TB/s.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -49,7 +54,7 @@ struct AttnParams {
     int32_t kv_heads, group;
     float inv_group;
     int32_t min_length;  // least length of a CTA's run of the list
-    int32_t whole;      // every (request, row tile, KV head) by one CTA
+    int32_t whole;       // every (request, row tile, KV head) by one CTA
     // without the list: CTAs of a cluster, row tiles that a request may have
     int32_t cluster, row_tiles;
     int64_t q_stride;
@@ -69,20 +74,20 @@ struct AttnParams {
 enum { kJoinPieces, kJoinToken, kJoinRow, kJoinRows, kJoinHead, kJoinInts = 8 };
 
 // The consumer warps: kNG groups, each taking every kNG-th page of the CTA's run;
-// within a group kWM warps along the rows (kMT tiles of 16 rows each) by kWN warps
-// along the page's tokens.  8 or 12 warps (4 of each of two CTAs), as many as the accumulators' registers
-// allow: a warp's softmax is a chain of dependent instructions, and only other
-// warps fill its gaps.
-template <int kD, bool kKvFp8, int kMT_, int kWM_, int kWN_, int kNG_, bool kDirect_ = false,
+// within a group kWM warps along the rows (16 each) by kWN warps along the page's
+// tokens.  8 or 12 warps, or 4 of each of an SM's two CTAs, as many as the
+// accumulators' registers allow: a warp's softmax is a chain of dependent
+// instructions, and only other warps fill its gaps.
+template <int kD, bool kKvFp8, int kWM_, int kWN_, int kNG_, bool kDirect_ = false,
           int kCtas_ = 1>
 struct AttnCfg {
     static constexpr int kDim = kD;
     static constexpr bool kDirect = kDirect_;  // a cluster to a unit, no list
     static constexpr int kCtas = kCtas_;       // of an SM
-    using Direct = AttnCfg<kD, kKvFp8, kMT_, kWM_, kWN_, kNG_, true>;
+    using Direct = AttnCfg<kD, kKvFp8, kWM_, kWN_, kNG_, true>;
     static constexpr bool kFp8 = kKvFp8;
-    static constexpr int kMT = kMT_, kWM = kWM_, kWN = kWN_, kNG = kNG_;
-    static constexpr int kRows = 16 * kMT * kWM;
+    static constexpr int kWM = kWM_, kWN = kWN_, kNG = kNG_;
+    static constexpr int kRows = 16 * kWM;
     static constexpr int kConsumers = kWM * kWN * kNG;
     static constexpr int kTokenWarps = kWN * kNG;  // warps that share a row
     static constexpr int kThreads = 32 * (kConsumers + 4);
@@ -92,19 +97,17 @@ struct AttnCfg {
     static constexpr int kTileBytes = kPage * kRowBytes;  // keys or values of one page
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kTokens = kPage / kWN;                       // of a page, per warp
-    static constexpr int kSub =
-        kD == 256 || kTokens < 32 ? 16 : 32;  // softmax step
+    static constexpr int kSub = kD == 256 || kTokens < 32 ? 16 : 32;  // softmax step
     static constexpr int kPairs = kRowBytes / 32;  // pairs of 16-byte chunks in a row
     static constexpr int kTilesD = kD / 8;         // accumulator tiles along the dims
     // Q fragments stay in registers where they fit beside the accumulators and the
     // 32-token softmax step, which is worth more (verification of five tokens: 622
     // us with both in registers and 16-token steps, 587 so)
-    static constexpr bool kQSmem = kMT > 1 || kD == 256 || (kD == 128 && kConsumers == 12);
+    static constexpr bool kQSmem = kD == 256 || (kD == 128 && kConsumers == 12);
     static constexpr int kQBytes = kRows * kD * 2;
     // The join of the warps takes so many dims at a time; 64 keep all threads busy
     // where the buffer then takes no stage that is needed.
-    static constexpr int kMergeDims =
-        kRows == 16 && (kD < 256 || kKvFp8) ? 64 : 32;
+    static constexpr int kMergeDims = kRows == 16 && (kD < 256 || kKvFp8) ? 64 : 32;
     static constexpr int kMergeLd = kMergeDims + 8;  // floats; keeps fragment stores apart
     static constexpr int kMergeBytes = kTokenWarps * kRows * kMergeLd * 4;
     static constexpr int kMlBytes = kTokenWarps * kRows * 8 + kRows * 4;
@@ -139,7 +142,8 @@ struct AttnCfg {
     // The launch gives every thread kLaunchRegs registers (launch bounds); the copying
     // warpgroup then hands most of its share to the consumers.
     static constexpr int kLaunchRegs = 65536 / (kThreads * kCtas) / 8 * 8;
-    static constexpr int kProducerRegs = kConsumers == 12 ? 56 : kD == 256 || kConsumers == 4 ? 40 : 72;
+    static constexpr int kProducerRegs =
+        kConsumers == 12 ? 56 : kD == 256 || kConsumers == 4 ? 40 : 72;
     static constexpr int kConsumerRegs = kConsumers == 12 ? 152 : kD == 256 ? 232 : 208;
     static_assert(128 * kProducerRegs + 32 * kConsumers * kConsumerRegs <= kThreads * kLaunchRegs,
                   "setmaxnreg.inc would wait forever");
@@ -205,26 +209,30 @@ struct Cursor {
     __device__ __forceinline__ void look_ahead(const AttnParams& p) {
         ahead = raw_request(p, min(b + 1, p.bt.num_requests - 1));
     }
-    __device__ __forceinline__ void next(const AttnParams& p) {
-        if (++h < p.kv_heads) return;
+    // False at the end of the list.
+    __device__ __forceinline__ bool next(const AttnParams& p) {
+        if (++h < p.kv_heads) return true;
         h = 0;
         if ((rt + 1) * kRows < r.rows) {
             ++rt;
         } else {
             rt = 0;
             do {
-                if (++b >= p.bt.num_requests) return;  // the end of the list
+                if (++b >= p.bt.num_requests) return false;
                 r = request_of(p, ahead, nullptr);
                 look_ahead(p);
             } while (r.rows == 0);
         }
         tiles = tiles_of<kRows>(p, r, rt);
+        return true;
     }
 };
 
 // In the list a unit is as long as its tiles and kUnitCost more in front of them,
 // for what a unit costs a CTA besides its tiles.  Positions are 32-bit: the host
-// refuses longer lists.
+// refuses longer lists.  (Offsets that run back and forth could still make one, and
+// a wrong cut of it; every walk therefore ends with the last request, and pieces
+// with the last CTA.)
 template <int kRows>
 struct Share {
     uint32_t begin, end, per;  // this CTA's run of the list
@@ -267,7 +275,7 @@ struct Walk {
     __device__ __forceinline__ void advance(const AttnParams& p) {
         pos += C::kUnitCost + u.cost() - offset;
         offset = 0;
-        if (pos < end) u.next(p);
+        if (pos < end && !u.next(p)) pos = end;
     }
     __device__ __forceinline__ void next(const AttnParams& p) {
         if (C::kDirect) {
@@ -324,6 +332,7 @@ __device__ void find_share(const AttnParams& p, Share<C::kRows>* s, uint32_t* s_
     }
     const uint32_t warp_sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) s_warp[warp] = warp_sum;
+    if (tid == 0) s->begin = s->end = 0;  // for a CTA without work
     __syncthreads();
     uint32_t total = 0, before = 0;
 #pragma unroll
@@ -334,11 +343,6 @@ __device__ void find_share(const AttnParams& p, Share<C::kRows>* s, uint32_t* s_
     const uint32_t per = max((total + gridDim.x - 1) / gridDim.x, (uint32_t)p.min_length);
     const uint32_t begin = (uint32_t)min((unsigned long long)per * blockIdx.x,
                                          (unsigned long long)total);
-    if (tid == 0) {
-        s->begin = begin;
-        s->end = min(total, begin + per);
-        s->per = per;
-    }
     if (begin < total && before <= begin && begin < before + warp_sum) {
         uint32_t upto = sum;
 #pragma unroll
@@ -348,7 +352,7 @@ __device__ void find_share(const AttnParams& p, Share<C::kRows>* s, uint32_t* s_
         }
         before += upto - sum;
         if (before <= begin && begin < before + sum) {
-            for (int b = first;; ++b) {
+            for (int b = first; b < min(n, first + each); ++b) {
                 if (each > 1) r = request_of(p, raw_request(p, b), nullptr);
                 int rt = 0;
                 for (; rt * C::kRows < r.rows; ++rt) {
@@ -356,6 +360,9 @@ __device__ void find_share(const AttnParams& p, Share<C::kRows>* s, uint32_t* s_
                     const uint32_t length = max(1, tiles) + C::kUnitCost;
                     if (begin < before + length * p.kv_heads) {
                         const uint32_t h = (begin - before) / length;
+                        s->begin = begin;
+                        s->end = min(total, begin + per);
+                        s->per = per;
                         s->offset = begin - before - h * length;
                         s->at.b = b;
                         s->at.rt = rt;
@@ -487,7 +494,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
     // operands of the MMAs: the cache's own type, or f16 lifted from FP8
     constexpr bool kBf16 = kQBf16 && !C::kFp8;
-    constexpr int kD = C::kDim, kMT = C::kMT;
+    constexpr int kD = C::kDim;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t s_full[C::kFull], s_empty[C::kStages];
     __shared__ int s_valid[C::kStages];
@@ -589,6 +596,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // first piece of a row tile that other CTAs finish
                 int32_t* j = p.joins + blockIdx.x * kJoinInts;
                 pieces = 1 + (int)((u.cost() - walk.count + s_share.per - 1) / s_share.per);
+                pieces = min(pieces, (int)(gridDim.x - blockIdx.x));
                 j[kJoinToken] = u.r.q0;
                 j[kJoinRow] = u.rt * C::kRows;
                 j[kJoinRows] = min(C::kRows, u.r.rows - u.rt * C::kRows);
@@ -597,7 +605,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             walk = v;
             ahead = ahead_v;
         }
-        if (me == 0 && lane == 0 && !C::kDirect) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
+        if (me == 0 && lane == 0 && !C::kDirect)
+            p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
         if (lane == 0 && *abort_flag) {
             // an unwinding CTA must not exit under copies in flight
             for (int i = n - C::kProducers; i >= 0 && i > n - C::kProducers - C::kStages;
@@ -695,10 +704,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 for (int i = 0; i < kWords; ++i)
                     top = max(top, max(qw[x][i] & 0x7fffu, (qw[x][i] >> 16) & 0x7fffu));
                 top = __reduce_max_sync(0xffffffffu, top);
-                // biased exponent; zero, infinite and NaN rows stay unscaled
+                // biased exponent; infinite and NaN rows stay unscaled, and rows below
+                // 2^-63, whose scores are 0 in fp32 next to any other
                 const uint32_t e = top >> 7;
                 float up = 1.f;
-                if (e != 0 && e < 254) {
+                if (e >= 64 && e < 254) {
                     up = __uint_as_float((254 - e) << 23);
                     factor *= __uint_as_float(e << 23);
                 }
@@ -723,12 +733,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (v.pos < v.end) load_q(v.u);
         }
         consumer_sync<32 * C::kConsumers>();
-        float f[kMT][2];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-            f[mt][0] = s_factor[16 * (wm * kMT + mt) + g];
-            f[mt][1] = s_factor[16 * (wm * kMT + mt) + g + 8];
-        }
+        const float f[2] = {s_factor[16 * wm + g], s_factor[16 * wm + g + 8]};
         uint32_t qf[C::kQSmem ? 1 : kD / 16][4];
         if (!C::kQSmem) {
 #pragma unroll
@@ -741,27 +746,19 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
         }
 
-        // this thread's rows: g and g + 8 of each 16; what they see
-        int vis[kMT][2];
+        // what this thread's rows, g and g + 8 of the warp's 16, see
+        int vis[2];
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = tile_row + 16 * (wm * kMT + mt) + g + 8 * x;
-                vis[mt][x] = r < u.r.rows ? u.r.seq - u.r.nb + token_of(p, r) + 1 : 0;
-            }
-        const int vis_first = u.r.seq - u.r.nb + token_of(p, tile_row + 16 * wm * kMT) + 1;
-
-        float o[kMT][C::kTilesD][4];
-        float m[kMT][2], l[kMT][2];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-            for (int i = 0; i < C::kTilesD; ++i)
-                o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.f;
+        for (int x = 0; x < 2; ++x) {
+            const int r = tile_row + 16 * wm + g + 8 * x;
+            vis[x] = r < u.r.rows ? u.r.seq - u.r.nb + token_of(p, r) + 1 : 0;
         }
+        const int vis_first = u.r.seq - u.r.nb + token_of(p, tile_row + 16 * wm) + 1;
+
+        float o[C::kTilesD][4];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < C::kTilesD; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
         const int last = min(u.tiles, tile + walk.count);
         // this group's pages: those whose number in the run is grp modulo kNG
@@ -792,124 +789,106 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                 for (int sub = 0; sub < C::kTokens; sub += C::kSub) {
                     constexpr int kNt = C::kSub / 8;
-                    float s[kMT][kNt][4];
+                    float s[kNt][4];
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                        for (int i = 0; i < kNt; ++i)
-                            s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
+                    for (int i = 0; i < kNt; ++i)
+                        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
                     constexpr int kSteps = C::kFp8 ? 2 : 1;  // MMA steps in a chunk pair
 #pragma unroll
                     for (int j = 0; j < C::kPairs; ++j) {
-                        uint32_t qa[kMT][kSteps][4];
+                        uint32_t qa[kSteps][4];
 #pragma unroll
-                        for (int mt = 0; mt < kMT; ++mt)
+                        for (int x = 0; x < kSteps; ++x) {
+                            if (C::kQSmem) {
+                                const uint4 w =
+                                    s_q[(wm * (kD / 16) + kSteps * j + x) * 32 + lane];
+                                qa[x][0] = w.x;
+                                qa[x][1] = w.y;
+                                qa[x][2] = w.z;
+                                qa[x][3] = w.w;
+                            } else {
 #pragma unroll
-                            for (int x = 0; x < kSteps; ++x) {
-                                if (C::kQSmem) {
-                                    const uint4 w =
-                                        s_q[((wm * kMT + mt) * (kD / 16) + kSteps * j + x) * 32 + lane];
-                                    qa[mt][x][0] = w.x;
-                                    qa[mt][x][1] = w.y;
-                                    qa[mt][x][2] = w.z;
-                                    qa[mt][x][3] = w.w;
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        qa[mt][x][i] = qf[C::kQSmem ? 0 : kSteps * j + x][i];
-                                }
+                                for (int i = 0; i < 4; ++i)
+                                    qa[x][i] = qf[C::kQSmem ? 0 : kSteps * j + x][i];
                             }
+                        }
 #pragma unroll
                         for (int i = 0; i < C::kSub / 16; ++i) {
                             uint32_t k[4];
-                            ldmatrix4(k, stage + k_at[j % kPairsBox] + pair_offset(j, sub + 16 * i));
+                            ldmatrix4(k,
+                                      stage + k_at[j % kPairsBox] + pair_offset(j, sub + 16 * i));
                             if (C::kFp8) {
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
                                     uint32_t k0, k1, k2, k3;
                                     lift(k[x], k0, k1);
                                     lift(k[2 + x], k2, k3);
-#pragma unroll
-                                    for (int mt = 0; mt < kMT; ++mt) {
-                                        mma16816<false>(s[mt][2 * i], qa[mt][x % kSteps], k0, k1);
-                                        mma16816<false>(s[mt][2 * i + 1], qa[mt][x % kSteps], k2, k3);
-                                    }
+                                    mma16816<false>(s[2 * i], qa[x % kSteps], k0, k1);
+                                    mma16816<false>(s[2 * i + 1], qa[x % kSteps], k2, k3);
                                 }
                             } else {
-#pragma unroll
-                                for (int mt = 0; mt < kMT; ++mt) {
-                                    mma16816<kBf16>(s[mt][2 * i], qa[mt][0], k[0], k[1]);
-                                    mma16816<kBf16>(s[mt][2 * i + 1], qa[mt][0], k[2], k[3]);
-                                }
+                                mma16816<kBf16>(s[2 * i], qa[0], k[0], k[1]);
+                                mma16816<kBf16>(s[2 * i + 1], qa[0], k[2], k[3]);
                             }
                         }
                     }
                     if (t * kPage + kPage > vis_first) {
 #pragma unroll
-                        for (int mt = 0; mt < kMT; ++mt)
+                        for (int i = 0; i < kNt; ++i)
 #pragma unroll
-                            for (int i = 0; i < kNt; ++i)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    if (first + sub + 8 * i + 2 * c + (x & 1) >= vis[mt][x >> 1])
-                                        s[mt][i][x] = -INFINITY;
+                            for (int x = 0; x < 4; ++x)
+                                if (first + sub + 8 * i + 2 * c + (x & 1) >= vis[x >> 1])
+                                    s[i][x] = -INFINITY;
                     }
-                    float top[kMT][2];
+                    float top[2];
                     bool grew = false;
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt)
+                    for (int x = 0; x < 2; ++x) {
+                        float y = -INFINITY;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float y = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < kNt; ++i)
-                                y = fmaxf(y, fmaxf(s[mt][i][2 * x], s[mt][i][2 * x + 1]));
-                            top[mt][x] = fmaxf(m[mt][x], quad_max(y) * f[mt][x]);
-                            grew |= top[mt][x] > m[mt][x];
-                        }
+                        for (int i = 0; i < kNt; ++i)
+                            y = fmaxf(y, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
+                        top[x] = fmaxf(m[x], quad_max(y) * f[x]);
+                        grew |= top[x] > m[x];
+                    }
                     if (__any_sync(0xffffffffu, grew)) {
+                        const float a0 = ex2(m[0] - base_of(top[0]));
+                        const float a1 = ex2(m[1] - base_of(top[1]));
+                        l[0] *= a0;
+                        l[1] *= a1;
 #pragma unroll
-                        for (int mt = 0; mt < kMT; ++mt) {
-                            const float a0 = ex2(m[mt][0] - base_of(top[mt][0]));
-                            const float a1 = ex2(m[mt][1] - base_of(top[mt][1]));
-                            l[mt][0] *= a0;
-                            l[mt][1] *= a1;
-#pragma unroll
-                            for (int i = 0; i < C::kTilesD; ++i) {
-                                o[mt][i][0] *= a0;
-                                o[mt][i][1] *= a0;
-                                o[mt][i][2] *= a1;
-                                o[mt][i][3] *= a1;
-                            }
-                            m[mt][0] = top[mt][0];
-                            m[mt][1] = top[mt][1];
+                        for (int i = 0; i < C::kTilesD; ++i) {
+                            o[i][0] *= a0;
+                            o[i][1] *= a0;
+                            o[i][2] *= a1;
+                            o[i][3] *= a1;
                         }
+                        m[0] = top[0];
+                        m[1] = top[1];
                     }
                     // P rounded to the operand type (the sums are of the unrounded
                     // values): half a step per probability, which averages out as the
                     // output's own rounding does
-                    uint32_t pf[kMT][C::kSub / 16][4];
+                    uint32_t pf[C::kSub / 16][4];
+                    const float b0 = base_of(m[0]), b1 = base_of(m[1]);
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) {
-                        const float b0 = base_of(m[mt][0]), b1 = base_of(m[mt][1]);
-#pragma unroll
-                        for (int i = 0; i < kNt; ++i) {
-                            const float p0 = ex2(fmaf(s[mt][i][0], f[mt][0], -b0));
-                            const float p1 = ex2(fmaf(s[mt][i][1], f[mt][0], -b0));
-                            const float p2 = ex2(fmaf(s[mt][i][2], f[mt][1], -b1));
-                            const float p3 = ex2(fmaf(s[mt][i][3], f[mt][1], -b1));
-                            l[mt][0] += p0 + p1;
-                            l[mt][1] += p2 + p3;
-                            pf[mt][i / 2][2 * (i & 1)] = pack2<kBf16>(p0, p1);
-                            pf[mt][i / 2][2 * (i & 1) + 1] = pack2<kBf16>(p2, p3);
-                        }
+                    for (int i = 0; i < kNt; ++i) {
+                        const float p0 = ex2(fmaf(s[i][0], f[0], -b0));
+                        const float p1 = ex2(fmaf(s[i][1], f[0], -b0));
+                        const float p2 = ex2(fmaf(s[i][2], f[1], -b1));
+                        const float p3 = ex2(fmaf(s[i][3], f[1], -b1));
+                        l[0] += p0 + p1;
+                        l[1] += p2 + p3;
+                        pf[i / 2][2 * (i & 1)] = pack2<kBf16>(p0, p1);
+                        pf[i / 2][2 * (i & 1) + 1] = pack2<kBf16>(p2, p3);
                     }
 #pragma unroll
                     for (int i = 0; i < C::kSub / 16; ++i) {
 #pragma unroll
                         for (int j = 0; j < C::kPairs; ++j) {
                             uint32_t v[4];
-                            ldmatrix4_t(v, stage + v_at[j % kPairsBox] + pair_offset(j, sub + 16 * i));
+                            ldmatrix4_t(v,
+                                        stage + v_at[j % kPairsBox] + pair_offset(j, sub + 16 * i));
                             if (C::kFp8) {
                                 // each register: two tokens by two dims; split by dim
 #pragma unroll
@@ -918,21 +897,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                     lift(__byte_perm(v[2 * x], 0, 0x3120), v0, v2);
                                     lift(__byte_perm(v[2 * x + 1], 0, 0x3120), v1, v3);
                                     constexpr int kStep = C::kFp8 ? 4 : 2;
-#pragma unroll
-                                    for (int mt = 0; mt < kMT; ++mt) {
-                                        mma16816<false>(o[mt][kStep * j + (C::kFp8 ? 2 * x : 0)],
-                                                        pf[mt][i], v0, v1);
-                                        mma16816<false>(o[mt][kStep * j + (C::kFp8 ? 2 * x : 0) + 1],
-                                                        pf[mt][i], v2, v3);
-                                    }
+                                    constexpr int kHalf = C::kFp8 ? 2 : 0;
+                                    mma16816<false>(o[kStep * j + kHalf * x], pf[i], v0, v1);
+                                    mma16816<false>(o[kStep * j + kHalf * x + 1], pf[i], v2, v3);
                                 }
                             } else {
                                 constexpr int kStep = C::kFp8 ? 0 : 2;
-#pragma unroll
-                                for (int mt = 0; mt < kMT; ++mt) {
-                                    mma16816<kBf16>(o[mt][kStep * j], pf[mt][i], v[0], v[1]);
-                                    mma16816<kBf16>(o[mt][kStep * j + 1], pf[mt][i], v[2], v[3]);
-                                }
+                                mma16816<kBf16>(o[kStep * j], pf[i], v[0], v[1]);
+                                mma16816<kBf16>(o[kStep * j + 1], pf[i], v[2], v[3]);
                             }
                         }
                     }
@@ -947,15 +919,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         // each thread adds four dims of a row over the warps, weighted by what their
         // maxima lack to the common one.  (The next unit's barriers keep its writes
         // from overtaking the last pass's reads.)
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-            const int r = 16 * (wm * kMT + mt) + g;
-            l[mt][0] = quad_sum(l[mt][0]);
-            l[mt][1] = quad_sum(l[mt][1]);
-            if (c == 0) {
-                s_ml[tw * C::kRows + r] = make_float2(m[mt][0], l[mt][0]);
-                s_ml[tw * C::kRows + r + 8] = make_float2(m[mt][1], l[mt][1]);
-            }
+        const int r = 16 * wm + g;
+        l[0] = quad_sum(l[0]);
+        l[1] = quad_sum(l[1]);
+        if (c == 0) {
+            s_ml[tw * C::kRows + r] = make_float2(m[0], l[0]);
+            s_ml[tw * C::kRows + r + 8] = make_float2(m[1], l[1]);
         }
         const bool complete = walk.complete(p);
         // a cluster's pieces stay in the ring, which its only unit is done with
@@ -963,7 +932,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         float2* piece_ml = reinterpret_cast<float2*>(piece_o + C::kRows * kD);
         const int rows = min(C::kRows, u.r.rows - tile_row);
         constexpr int kQuads = C::kMergeDims / 4;
-        constexpr int kItems = (C::kRows * kQuads + 32 * C::kConsumers - 1) / (32 * C::kConsumers);  // rows of a thread
+        constexpr int kThreads = 32 * C::kConsumers;
+        constexpr int kItems = (C::kRows * kQuads + kThreads - 1) / kThreads;  // rows of a thread
         const int quad = tid % kQuads * 4;
         float weight[kItems][C::kTokenWarps];
         int64_t at[kItems];  // output row, or row of the piece
@@ -972,31 +942,28 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int d0 = 0; d0 < kD; d0 += C::kMergeDims) {
             if (d0 > 0) consumer_sync<32 * C::kConsumers>();  // the last pass has been read
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int x = 0; x < 2; ++x) {
+                float* dst = s_merge + (tw * C::kRows + 16 * wm + g + 8 * x) * C::kMergeLd;
+                constexpr int kPer = C::kMergeDims / 8;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float* dst = s_merge + (tw * C::kRows + 16 * (wm * kMT + mt) + g + 8 * x) *
-                                              C::kMergeLd;
-                    constexpr int kPer = C::kMergeDims / 8;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const float(&e)[4] = o[mt][d0 / 8 + i];
-                        if (C::kFp8) {  // tiles of even and odd dims in turn
-                            if (i % 2 == 0) {
-                                const float(&q)[4] = o[mt][d0 / 8 + (C::kFp8 ? i + 1 : 0)];
-                                *reinterpret_cast<float4*>(dst + 8 * i + 4 * c) = make_float4(
-                                    e[2 * x], q[2 * x], e[2 * x + 1], q[2 * x + 1]);
-                            }
-                        } else {
-                            *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) =
-                                make_float2(e[2 * x], e[2 * x + 1]);
+                for (int i = 0; i < kPer; ++i) {
+                    const float(&e)[4] = o[d0 / 8 + i];
+                    if (C::kFp8) {  // tiles of even and odd dims in turn
+                        if (i % 2 == 0) {
+                            const float(&q)[4] = o[d0 / 8 + (C::kFp8 ? i + 1 : 0)];
+                            *reinterpret_cast<float4*>(dst + 8 * i + 4 * c) = make_float4(
+                                e[2 * x], q[2 * x], e[2 * x + 1], q[2 * x + 1]);
                         }
+                    } else {
+                        *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) =
+                            make_float2(e[2 * x], e[2 * x + 1]);
                     }
                 }
+            }
             consumer_sync<32 * C::kConsumers>();
 #pragma unroll
             for (int x = 0; x < kItems; ++x) {
-                const int r = (tid + 32 * C::kConsumers * x) / kQuads;
+                const int r = (tid + kThreads * x) / kQuads;
                 if (r >= rows) continue;
                 if (d0 == 0) {
                     float top = -INFINITY, total = 0.f;
@@ -1251,7 +1218,7 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
     // an SM has for them.
     if constexpr (C::kDim < 256) {
         constexpr int kWM = C::kRows == 16 ? 1 : C::kRows == 32 ? 2 : 4;
-        using S = AttnCfg<C::kDim, C::kFp8, 1, kWM, kWM == 4 ? 1 : 2, kWM == 1 ? 2 : 1, true, 2>;
+        using S = AttnCfg<C::kDim, C::kFp8, kWM, kWM == 4 ? 1 : 2, kWM == 1 ? 2 : 1, true, 2>;
         const int64_t small_tiles = ((int64_t)p.bt.max_q * p.group + S::kRows - 1) / S::kRows;
         const int64_t small_units = small_tiles * p.bt.num_requests * p.kv_heads;
         if (!p.whole && small_units > sms && small_units < (1 << 24) &&
@@ -1288,18 +1255,18 @@ cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* lau
     // has 32 and sixteen
     switch (row_tile((int64_t)p.bt.max_q * p.group, p.whole != 0)) {
         case 16:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, 1, 2, 4>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 1, 2, 4>, kQBf16>(
                 p, cache, launches, stream);
         case 32:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, 2, 2, kD == 256 ? 2 : 3>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 2, 2, kD == 256 ? 2 : 3>, kQBf16>(
                 p, cache, launches, stream);
         case 48:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, kD == 256 ? 4 : 3,
+            return launch_cfg<AttnCfg<kD, kFp8, kD == 256 ? 4 : 3,
                                       kD == 256 || (kD == 128 && !kFp8) ? 2 : 1,
                                       kD == 256 ? 1 : kD == 128 && !kFp8 ? 2 : 4>,
                               kQBf16>(p, cache, launches, stream);
         default:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, 4, kD == 256 ? 2 : 1, kD == 256 ? 1 : 3>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 4, kD == 256 ? 2 : 1, kD == 256 ? 1 : 3>, kQBf16>(
                 p, cache, launches, stream);
     }
 }

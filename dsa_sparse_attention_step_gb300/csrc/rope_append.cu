@@ -244,19 +244,19 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
             make_float2(cs, sn);
     }
     __syncthreads();
-    if (!kAhead) {
+    if constexpr (kAhead) {
+        for (int i = tid; i < count * items;) {
+            i += kBatch * kThreads;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                finish_unit<T, kFp8, kDim>(a, u[x], s_turn);
+                u[x] = load_unit<T, kFp8, kDim>(a, first, items, count, i + x * kThreads);
+            }
+        }
+    } else {
         for (int i = tid; i < count * items; i += kThreads)
             finish_unit<T, kFp8, kDim>(a, load_unit<T, kFp8, kDim>(a, first, items, count, i),
                                        s_turn);
-        return;
-    }
-    for (int i = tid; i < count * items;) {
-        i += kBatch * kThreads;
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            finish_unit<T, kFp8, kDim>(a, u[x], s_turn);
-            u[x] = load_unit<T, kFp8, kDim>(a, first, items, count, i + x * kThreads);
-        }
     }
 }
 

@@ -212,6 +212,18 @@ def test_requests_that_contradict_the_host_sizes_are_reported_and_not_written():
     assert torch.isnan(out[2]).all() and torch.equal(out[:2], ok[:2])
 
 
+@pytest.mark.parametrize("requests", [6, 400])
+def test_offsets_that_run_back_and_forth_are_reported(requests):
+    """Every second request ends before it begins; the others share their rows.
+    What the rows then hold is anybody's, but nothing else is touched."""
+    c = Case([200] * requests, [0] * requests, 4, 2, 64, BF16, seed=20)
+    c.new = [3] + [0] * (requests - 1)
+    c.offsets = [0] + [3, 0] * (requests // 2)
+    c.q = torch.randn(3, 4, 64, device=DEV).to(BF16)
+    out, lse = c.run(status=DEVICE_CHECK)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
 def test_queries_as_a_slice_of_a_projection():
     c = Case([130, 700], [2, 1], 8, 2, 128, BF16, seed=11)
     wide = torch.full((3, 12, 128), NAN, dtype=BF16, device=DEV)
