@@ -1218,7 +1218,11 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
     // an SM has for them.
     if constexpr (C::kDim < 256) {
         constexpr int kWM = C::kRows == 16 ? 1 : C::kRows == 32 ? 2 : 4;
-        using S = AttnCfg<C::kDim, C::kFp8, kWM, kWM == 4 ? 1 : 2, kWM == 1 ? 2 : 1, true, 2>;
+        // 16 rows: four warps to a page for 128 16-bit dims (5.5 -> 5.2 us for the
+        // shortest), else two groups of two (64 FP8 requests of 500: 9.2 us, with four
+        // 10.9)
+        constexpr int kWN = kWM == 1 && (C::kDim == 64 || C::kFp8) ? 2 : 4 / kWM;
+        using S = AttnCfg<C::kDim, C::kFp8, kWM, kWN, 4 / (kWM * kWN), true, 2>;
         const int64_t small_tiles = ((int64_t)p.bt.max_q * p.group + S::kRows - 1) / S::kRows;
         const int64_t small_units = small_tiles * p.bt.num_requests * p.kv_heads;
         if (!p.whole && small_units > sms && small_units < (1 << 24) &&
@@ -1251,11 +1255,14 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
 template <int kD, bool kFp8, bool kQBf16>
 cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* launches,
                         cudaStream_t stream) {
-    // D = 256 has 128 accumulators a thread for 16 rows and so eight warps, D = 64
-    // has 32 and sixteen
+    // D = 256 has 128 accumulators a thread for 16 rows and so eight warps.  At 16 rows
+    // four warps to a page halve its latency where their 16-token steps are enough to
+    // keep up (one wide FP8 head: 38.4 -> 35.3 us); 64 dims and FP8 need the longer
+    // steps of two (64 ragged FP8 requests: 331 us, with four 381).
+    constexpr bool kFour = kD == 256 || (kD == 128 && !kFp8);
     switch (row_tile((int64_t)p.bt.max_q * p.group, p.whole != 0)) {
         case 16:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, 2, 4>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 1, kFour ? 4 : 2, kFour ? 2 : 4>, kQBf16>(
                 p, cache, launches, stream);
         case 32:
             return launch_cfg<AttnCfg<kD, kFp8, 2, 2, kD == 256 ? 2 : 3>, kQBf16>(

@@ -177,6 +177,17 @@ def test_scores_far_apart_and_equal():
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("kv", [BF16, FP8])
+def test_a_row_of_nan_stays_alone(kv):
+    c = Case([300, 90], [3, 1], 8, 2, 128, BF16, kv, seed=21)
+    want, want_lse = c.run()
+    c.q[1, 2, 5] = NAN
+    out, lse = c.run()
+    assert torch.isnan(out[1, 2]).all() and torch.isnan(lse[1, 2])
+    out[1, 2], lse[1, 2] = want[1, 2], want_lse[1, 2]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_queries_of_extreme_size_over_fp8():
     """bf16 queries beyond f16's range, and far below it."""
     c = Case([600, 601, 602], [1, 1, 1], 4, 2, 64, BF16, FP8, seed=7)
