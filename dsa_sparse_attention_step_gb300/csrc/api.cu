@@ -64,7 +64,8 @@ size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim);
 cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
                                    float sm_scale, void* out, float* lse, void* ws, bool whole,
-                                   int32_t* status, int* launches, cudaStream_t stream);
+                                   bool wait_test, int32_t* status, int* launches,
+                                   cudaStream_t stream);
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int32_t> g_batch_invariant{0};  // dsa_set_batch_invariant
@@ -497,10 +498,11 @@ size_t dsa_paged_attention_workspace_size(const dsa_batch* batch, const dsa_kv_c
         (int64_t)batch->max_q_per_request * (num_q_heads / cache->num_kv_heads), cache->head_dim);
 }
 
-dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache,
-                               dsa_float_format format, int32_t num_q_heads, const void* q,
-                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
-                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream) {
+static dsa_status paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache,
+                                  dsa_float_format format, int32_t num_q_heads, const void* q,
+                                  int64_t q_stride, float sm_scale, void* out, float* lse,
+                                  void* ws, size_t ws_bytes, bool wait_test, int32_t* dev_status,
+                                  dsa_stream_t stream) {
     dsa_status st = check_batch(batch, true);
     if (st != DSA_OK) return st;
     st = check_kv_cache(cache, format);
@@ -523,10 +525,27 @@ dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache
     int launches = 0;
     const dsa_status rc = cuda_status(
         launch_paged_attention(to_args(batch), *cache, (int)format, num_q_heads, q, q_stride,
-                               sm_scale, out, lse, ws, whole, dev_status, &launches,
+                               sm_scale, out, lse, ws, whole, wait_test, dev_status, &launches,
                                (cudaStream_t)stream));
     g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
     return rc;
+}
+
+dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache,
+                               dsa_float_format format, int32_t num_q_heads, const void* q,
+                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream) {
+    return paged_attention(batch, cache, format, num_q_heads, q, q_stride, sm_scale, out, lse, ws,
+                           ws_bytes, false, dev_status, stream);
+}
+
+dsa_status dsa_test_paged_attention_wait_timeout(const dsa_batch* batch, const dsa_kv_cache* cache,
+                                                 dsa_float_format format, int32_t num_q_heads,
+                                                 const void* q, int64_t q_stride, float sm_scale,
+                                                 void* out, float* lse, void* ws, size_t ws_bytes,
+                                                 int32_t* dev_status, dsa_stream_t stream) {
+    return paged_attention(batch, cache, format, num_q_heads, q, q_stride, sm_scale, out, lse, ws,
+                           ws_bytes, true, dev_status, stream);
 }
 
 }  // extern "C"

@@ -27,13 +27,15 @@ size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim) {
 cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
                                    float sm_scale, void* out, float* lse, void* ws, bool whole,
-                                   int32_t* status, int* launches, cudaStream_t stream) {
+                                   bool wait_test, int32_t* status, int* launches,
+                                   cudaStream_t stream) {
     AttnParams p;
     p.bt = bt;
     p.kv_heads = cache.num_kv_heads;
     p.group = num_q_heads / cache.num_kv_heads;
     p.inv_group = 1.0f / (float)p.group;
     p.whole = whole;
+    p.withhold = wait_test;
     p.min_length = p.cluster = p.row_tiles = 0;  // set by the launch
     p.q_stride = q_stride;
     p.q = q;

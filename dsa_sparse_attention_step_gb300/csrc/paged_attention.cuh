@@ -57,6 +57,7 @@ struct AttnParams {
     int32_t whole;       // every (request, row tile, KV head) by one CTA
     // without the list: CTAs of a cluster, row tiles that a request may have
     int32_t cluster, row_tiles;
+    int32_t withhold;  // test only: the first page's copy is not issued
     int64_t q_stride;
     const void* q;
     void* out;
@@ -566,7 +567,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (lane == 0 && ok && (ok = mbar_wait(&s_empty[st], parity, abort_flag))) {
                     const bool valid = page >= 0 && page < p.bt.num_pages;
                     s_valid[st] = valid;
-                    if (valid) {
+                    if (p.withhold && n == 0) {
+                        // nobody will arrive on this page's barrier
+                    } else if (valid) {
                         mbar_arrive_expect_tx(&s_full[fb], C::kStageBytes);
                         uint8_t* dst = ring + st * C::kStageBytes;
                         const int z = page * p.kv_heads + u.h;

@@ -28,6 +28,18 @@ dsa_status dsa_test_sparse_mla_wait_timeout(const dsa_batch* batch, const uint16
                                            uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                                            int32_t* dev_status, dsa_stream_t stream);
 
+/* dsa_paged_attention with every CTA's first page withheld: no copy is issued and
+ * nothing arrives on its barrier.  The wait for it runs out (2^30 cycles, about half
+ * a second), the CTAs unwind (no copy left in flight) and store DSA_ERR_TIMEOUT into
+ * *dev_status; the contents of out and lse are then unspecified.  Arguments, checks
+ * and host-side return values are those of dsa_paged_attention; the GPU context
+ * stays usable. */
+dsa_status dsa_test_paged_attention_wait_timeout(const dsa_batch* batch, const dsa_kv_cache* cache,
+                                                 dsa_float_format format, int32_t num_q_heads,
+                                                 const void* q, int64_t q_stride, float sm_scale,
+                                                 void* out, float* lse, void* ws, size_t ws_bytes,
+                                                 int32_t* dev_status, dsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

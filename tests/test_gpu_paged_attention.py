@@ -19,7 +19,7 @@ from paged_helpers import DEV, PAGE, attention_reference, ceil_pages
 
 pytestmark = pytest.mark.gpu
 
-DEVICE_CHECK, INVALID, UNSUPPORTED, WORKSPACE = 5, 1, 2, 3
+DEVICE_CHECK, TIMEOUT = 5, 6
 BF16, F16, FP8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
 NAN = float("nan")
 
@@ -327,6 +327,24 @@ def test_pool_offsets_beyond_32_bits():
     low = Case([1000], [2], 8, 8, 128, BF16, seed=15)
     low.v = low.k
     want, want_lse = low.run()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("lens,hkv,d,kv", [
+    ([900, 300], 2, 128, BF16),           # clusters
+    ([300] * 90, 2, 64, FP8),             # half-size CTAs, four copying warps
+    ([30000, 700, 64], 2, 128, BF16)])    # the list and its joining kernel
+def test_a_wait_that_runs_out_is_reported_and_the_stream_recovers(lens, hkv, d, kv):
+    c = Case(lens, [1] * len(lens), 4 * hkv, hkv, d, BF16, kv, seed=22)
+    want, want_lse = c.run()
+    batch, cache, out = c.batch(), c.cache(), torch.empty_like(want)
+    ws = torch.empty(dsa.dsa_paged_attention_workspace_size(batch, cache, c.hq),
+                     dtype=torch.uint8, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dsa.dsa_test_paged_attention_wait_timeout(batch, cache, c.q, c.sm_scale, out, None, ws, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == TIMEOUT
+    out, lse = c.run()
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
