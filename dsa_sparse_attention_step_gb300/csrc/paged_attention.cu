@@ -21,7 +21,7 @@ bool paged_attention_supported(const BatchArgs& bt, int kv_heads, int group) {
 
 // Of the default plan, which needs more than the whole one.
 size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim) {
-    return ws_layout(head_dim, row_tile(max_rows, false)).total;
+    return ws_layout(head_dim, row_tile(head_dim, max_rows, false)).total;
 }
 
 cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cache, int format,
@@ -43,7 +43,8 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
     p.lse = lse;
     p.score_scale = sm_scale * cache.k_scale * kLog2e;
     p.v_scale = cache.v_scale;
-    const WsLayout w = ws_layout(cache.head_dim, row_tile((int64_t)bt.max_q * p.group, false));
+    const WsLayout w = ws_layout(
+        cache.head_dim, row_tile(cache.head_dim, (int64_t)bt.max_q * p.group, false));
     uint8_t* base = static_cast<uint8_t*>(ws);
     p.part_o = reinterpret_cast<float*>(base);
     p.part_ml = reinterpret_cast<float*>(base + w.ml);

@@ -1142,9 +1142,12 @@ constexpr int kMinTiles = 2;
 
 // Rows of a tile for requests of up to max_rows rows: the smallest that holds
 // them, so that the cache is read once, but 16 when every request runs whole
-// (a row's arithmetic must not depend on the other requests' row counts).
-inline int row_tile(int64_t max_rows, bool whole) {
-    return whole || max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 48 ? 48 : 64;
+// (a row's arithmetic must not depend on the other requests' row counts).  The
+// kernel's kRows and the workspace both follow it.
+inline int row_tile(int dim, int64_t max_rows, bool whole) {
+    if (whole || max_rows <= 16) return 16;
+    if (max_rows <= 32) return 32;
+    return max_rows <= 48 && dim < 256 ? 48 : 64;  // 256 dims: eight warps, no 3 x 4
 }
 
 // At most so many units: a request of n_b tokens has n_b group / rows row tiles,
@@ -1238,6 +1241,9 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
                                  p);
         }
     }
+    // the workspace was laid out for this tile
+    const int64_t rows = (int64_t)p.bt.max_q * p.group;
+    if (C::kRows != row_tile(C::kDim, rows, p.whole != 0)) return cudaErrorInvalidValue;
     if ((e = prepare_kernel<C, kQBf16>()) != cudaSuccess) return e;
     // no more CTAs than the longest list that these host sizes allow has work for
     p.min_length = C::kUnitCost + kMinTiles;
@@ -1249,7 +1255,6 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
                       (size_t)C::kSmem, stream, true, 1, tm_k, tm_v, p);
     if (e != cudaSuccess || p.whole || ctas == 1) return e;
     *launches = 2;
-    const int64_t rows = (int64_t)p.bt.max_q * p.group;
     const dim3 grid((unsigned)ctas, (unsigned)(rows < C::kRows ? rows : C::kRows));
     return launch_kernel(paged_join_kernel<C::kDim, kQBf16>, grid, dim3(kJoinThreads), 0, stream,
                          true, 1, p, (int)C::kRows);
@@ -1263,7 +1268,7 @@ cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* lau
     // keep up (one wide FP8 head: 38.4 -> 35.3 us); 64 dims and FP8 need the longer
     // steps of two (64 ragged FP8 requests: 331 us, with four 381).
     constexpr bool kFour = kD == 256 || (kD == 128 && !kFp8);
-    switch (row_tile((int64_t)p.bt.max_q * p.group, p.whole != 0)) {
+    switch (row_tile(kD, (int64_t)p.bt.max_q * p.group, p.whole != 0)) {
         case 16:
             return launch_cfg<AttnCfg<kD, kFp8, 1, kFour ? 4 : 2, kFour ? 2 : 4>, kQBf16>(
                 p, cache, launches, stream);
@@ -1271,10 +1276,10 @@ cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* lau
             return launch_cfg<AttnCfg<kD, kFp8, 2, 2, kD == 256 ? 2 : 3>, kQBf16>(
                 p, cache, launches, stream);
         case 48:
-            return launch_cfg<AttnCfg<kD, kFp8, kD == 256 ? 4 : 3,
-                                      kD == 256 || (kD == 128 && !kFp8) ? 2 : 1,
-                                      kD == 256 ? 1 : kD == 128 && !kFp8 ? 2 : 4>,
-                              kQBf16>(p, cache, launches, stream);
+            if constexpr (kD < 256)
+                return launch_cfg<AttnCfg<kD, kFp8, 3, kFour ? 2 : 1, kFour ? 2 : 4>, kQBf16>(
+                    p, cache, launches, stream);
+            return cudaErrorInvalidValue;  // row_tile gives 256 dims no 48
         default:
             return launch_cfg<AttnCfg<kD, kFp8, 4, kD == 256 ? 2 : 1, kD == 256 ? 1 : 3>, kQBf16>(
                 p, cache, launches, stream);

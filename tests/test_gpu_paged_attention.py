@@ -70,12 +70,14 @@ class Case:
         out = torch.full(self.q.shape, NAN, dtype=self.dtype, device=DEV)
         lse = torch.full(self.q.shape[:2], NAN, dtype=torch.float32, device=DEV)
         need = dsa.dsa_paged_attention_workspace_size(batch, cache, self.hq)
-        ws = torch.full((need // 4 + 4,), NAN, dtype=torch.float32, device=DEV)  # any contents
+        ws = torch.full((need // 4 + (1 << 20),), NAN, dtype=torch.float32, device=DEV)  # any contents
+        ws[(need + 3) // 4:] = 7.0  # not part of it
         st = torch.zeros(1, dtype=torch.int32, device=DEV)
         dsa.dsa_paged_attention(batch, cache, self.q if q is None else q, self.sm_scale, out, lse,
                                 ws, st)
         torch.cuda.synchronize()
         assert int(st.item()) == status
+        assert (ws[(need + 3) // 4:] == 7.0).all()
         return out, lse
 
     def reference(self):
@@ -133,7 +135,10 @@ def test_lengths(length, new, kv):
 
 
 @pytest.mark.parametrize("hq,hkv,d,length,new", [(4, 1, 128, 70001, 1), (3, 3, 64, 33333, 3),
-                                                 (12, 1, 256, 20011, 4)])
+                                                 (12, 1, 256, 20011, 4), (8, 1, 256, 60011, 5),
+                                                 (16, 1, 256, 60013, 2), (16, 1, 256, 60017, 4),
+                                                 (24, 1, 128, 60019, 1), (48, 1, 128, 60021, 1),
+                                                 (64, 1, 64, 60023, 1), (40, 1, 64, 60025, 1)])
 def test_one_long_request_is_split_and_joined(hq, hkv, d, length, new):
     c = Case([length], [new], hq, hkv, d, BF16, seed=length)
     c.check(*c.run())

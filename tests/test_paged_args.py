@@ -122,6 +122,8 @@ def test_paged_attention_workspace_follows_rows_and_head_dim(lib):
     def size(hq, **kw):
         c = _cache(**kw)
         return lib.dsa_paged_attention_workspace_size(ctypes.byref(b), ctypes.byref(c), hq)
-    assert 0 < size(4) == size(32) < size(64) < size(128) == size(256)
+    assert 0 < size(4) == size(32) < size(64) < size(80) == size(96) < size(128) == size(256)
+    # 256 dims have no tile of 48 rows: 40 rows take the 64-row one
+    assert size(80, head_dim=256) == size(128, head_dim=256)
     assert size(4, head_dim=256) > size(4) > size(4, head_dim=64)
     assert size(5) == 0 and size(0) == 0 and size(4, head_dim=96) == 0
