@@ -132,7 +132,7 @@ uint64_t dsa_launch_count(void);
  * token depend on its own inputs alone, and equal the default plan's wherever
  * that plan runs the token whole.  Small batches then use fewer SMs.
  * Process-wide; read once by each later call of dsa_sparse_mla(_ex),
- * dsa_decode(_ex) and dsa_decode_noalloc.  Workspace sizes do not change.
+ * dsa_decode(_ex), dsa_decode_noalloc and dsa_paged_attention (see there).  Workspace sizes do not change.
  * Returns the previous setting (0 or 1); the default is 0. */
 int32_t dsa_set_batch_invariant(int32_t enabled);
 
