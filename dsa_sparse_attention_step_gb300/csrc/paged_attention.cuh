@@ -624,7 +624,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     Walk<C> walk(p, s_share);
     const int grp = warp / (C::kWM * C::kWN);
     const int wn = warp / C::kWM % C::kWN, wm = warp % C::kWM;
-    const int tw = grp * C::kWN + wn;  // of the warps that share rows
     const int g = lane >> 2, c = lane & 3;
     // ldmatrix addresses of this lane: for keys the matrices are token halves by
     // chunk of a pair, for values (transposed) chunks by token halves.  The swizzle
@@ -764,8 +763,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; i < C::kTilesD; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
         const int last = min(u.tiles, tile + walk.count);
-        // this group's pages: those whose number in the run is grp modulo kNG
-        for (int t = tile + (grp + C::kNG - n % C::kNG) % C::kNG; t < last; t += C::kNG) {
+        // this group's pages: those whose number in the run is grp modulo kNG.  The join
+        // takes the groups from the one with the unit's first page on, so that the
+        // order of its sums does not depend on the units before this one.
+        const int turn = (grp + C::kNG - n % C::kNG) % C::kNG;
+        const int tw = turn * C::kWN + wn;  // of the warps that share rows
+        for (int t = tile + turn; t < last; t += C::kNG) {
             const int i_run = n + (t - tile), st = i_run % C::kStages;
             if (!dead)
                 dead = !mbar_wait(&s_full[i_run % C::kFull], (i_run / C::kFull) & 1, abort_flag);
