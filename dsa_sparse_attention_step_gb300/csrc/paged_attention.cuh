@@ -495,6 +495,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
     // operands of the MMAs: the cache's own type, or f16 lifted from FP8
     constexpr bool kBf16 = kQBf16 && !C::kFp8;
+    // Probabilities that become f16 are held at 2^15 times their size, the row's largest
+    // at 2^15: f16 has normal numbers down to 2^-29 of it then, and steps of 2^-39 below
+    // (at their own size 2^-14 and 2^-24, where the positions beside a large one, 2^-25
+    // each, would vanish from the product but not from the sum).
+    constexpr float kPExp = kBf16 ? 0.f : 15.f, kPUnit = kBf16 ? 1.f : 0x1p-15f;
     constexpr int kD = C::kDim;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t s_full[C::kFull], s_empty[C::kStages];
@@ -854,7 +859,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                         for (int i = 0; i < kNt; ++i)
                             y = fmaxf(y, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
-                        top[x] = fmaxf(m[x], quad_max(y) * f[x]);
+                        // rounded up, as the bases below, so that no p exceeds 2^kPExp
+                        top[x] = fmaxf(m[x], __fmul_ru(quad_max(y), f[x]));
                         grew |= top[x] > m[x];
                     }
                     if (__any_sync(0xffffffffu, grew)) {
@@ -872,11 +878,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         m[0] = top[0];
                         m[1] = top[1];
                     }
-                    // P rounded to the operand type (the sums are of the unrounded
-                    // values): half a step per probability, which averages out as the
-                    // output's own rounding does
+                    // P rounded to the operand type, by half a step at most: 2^-9 of a
+                    // probability in bf16, 2^-12 in f16 (2^-40 of the row's largest for
+                    // those below 2^-29 of it).  The sums are of the unrounded values.
                     uint32_t pf[C::kSub / 16][4];
-                    const float b0 = base_of(m[0]), b1 = base_of(m[1]);
+                    const float b0 = __fsub_ru(base_of(m[0]), kPExp);
+                    const float b1 = __fsub_ru(base_of(m[1]), kPExp);
 #pragma unroll
                     for (int i = 0; i < kNt; ++i) {
                         const float p0 = ex2(fmaf(s[i][0], f[0], -b0));
@@ -929,8 +936,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         l[0] = quad_sum(l[0]);
         l[1] = quad_sum(l[1]);
         if (c == 0) {
-            s_ml[tw * C::kRows + r] = make_float2(m[0], l[0]);
-            s_ml[tw * C::kRows + r + 8] = make_float2(m[1], l[1]);
+            s_ml[tw * C::kRows + r] = make_float2(m[0], l[0] * kPUnit);
+            s_ml[tw * C::kRows + r + 8] = make_float2(m[1], l[1] * kPUnit);
         }
         const bool complete = walk.complete(p);
         // a cluster's pieces stay in the ring, which its only unit is done with
@@ -980,8 +987,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                     for (int w = 0; w < C::kTokenWarps; ++w) {
                         const float2 ml = s_ml[w * C::kRows + r];
-                        weight[x][w] = ex2(ml.x - base);
-                        total += ml.y * weight[x][w];
+                        const float a = ex2(ml.x - base);
+                        total += ml.y * a;
+                        weight[x][w] = a * kPUnit;
                     }
                     if (complete) {
                         const int j = token_of(p, tile_row + r);

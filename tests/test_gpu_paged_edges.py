@@ -1,13 +1,34 @@
-"""dsa_paged_attention where values, scores, batches and buffers are out of the ordinary."""
+"""dsa_paged_attention where values, scores, batches and buffers are out of the ordinary.
+
+Tolerances are those of test_gpu_paged_attention, but for probabilities rounded to f16,
+which are held at 2^15 times their size: half a step (eps / 2) of those from 2^-29 of the
+row's largest on, and half of f16's smallest step, 2^-40, of those below."""
 import copy
 
 import pytest
 import torch
 
 import dsa_sparse_attention_step_gb300 as dsa
-from test_gpu_paged_attention import BF16, DEV, FP8, Case
+from test_gpu_paged_attention import BF16, DEV, F16, FP8, NAN, Case
 
 pytestmark = pytest.mark.gpu
+
+
+def tolerances(c, r):
+    """(of out, of lse) for the reference r of case c."""
+    n = max(c.lens)
+    bf16_p = c.k.dtype == BF16
+    e = (c.d + 8) * 2.0**-23 * r["terms"]
+    tol = (torch.finfo(c.dtype).eps / 2 * r["out"].abs() +
+           torch.finfo(BF16 if bf16_p else F16).eps / 2 * r["mean_abs"] +
+           (2 * e + n * 2.0**-24 + 2.0**-20)[..., None] * r["mean_abs"])
+    if not bf16_p:
+        tol += n * 2.0**-40 * r["max_abs"][..., None]
+    if c.dtype == F16:
+        tol += 2.0**-25
+    fine = torch.where(torch.isinf(r["lse"]), 0.0, r["lse"])
+    return tol, e + n * 2.0**-24 + 2.0**-20 + 2.0**-22 * fine.abs()
+
 
 def rows_of(c, b):
     return slice(c.offsets[b], c.offsets[b + 1])
@@ -45,3 +66,47 @@ def test_batch_invariant_with_several_units_a_cta(d, kv):
             assert torch.equal(l, lse[rows_of(c, b)]) and torch.equal(o, out[rows_of(c, b)])
     finally:
         dsa.dsa_set_batch_invariant(prev)
+
+
+@pytest.mark.parametrize("dtype,kv", [(F16, F16), (BF16, FP8), (F16, FP8), (BF16, BF16)])
+@pytest.mark.parametrize("requests,length,d", [
+    (1, 700, 128),     # a cluster to the unit
+    (200, 300, 64),    # half-size CTAs
+    (160, 2048, 64), (160, 2048, 128), (160, 1100, 256)])  # the list
+def test_many_small_probabilities_beside_a_large_one(requests, length, d, dtype, kv):
+    """A position about 18 above all others, whose value is 0: what is left of the
+    output is the sum of the others' probabilities, some 2^-26 each."""
+    c = Case([length] * requests, [1] * requests, 4, 1, d, dtype, kv, seed=41)
+    k, v = c.k.float(), c.v.float() + 4 / c.scales[1]
+    k = torch.where(k.isnan(), k, 0.0)
+    first = c.table[:, 0].long()
+    k[first, :, 5] = 18.0 / d**0.5 / c.scales[0]
+    v[first, :, 5] = 0.0
+    c.k, c.v = k.to(kv), v.to(kv)
+    c.q[:] = 1.0
+    out, lse = c.run()
+    r = c.reference()
+    tol, lse_tol = tolerances(c, r)
+    err = (out.double() - r["out"]).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    assert ((lse.double() - r["lse"]).abs() <= lse_tol).all()
+
+
+@pytest.mark.parametrize("dtype,kv", [(F16, F16), (F16, FP8), (BF16, FP8)])
+def test_scores_of_millions(dtype, kv):
+    """Scores whose steps in fp32 are of the order of 1: the largest stays a finite
+    probability.  Each row sees one position far above the rest."""
+    c = Case([300, 700], [1, 1], 4, 2, 64, dtype, kv, seed=42)
+    k = torch.where(c.k.float().isnan(), NAN, 0.0)
+    for b, length in enumerate(c.lens):
+        at = length - 7
+        k[c.table[b, at // 64].long(), :, at % 64] = 448.0
+    c.k = k.to(kv)
+    c.q[:] = 448.0 + 64 * torch.arange(4, device=DEV)[:, None]
+    c.sm_scale = 1.37 / (c.scales[0])
+    out, _ = c.run()
+    for b, length in enumerate(c.lens):
+        at = length - 7
+        want = c.v[c.table[b, at // 64].long(), :, at % 64].float() * c.scales[1]
+        want = want.repeat_interleave(2, dim=0)
+        assert ((out[b].float() - want).abs() <= torch.finfo(dtype).eps * want.abs()).all()
