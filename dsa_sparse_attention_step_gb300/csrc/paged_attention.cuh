@@ -444,6 +444,11 @@ __device__ __forceinline__ float quad_sum(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+// An unnormalised output as a result; 0 where the sum is 0 (factor 0), whatever x is.
+__device__ __forceinline__ float result(float x, float factor) {
+    return factor == 0.f ? 0.f : x * factor;
+}
+
 // A maximum as a subtrahend: 0 for a row that has seen nothing yet.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -1021,8 +1026,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (complete)
                     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at[x] * kD + d0 +
                                               quad) =
-                        make_uint2(pack2<kQBf16>(sum.x * inv[x], sum.y * inv[x]),
-                                   pack2<kQBf16>(sum.z * inv[x], sum.w * inv[x]));
+                        make_uint2(pack2<kQBf16>(result(sum.x, inv[x]), result(sum.y, inv[x])),
+                                   pack2<kQBf16>(result(sum.z, inv[x]), result(sum.w, inv[x])));
                 else
                     *reinterpret_cast<float4*>((C::kDirect ? piece_o : p.part_o) + at[x] * kD + d0 +
                                                quad) = sum;
@@ -1057,8 +1062,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                     walk.u.h * p.group + tile_row + r - j * p.group;
                 const float scale = total == 0.f ? 0.f : p.v_scale / total;
                 *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kD + d) =
-                    make_uint2(pack2<kQBf16>(sum.x * scale, sum.y * scale),
-                               pack2<kQBf16>(sum.z * scale, sum.w * scale));
+                    make_uint2(pack2<kQBf16>(result(sum.x, scale), result(sum.y, scale)),
+                               pack2<kQBf16>(result(sum.z, scale), result(sum.w, scale)));
                 if (p.lse && d == 0)
                     p.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
             }
@@ -1121,8 +1126,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnPara
                 (int64_t)(join.y + t) * (p.kv_heads * p.group) + join_head + r - t * p.group;
             const float inv = l == 0.f ? 0.f : p.v_scale / l;
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * kDim + 4 * x) =
-                make_uint2(pack2<kQBf16>(o.x * inv, o.y * inv),
-                           pack2<kQBf16>(o.z * inv, o.w * inv));
+                make_uint2(pack2<kQBf16>(result(o.x, inv), result(o.y, inv)),
+                           pack2<kQBf16>(result(o.z, inv), result(o.w, inv)));
             if (p.lse && x == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
         __syncthreads();

@@ -110,3 +110,21 @@ def test_scores_of_millions(dtype, kv):
         want = c.v[c.table[b, at // 64].long(), :, at % 64].float() * c.scales[1]
         want = want.repeat_interleave(2, dim=0)
         assert ((out[b].float() - want).abs() <= torch.finfo(dtype).eps * want.abs()).all()
+
+
+@pytest.mark.parametrize("kv", [BF16, FP8])
+@pytest.mark.parametrize("copies", [1, 90])
+def test_rows_that_see_nothing_are_zero_whatever_the_values(kv, copies):
+    """More new tokens than context, and values of the context that are not numbers."""
+    lens, new = [3, 2, 70] * copies, [6, 5, 2] * copies
+    c = Case(lens, new, 8, 2, 128, BF16, kv, seed=44)
+    v = c.v.float()
+    for b in range(len(lens)):
+        v[c.table[b, 0].long(), :, :3] = NAN
+    c.v = v.to(kv)
+    out, lse = c.run()
+    for b, (length, n) in enumerate(zip(lens, new)):
+        blind = slice(c.offsets[b], c.offsets[b] + max(0, n - length))
+        assert (out[blind] == 0).all() and torch.isneginf(lse[blind]).all()
+        seeing = slice(blind.stop, c.offsets[b + 1])
+        assert out[seeing].isnan().all() and torch.isfinite(lse[seeing]).all()
