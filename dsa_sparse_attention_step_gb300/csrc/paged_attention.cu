@@ -6,12 +6,12 @@ namespace dsa {
 
 using namespace paged;
 
-cudaError_t launch_paged_attention_64(const AttnParams& p, const dsa_kv_cache& cache, int format,
-                                      int* launches, cudaStream_t stream);
-cudaError_t launch_paged_attention_128(const AttnParams& p, const dsa_kv_cache& cache, int format,
-                                       int* launches, cudaStream_t stream);
-cudaError_t launch_paged_attention_256(const AttnParams& p, const dsa_kv_cache& cache, int format,
-                                       int* launches, cudaStream_t stream);
+// _many: for requests of several tokens (kMany).
+using Launch = cudaError_t(const AttnParams& p, const dsa_kv_cache& cache, int format,
+                           int* launches, cudaStream_t stream);
+Launch launch_paged_attention_64, launch_paged_attention_128, launch_paged_attention_256;
+Launch launch_paged_attention_64_many, launch_paged_attention_128_many,
+    launch_paged_attention_256_many;
 
 // Positions in the list of key tiles are 32-bit (kUnitCost is at most 8).
 bool paged_attention_supported(const BatchArgs& bt, int kv_heads, int group) {
@@ -39,6 +39,7 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
     p.min_length = p.cluster = p.row_tiles = 0;  // set by the launch
     p.q_stride = q_stride;
     p.q = q;
+    p.v_pages = cache.v_pages;
     p.out = out;
     p.lse = lse;
     p.score_scale = sm_scale * cache.k_scale * kLog2e;
@@ -51,11 +52,17 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
     p.joins = reinterpret_cast<int32_t*>(base + w.joins);
     p.status = status;
     *launches = 1;
+    // a request's results may not depend on the others' token counts when it runs whole
+    const bool many = bt.max_q > 1 || whole;
+    Launch* launch;
     switch (cache.head_dim) {
-        case 64: return launch_paged_attention_64(p, cache, format, launches, stream);
-        case 128: return launch_paged_attention_128(p, cache, format, launches, stream);
-        default: return launch_paged_attention_256(p, cache, format, launches, stream);
+        case 64: launch = many ? launch_paged_attention_64_many : launch_paged_attention_64; break;
+        case 128:
+            launch = many ? launch_paged_attention_128_many : launch_paged_attention_128;
+            break;
+        default: launch = many ? launch_paged_attention_256_many : launch_paged_attention_256;
     }
+    return launch(p, cache, format, launches, stream);
 }
 
 }  // namespace dsa

@@ -60,6 +60,7 @@ struct AttnParams {
     int32_t withhold;  // test only: the first page's copy is not issued
     int64_t q_stride;
     const void* q;
+    const void* v_pages;
     void* out;
     float* lse;
     float score_scale;  // sm_scale * k_scale * log2 e
@@ -410,6 +411,29 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Infinite and NaN elements in 16 bytes of a cache: whether there are any, and the rest
+// with zeros in their place.
+template <bool kFp8, bool kBf16>
+__device__ __forceinline__ bool any_not_finite(const uint4& u) {
+    if (kFp8)  // magnitude 0x7f
+        return (((u.x & 0x7f7f7f7fu) + 0x01010101u | (u.y & 0x7f7f7f7fu) + 0x01010101u |
+                 (u.z & 0x7f7f7f7fu) + 0x01010101u | (u.w & 0x7f7f7f7fu) + 0x01010101u) &
+                0x80808080u) != 0;
+    const uint32_t top = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                  __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    constexpr uint32_t kInf = kBf16 ? 0x7f80 : 0x7c00;
+    return max(top & 0xffffu, top >> 16) >= kInf;
+}
+
+template <bool kFp8, bool kBf16>
+__device__ __forceinline__ uint4 finite_part(const uint4& u) {
+    constexpr uint32_t kMask = kFp8 ? 0x7f7f7f7fu : kBf16 ? 0x7f807f80u : 0x7c007c00u;
+    auto part = [](uint32_t w) {
+        return w & ~(kFp8 ? __vcmpeq4(w & kMask, kMask) : __vcmpeq2(w & kMask, kMask));
+    };
+    return make_uint4(part(u.x), part(u.y), part(u.z), part(u.w));
+}
+
 // Four E4M3 codes as two pairs of f16, exact.
 __device__ __forceinline__ void lift(uint32_t codes, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
@@ -487,6 +511,26 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t addr, int rank) {
     return v;
 }
 
+template <bool kBf16>
+__device__ __forceinline__ float unpack(uint16_t bits) {
+    return kBf16 ? __uint_as_float((uint32_t)bits << 16) : __half2float(__ushort_as_half(bits));
+}
+
+// The value at a unit's position, if it is infinite or NaN, else 0: added to a row that
+// sees it, as good as its product with the probability.
+template <typename C, bool kBf16>
+__device__ __forceinline__ float not_finite_value(const AttnParams& p, const Cursor<C::kRows>& u,
+                                                  int position, int dim) {
+    const int page = __ldg(p.bt.block_table + (int64_t)u.b * p.bt.max_pages + position / kPage);
+    if (page < 0 || page >= p.bt.num_pages) return 0.f;
+    const int64_t at =
+        (((int64_t)page * p.kv_heads + u.h) * kPage + position % kPage) * C::kDim + dim;
+    const float x =
+        C::kFp8 ? e4m3x2_to_float2(static_cast<const uint8_t*>(p.v_pages)[at]).x
+                : unpack<kBf16>(static_cast<const uint16_t*>(p.v_pages)[C::kFp8 ? 0 : at]);
+    return isfinite(x) ? 0.f : x;
+}
+
 template <int kCount>
 __device__ __forceinline__ void consumer_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kCount) : "memory");
@@ -494,7 +538,11 @@ __device__ __forceinline__ void consumer_sync() {
 
 // ---- the kernel ----------------------------------------------------------------
 
-template <typename C, bool kQBf16>
+// kMany: requests may bring several tokens, so that positions of the context are hidden
+// from some rows.  With one token none is, and what it takes (below: values that are not
+// finite) would cost short calls 1 to 4%; with several it costs long ones nothing and the
+// shortest 0.2 to 0.7 us (186 requests of up to 226, 8 tokens: 9.3 -> 10.0 us).
+template <typename C, bool kQBf16, bool kMany>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
@@ -512,6 +560,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     __shared__ uint32_t s_warp[C::kThreads / 32];
     __shared__ Share<C::kRows> s_share;
     __shared__ int s_abort;
+    __shared__ int s_cleared;  // n of the unit some of whose values were cleared
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                ~(uintptr_t)1023);
     uint8_t* tail = ring + C::kStages * C::kStageBytes;
@@ -526,6 +575,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; i < C::kStages; ++i) mbar_init(&s_empty[i], C::kWM * C::kWN);
         fence_mbar_init();
         s_abort = 0;
+        s_cleared = -1;
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
@@ -765,7 +815,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int r = tile_row + 16 * wm + g + 8 * x;
             vis[x] = r < u.r.rows ? u.r.seq - u.r.nb + token_of(p, r) + 1 : 0;
         }
-        const int vis_first = u.r.seq - u.r.nb + token_of(p, tile_row + 16 * wm) + 1;
+        // and what the row tile's first row, and so every row of it, sees
+        const int vis_first = u.r.seq - u.r.nb + token_of(p, tile_row) + 1;
 
         float o[C::kTilesD][4];
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -801,6 +852,30 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     fence_proxy_async_smem();  // the next copy into this stage comes after
                     __syncwarp();
+                }
+                const int shown = min(first + C::kTokens, u.r.seq);
+                if (kMany && max(first, vis_first) < shown) {
+                    // the same for infinite and NaN values of new tokens that some of the
+                    // row tile's rows do not see; the others get them when the unit is done
+                    constexpr int kChunks = C::kRowBytes / 16, kPer = C::kBoxBytes / 16;
+                    const int x = lane % kChunks, r0 = max(first, vis_first) + lane / kChunks;
+                    uint8_t* v = ring + st * C::kStageBytes + C::kTileBytes +
+                                 (x / kPer) * (kPage * C::kBoxBytes) + (x % kPer) * 16;
+                    bool bad = false;
+#pragma unroll 1
+                    for (int r = r0; r < shown; r += 32 / kChunks)
+                        bad |= any_not_finite<C::kFp8, kBf16>(
+                            *reinterpret_cast<const uint4*>(v + r % kPage * C::kBoxBytes));
+                    if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                        for (int r = r0; r < shown; r += 32 / kChunks) {
+                            uint4* at = reinterpret_cast<uint4*>(v + r % kPage * C::kBoxBytes);
+                            *at = finite_part<C::kFp8, kBf16>(*at);
+                        }
+                        *static_cast<volatile int*>(&s_cleared) = n;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
                 }
 #pragma unroll
                 for (int sub = 0; sub < C::kTokens; sub += C::kSub) {
@@ -1033,6 +1108,31 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                quad) = sum;
             }
         }
+        if (kMany && s_cleared == n - max(0, last - tile)) {
+            // values of this run's tiles were cleared: add them to the rows that see them
+            consumer_sync<32 * C::kConsumers>();
+#pragma unroll 1
+            for (int i = tid; i < rows * kD; i += kThreads) {
+                const int row = tile_row + i / kD, d = i % kD, j = token_of(p, row);
+                const int to = min(min(u.r.seq, last * kPage), u.r.seq - u.r.nb + j + 1);
+                float bad = 0.f;
+#pragma unroll 1
+                for (int x = max(vis_first, tile * kPage); x < to; ++x)
+                    bad += not_finite_value<C, kBf16>(p, u, x, d);
+                if (bad == 0.f) continue;
+                if (complete) {
+                    const int64_t at = (int64_t)(u.r.q0 + j) * (p.kv_heads * p.group) +
+                                       u.h * p.group + row - j * p.group;
+                    uint16_t* out = static_cast<uint16_t*>(p.out) + at * kD + d;
+                    *out = (uint16_t)pack2<kQBf16>(unpack<kQBf16>(*out) + bad, 0.f);
+                } else if (C::kDirect) {
+                    piece_o[i] += bad;
+                } else {
+                    p.part_o[(2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0)) * C::kRows * kD + i] +=
+                        bad;
+                }
+            }
+        }
         if (C::kDirect && p.cluster > 1) {
             // the cluster's pieces, read from its CTAs' shared memory
             constexpr int kRowQuads = kD / 4;
@@ -1187,20 +1287,20 @@ inline WsLayout ws_layout(int dim, int rows) {
 
 // The kernel's attributes, set once: its dynamic shared memory, and its registers,
 // of which the consumers would wait forever for more than the launch brings.
-template <typename C, bool kQBf16>
+template <typename C, bool kQBf16, bool kMany>
 cudaError_t prepare_kernel() {
     static const cudaError_t ready = [] {
         cudaFuncAttributes a;
-        cudaError_t e = cudaFuncGetAttributes(&a, paged_attention_kernel<C, kQBf16>);
+        cudaError_t e = cudaFuncGetAttributes(&a, paged_attention_kernel<C, kQBf16, kMany>);
         if (e == cudaSuccess && a.numRegs < C::kLaunchRegs) e = cudaErrorInvalidConfiguration;
         return e;
     }();
     if (ready != cudaSuccess) return ready;
-    return cudaFuncSetAttribute(paged_attention_kernel<C, kQBf16>,
+    return cudaFuncSetAttribute(paged_attention_kernel<C, kQBf16, kMany>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
 }
 
-template <typename C, bool kQBf16>
+template <typename C, bool kQBf16, bool kMany>
 cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
                        cudaStream_t stream) {
     CUtensorMap tm_k, tm_v;
@@ -1228,8 +1328,8 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
         while (p.cluster < 8 && units * p.cluster * 2 <= sms) p.cluster *= 2;
         p.row_tiles = (int)row_tiles;
         if (tiles * C::kStageBytes <= (int64_t)p.cluster * (units <= sms ? 524288 : 262144)) {
-            if ((e = prepare_kernel<D, kQBf16>()) != cudaSuccess) return e;
-            return launch_kernel(paged_attention_kernel<D, kQBf16>,
+            if ((e = prepare_kernel<D, kQBf16, kMany>()) != cudaSuccess) return e;
+            return launch_kernel(paged_attention_kernel<D, kQBf16, kMany>,
                                  dim3((unsigned)(units * p.cluster)), dim3(D::kThreads),
                                  (size_t)D::kSmem, stream, true, p.cluster, tm_k, tm_v, p);
         }
@@ -1253,8 +1353,8 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
             tiles * (C::kStageBytes + 8192) <= 524288) {
             p.cluster = 1;
             p.row_tiles = (int)small_tiles;
-            if ((e = prepare_kernel<S, kQBf16>()) != cudaSuccess) return e;
-            return launch_kernel(paged_attention_kernel<S, kQBf16>, dim3((unsigned)small_units),
+            if ((e = prepare_kernel<S, kQBf16, kMany>()) != cudaSuccess) return e;
+            return launch_kernel(paged_attention_kernel<S, kQBf16, kMany>, dim3((unsigned)small_units),
                                  dim3(S::kThreads), (size_t)S::kSmem, stream, true, 1, tm_k, tm_v,
                                  p);
         }
@@ -1262,14 +1362,14 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
     // the workspace was laid out for this tile
     const int64_t rows = (int64_t)p.bt.max_q * p.group;
     if (C::kRows != row_tile(C::kDim, rows, p.whole != 0)) return cudaErrorInvalidValue;
-    if ((e = prepare_kernel<C, kQBf16>()) != cudaSuccess) return e;
+    if ((e = prepare_kernel<C, kQBf16, kMany>()) != cudaSuccess) return e;
     // no more CTAs than the longest list that these host sizes allow has work for
     p.min_length = C::kUnitCost + kMinTiles;
     const double length =
         most_units(p.bt, p.kv_heads, p.group, C::kRows) * (double)(tiles + C::kUnitCost);
     int ctas = sms < kMaxCtas ? sms : kMaxCtas;
     if (length < (double)ctas * p.min_length) ctas = (int)(length / p.min_length) + 1;
-    e = launch_kernel(paged_attention_kernel<C, kQBf16>, dim3((unsigned)ctas), dim3(C::kThreads),
+    e = launch_kernel(paged_attention_kernel<C, kQBf16, kMany>, dim3((unsigned)ctas), dim3(C::kThreads),
                       (size_t)C::kSmem, stream, true, 1, tm_k, tm_v, p);
     if (e != cudaSuccess || p.whole || ctas == 1) return e;
     *launches = 2;
@@ -1278,7 +1378,7 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
                          true, 1, p, (int)C::kRows);
 }
 
-template <int kD, bool kFp8, bool kQBf16>
+template <int kD, bool kFp8, bool kQBf16, bool kMany>
 cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* launches,
                         cudaStream_t stream) {
     // D = 256 has 128 accumulators a thread for 16 rows and so eight warps.  At 16 rows
@@ -1288,31 +1388,31 @@ cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* lau
     constexpr bool kFour = kD == 256 || (kD == 128 && !kFp8);
     switch (row_tile(kD, (int64_t)p.bt.max_q * p.group, p.whole != 0)) {
         case 16:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, kFour ? 4 : 2, kFour ? 2 : 4>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 1, kFour ? 4 : 2, kFour ? 2 : 4>, kQBf16, kMany>(
                 p, cache, launches, stream);
         case 32:
-            return launch_cfg<AttnCfg<kD, kFp8, 2, 2, kD == 256 ? 2 : 3>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 2, 2, kD == 256 ? 2 : 3>, kQBf16, kMany>(
                 p, cache, launches, stream);
         case 48:
             if constexpr (kD < 256)
-                return launch_cfg<AttnCfg<kD, kFp8, 3, kFour ? 2 : 1, kFour ? 2 : 4>, kQBf16>(
+                return launch_cfg<AttnCfg<kD, kFp8, 3, kFour ? 2 : 1, kFour ? 2 : 4>, kQBf16, kMany>(
                     p, cache, launches, stream);
             return cudaErrorInvalidValue;  // row_tile gives 256 dims no 48
         default:
-            return launch_cfg<AttnCfg<kD, kFp8, 4, kD == 256 ? 2 : 1, kD == 256 ? 1 : 3>, kQBf16>(
+            return launch_cfg<AttnCfg<kD, kFp8, 4, kD == 256 ? 2 : 1, kD == 256 ? 1 : 3>, kQBf16, kMany>(
                 p, cache, launches, stream);
     }
 }
 
-template <int kD>
+template <int kD, bool kMany>
 cudaError_t launch_dim(const AttnParams& p, const dsa_kv_cache& cache, int format, int* launches,
                        cudaStream_t stream) {
     const bool fp8 = cache.format == DSA_KV_FP8_E4M3;
     if (format == DSA_FLOAT_BF16)
-        return fp8 ? launch_rows<kD, true, true>(p, cache, launches, stream)
-                   : launch_rows<kD, false, true>(p, cache, launches, stream);
-    return fp8 ? launch_rows<kD, true, false>(p, cache, launches, stream)
-               : launch_rows<kD, false, false>(p, cache, launches, stream);
+        return fp8 ? launch_rows<kD, true, true, kMany>(p, cache, launches, stream)
+                   : launch_rows<kD, false, true, kMany>(p, cache, launches, stream);
+    return fp8 ? launch_rows<kD, true, false, kMany>(p, cache, launches, stream)
+               : launch_rows<kD, false, false, kMany>(p, cache, launches, stream);
 }
 
 }  // namespace paged

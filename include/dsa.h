@@ -528,8 +528,9 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
  * Unlike the other calls this one takes seq_lens[b] < n_b: tokens before
  * position 0 see nothing, so a padding request has seq_lens[b] = 0 and any
  * n_b.  A token that sees nothing gives out = 0 and lse = -inf.
- * Cache contents at positions at or beyond seq_lens[b] never reach a result,
- * whatever they hold.
+ * Cache contents at positions that a token does not see never reach its result,
+ * whatever they hold: neither those at or beyond seq_lens[b] nor later tokens'.
+ * An infinite or NaN value reaches the tokens that see it, in its own dim.
  * Device checks: a table entry outside [0, num_pages) is recorded as
  * DSA_ERR_DEVICE_CHECK and its positions are left out; a request whose arrays
  * contradict the host sizes is recorded too and its rows are not written.

@@ -13,6 +13,8 @@ from test_gpu_paged_attention import BF16, DEV, F16, FP8, NAN, Case
 
 pytestmark = pytest.mark.gpu
 
+INF = float("inf")
+
 
 def tolerances(c, r):
     """(of out, of lse) for the reference r of case c."""
@@ -110,6 +112,46 @@ def test_scores_of_millions(dtype, kv):
         want = c.v[c.table[b, at // 64].long(), :, at % 64].float() * c.scales[1]
         want = want.repeat_interleave(2, dim=0)
         assert ((out[b].float() - want).abs() <= torch.finfo(dtype).eps * want.abs()).all()
+
+
+@pytest.mark.parametrize("lens,new,hq,hkv", [
+    ([200, 130, 67], [5, 3, 4], 8, 2),                       # clusters
+    ([200, 130, 67] * 60, [5, 3, 4] * 60, 8, 2),             # half-size CTAs, or the list
+    ([2900, 1300, 64, 700] * 12, [5, 2, 4, 1] * 12, 16, 4),  # the list
+    ([150, 90], [150, 60], 6, 2)])                           # a prompt
+@pytest.mark.parametrize("d,dtype,kv,bad", [
+    (64, BF16, BF16, NAN), (128, BF16, BF16, INF), (256, BF16, BF16, -INF), (64, F16, F16, -INF),
+    (128, F16, F16, NAN), (256, F16, F16, INF), (64, BF16, FP8, NAN), (128, F16, FP8, NAN),
+    (256, BF16, FP8, NAN)])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(lens, new, hq, hkv, d, dtype, kv,
+                                                                 bad):
+    """The last two new tokens' values (the last, of two; none, of one) are not finite in
+    two dims of each head.  Rows before them are as if they were not there."""
+    c = Case(lens, new, hq, hkv, d, dtype, kv, seed=43)
+    r = c.reference()
+    tol, lse_tol = tolerances(c, r)
+    want = r["out"].clone()
+    g = hq // hkv
+    v = c.v.float()
+    for b, (length, n) in enumerate(zip(lens, new)):
+        for at in range(max(length - 2, length - n + 1), length):
+            page = c.table[b, at // 64].long()
+            for h in range(hkv):
+                dims = [(5 * b + h) % d, (7 * h + at) % d]
+                v[page, h, at % 64, dims] = bad
+                first = c.offsets[b] + at - (length - n)  # the first row that sees it
+                for dim in dims:
+                    want[first:c.offsets[b + 1], h * g:(h + 1) * g, dim] = bad
+    c.v = v.to(kv)
+    out, lse = c.run()
+    out = out.double()
+    assert torch.equal(out.isnan(), want.isnan())
+    same = torch.isfinite(want)
+    assert torch.equal(torch.where(same | want.isnan(), 0.0, out),
+                       torch.where(same | want.isnan(), 0.0, want))
+    err = torch.where(same, out - want, 0.0).abs()
+    assert (err <= tol).all(), float((err / tol.clamp_min(1e-30)).max())
+    assert ((lse.double() - r["lse"]).abs() <= lse_tol).all()
 
 
 @pytest.mark.parametrize("kv", [BF16, FP8])
