@@ -172,6 +172,16 @@ bool row_ok(const void* p, int64_t stride, int64_t heads, int head_dim) {
     return p && aligned16(p) && stride % 8 == 0 && stride >= heads * head_dim;
 }
 
+// An array of `count` elements; whether two of them share bytes.
+struct Span {
+    uintptr_t begin, end;
+    Span(const void* p, int64_t count, size_t size)
+        : begin(reinterpret_cast<uintptr_t>(p)), end(p ? begin + (uintptr_t)count * size : begin) {}
+};
+bool overlap(const Span& a, const Span& b) {
+    return a.begin < b.end && b.begin < a.end && a.begin < a.end && b.begin < b.end;
+}
+
 constexpr int kMaxHeads = 1 << 14;  // query heads, and KV heads, of one layer
 
 }  // namespace
@@ -449,6 +459,18 @@ dsa_status dsa_build_tables(int32_t num_requests, const int32_t* cached_lens,
     if ((slots && !aligned16(slots)) || (positions && !aligned16(positions)) ||
         (token_requests && !aligned16(token_requests)))
         return DSA_ERR_INVALID_ARG;
+    // every CTA reads all lengths while others write: outputs (first) and inputs apart
+    const Span spans[] = {Span(block_table, (int64_t)num_requests * max_pages, 4),
+                          Span(q_offsets, (int64_t)num_requests + 1, 4),
+                          Span(seq_lens, num_requests, 4), Span(slots, max_tokens, 8),
+                          Span(positions, max_tokens, 4), Span(token_requests, max_tokens, 4),
+                          Span(pages_taken, 1, 4), Span(dev_status, 1, 4),
+                          Span(cached_lens, num_requests, 4), Span(new_lens, num_requests, 4),
+                          Span(free_pages, num_free, 4)};
+    constexpr int kOutputs = 8;
+    for (int i = 0; i < kOutputs; ++i)
+        for (int j = i + 1; j < (int)(sizeof(spans) / sizeof(spans[0])); ++j)
+            if (overlap(spans[i], spans[j])) return DSA_ERR_INVALID_ARG;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(launch_build_tables(num_requests, cached_lens, new_lens, free_pages,
                                            num_free, num_pages, max_pages, max_tokens, block_table,

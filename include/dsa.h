@@ -449,6 +449,9 @@ typedef struct {
  *   q_offsets [B+1], seq_lens [B], pages_taken [1] int32: outputs
  *   slots [max_tokens] int64, positions, token_requests [max_tokens] int32:
  *                          outputs, 16-byte aligned, each may be NULL
+ * Outputs overlap neither one another nor an input (DSA_ERR_INVALID_ARG): the
+ * next step's cached_lens may be this step's seq_lens, but its own seq_lens then
+ * go to another array.
  * B is at most 4096 (DSA_ERR_UNSUPPORTED above).  With the inputs unchanged the
  * call may be repeated: it writes the same values again.  One kernel launch.
  * Device checks, each recorded as DSA_ERR_DEVICE_CHECK in *dev_status:

@@ -127,3 +127,29 @@ def test_paged_attention_workspace_follows_rows_and_head_dim(lib):
     assert size(80, head_dim=256) == size(128, head_dim=256)
     assert size(4, head_dim=256) > size(4) > size(4, head_dim=64)
     assert size(5) == 0 and size(0) == 0 and size(4, head_dim=96) == 0
+
+
+# Arrays of a call for 2 requests, 8 free pages, 4 table columns and 16 tokens, apart.
+TABLE_ARRAYS = dict(cached=(4096, 8), new=(8192, 8), free=(12288, 32), table=(16384, 32),
+                    q_offsets=(20480, 12), seq_lens=(24576, 8), slots=(28672, 128),
+                    positions=(32768, 64), requests=(36864, 64), taken=(40960, 4),
+                    status=(45056, 4))
+TABLE_INPUTS = ("cached", "new", "free")
+
+
+@pytest.mark.parametrize("name", [n for n in TABLE_ARRAYS if n not in TABLE_INPUTS])
+@pytest.mark.parametrize("other", list(TABLE_ARRAYS))
+def test_build_tables_refuses_an_output_that_overlaps(lib, name, other):
+    """In place (seq_lens as cached_lens), whole or by an edge: CTAs would read what
+    others write."""
+    if name == other:
+        return
+    at, size = TABLE_ARRAYS[other]
+    own = TABLE_ARRAYS[name][1]
+    ends = [at] if name in ("slots", "positions", "requests") else [at, at + size - 4,
+                                                                    at - own + 4]
+    for begin in ends:
+        a = {n: ctypes.c_void_p(begin if n == name else TABLE_ARRAYS[n][0]) for n in TABLE_ARRAYS}
+        assert lib.dsa_build_tables(2, a["cached"], a["new"], a["free"], 8, 64, 4, 16, a["table"],
+                                    a["q_offsets"], a["seq_lens"], a["slots"], a["positions"],
+                                    a["requests"], a["taken"], a["status"], None) == INVALID
