@@ -532,6 +532,15 @@ def _sized(t, n, dtype, name):
     return _ptr(t, dtype, name)
 
 
+def _positions(t, axes, tokens):
+    """Pointer of positions [axes, tokens].  Axes are `tokens` apart, so with two or
+    more a wider buffer would be misread; one axis takes the first `tokens` of any."""
+    p = _sized(t, axes * tokens, torch.int32, "positions")
+    if t is not None and axes > 1 and t.dim() > 1 and t.shape[-1] != tokens:
+        raise ValueError("positions must be [%d, %d]" % (axes, tokens))
+    return p
+
+
 def prepare_build_tables(cached_lens, new_lens, free_pages, num_pages, block_table, q_offsets,
                          seq_lens, slots=None, positions=None, token_requests=None,
                          pages_taken=None, dev_status=None, stream=None):
@@ -585,7 +594,7 @@ def prepare_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_statu
         raise ValueError("q, k, v and q_out must have the same tokens")
     (kp, ks), (vp, vs), (qp, qs), (op, os_) = rows
     args = (tokens, cache.ref(), _FLOAT_FORMATS[dtype], rope.ref(),
-            _sized(positions, len(rope.sections) * tokens, torch.int32, "positions"),
+            _positions(positions, len(rope.sections), tokens),
             _sized(slots, tokens, torch.int64, "slots"), hq, qp, qs, kp, ks, vp, vs, op, os_,
             _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     keep = (cache, rope, positions, slots, q, k, v, q_out, dev_status, stream)
@@ -594,7 +603,8 @@ def prepare_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_statu
 
 def dsa_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_status=None, stream=None):
     """Rotary positions on q (into q_out) and k, and the write of k and v into
-    the cache at `slots` (see include/dsa.h).  positions: int32 [axes, tokens];
+    the cache at `slots` (see include/dsa.h).  positions: int32 [axes, tokens]
+    (of a wider buffer of several axes, a contiguous copy of its live part);
     q, k, v: [tokens, heads, head_dim], also as slices of a fused projection."""
     prepare_rope_append(cache, rope, positions, slots, q, k, v, q_out, dev_status, stream)()
 

@@ -170,3 +170,35 @@ def test_rows_that_see_nothing_are_zero_whatever_the_values(kv, copies):
         assert (out[blind] == 0).all() and torch.isneginf(lse[blind]).all()
         seeing = slice(blind.stop, c.offsets[b + 1])
         assert out[seeing].isnan().all() and torch.isfinite(lse[seeing]).all()
+
+
+@pytest.mark.parametrize("axes", [2, 3])
+def test_positions_of_another_shape_are_refused(axes):
+    """Axes are as far apart as there are tokens: of a wider buffer the second would be
+    read in the wrong place."""
+    tokens, sections = 6, [8] * axes
+    qkv = torch.randn(tokens, 8, 64, device=DEV).to(BF16)
+    q, k, v = qkv.split([4, 2, 2], dim=1)
+    pool = torch.zeros(2, 3, 2, 64, 64, dtype=BF16, device=DEV)
+    freq = torch.rand(8 * axes, dtype=torch.float64, device=DEV)
+    cache, rope = dsa.KvCache(pool[0], pool[1]), dsa.Rope(freq, sections)
+    slots = torch.arange(tokens, device=DEV)
+    out = torch.empty(tokens, 4, 64, dtype=BF16, device=DEV)
+    pos = torch.randint(0, 1000, (axes, 9), dtype=torch.int32, device=DEV)
+
+    def call(p):
+        dsa.dsa_rope_append(cache, rope, p, slots, q, k, v, out)
+        return out.clone()
+    for bad in (pos, pos.T.contiguous()[:tokens], pos[:, :tokens].T.contiguous(),
+                pos[:axes - 1, :tokens].contiguous()):
+        with pytest.raises(ValueError):
+            call(bad)
+    live = pos[:, :tokens].contiguous()
+    want = call(live)
+    more = torch.cat([live, live[:1]])  # axes that the heads do not use
+    for good in (live.view(-1), more, more.view(-1)):
+        assert torch.equal(call(good), want)
+    # one axis: the first of a larger buffer
+    rope = dsa.Rope(freq[:8])
+    want = call(live[:1])
+    assert torch.equal(call(pos[0]), want) and torch.equal(call(pos[:1]), want)
