@@ -532,6 +532,18 @@ def _sized(t, n, dtype, name):
     return _ptr(t, dtype, name)
 
 
+def _per_token(t, tokens, row, dtype, name):
+    """Pointer of an output with a row of this shape for each of `tokens` tokens or
+    more: [..., *row], the row flattened, or one flat array."""
+    n = 1
+    for size in row:
+        n *= size
+    p = _sized(t, tokens * n, dtype, name)
+    if t is not None and t.dim() > 1 and tuple(t.shape[-len(row):]) != row and t.shape[-1] != n:
+        raise ValueError("%s must be [%d, %s]" % (name, tokens, ", ".join(map(str, row))))
+    return p
+
+
 def _positions(t, axes, tokens):
     """Pointer of positions [axes, tokens].  Axes are `tokens` apart, so with two or
     more a wider buffer would be misread; one axis takes the first `tokens` of any."""
@@ -626,8 +638,8 @@ def prepare_paged_attention(batch, cache, q, sm_scale, out, lse=None, ws=None, d
     if q.shape[0] < tokens:
         raise ValueError("q has %d tokens, the batch %d" % (q.shape[0], tokens))
     args = (batch.ref(), cache.ref(), _FLOAT_FORMATS[q.dtype], hq, qp, qs, float(sm_scale),
-            _sized(out, tokens * hq * dim, q.dtype, "out"),
-            _sized(lse, tokens * hq, torch.float32, "lse"), _ptr(ws),
+            _per_token(out, tokens, (hq, dim), q.dtype, "out"),
+            _per_token(lse, tokens, (hq,), torch.float32, "lse"), _ptr(ws),
             0 if ws is None else ws.numel() * ws.element_size(),
             _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     keep = (batch, cache, q, out, lse, ws, dev_status, stream)

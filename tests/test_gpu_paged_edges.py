@@ -172,6 +172,30 @@ def test_rows_that_see_nothing_are_zero_whatever_the_values(kv, copies):
         assert out[seeing].isnan().all() and torch.isfinite(lse[seeing]).all()
 
 
+def test_buffers_of_another_shape_are_refused():
+    c = Case([300, 64], [1, 1], 4, 2, 64, BF16, seed=46)
+    batch, cache = c.batch(), c.cache()
+    ws = torch.empty(dsa.dsa_paged_attention_workspace_size(batch, cache, 4), dtype=torch.uint8,
+                     device=DEV)
+
+    def empty(*shape, dtype=BF16):
+        return torch.zeros(*shape, dtype=dtype, device=DEV)
+    want, want_lse = c.run()
+    for out, lse in ((empty(2, 4, 64), empty(2, 4, dtype=torch.float32)),
+                     (empty(5, 4, 64), empty(5, 4, dtype=torch.float32)),      # a larger capacity
+                     (empty(2, 256), empty(8, dtype=torch.float32)),           # heads flattened
+                     (empty(600), empty(11, dtype=torch.float32))):            # flat
+        dsa.dsa_paged_attention(batch, cache, c.q, c.sm_scale, out, lse, ws)
+        assert torch.equal(out.view(-1)[:512], want.view(-1))
+        assert torch.equal(lse.view(-1)[:8], want_lse.view(-1))
+    for out, lse in ((empty(2, 64, 4), None), (empty(4, 2, 64), None), (empty(2, 8, 64), None),
+                     (empty(2, 512), None),
+                     (empty(2, 4, 64), empty(4, 2, dtype=torch.float32)),
+                     (empty(2, 4, 64), empty(2, 8, dtype=torch.float32))):
+        with pytest.raises(ValueError):
+            dsa.dsa_paged_attention(batch, cache, c.q, c.sm_scale, out, lse, ws)
+
+
 @pytest.mark.parametrize("axes", [2, 3])
 def test_positions_of_another_shape_are_refused(axes):
     """Axes are as far apart as there are tokens: of a wider buffer the second would be
