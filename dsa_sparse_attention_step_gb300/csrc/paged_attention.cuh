@@ -670,12 +670,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         if (me == 0 && lane == 0 && !C::kDirect)
             p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
-        if (lane == 0 && *abort_flag) {
-            // an unwinding CTA must not exit under copies in flight
+        if (lane == 0) {
+            // the CTA must not exit under copies in flight, which it would if a consumer
+            // gave up after the last page had been issued: wait for what was issued last
             for (int i = n - C::kProducers; i >= 0 && i > n - C::kProducers - C::kStages;
                  i -= C::kProducers)
                 mbar_drain(&s_full[i % C::kFull], (i / C::kFull) & 1);
-            record_error(p.status, DSA_ERR_TIMEOUT);
+            if (*abort_flag) record_error(p.status, DSA_ERR_TIMEOUT);
         }
         return;
     }
