@@ -60,6 +60,7 @@ cudaError_t launch_rope_append(int num_tokens, const dsa_kv_cache& cache, int fo
                                int32_t* status, cudaStream_t stream);
 
 bool paged_attention_supported(const BatchArgs& bt, int kv_heads, int group);
+float paged_score_scale(float sm_scale, const dsa_kv_cache& cache);
 size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim);
 cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
@@ -537,6 +538,7 @@ static dsa_status paged_attention(const dsa_batch* batch, const dsa_kv_cache* ca
         !paged_attention_supported(to_args(batch), cache->num_kv_heads, group))
         return DSA_ERR_UNSUPPORTED;
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+    if (!std::isnormal(paged_score_scale(sm_scale, *cache))) return DSA_ERR_INVALID_ARG;
     if (batch->total_q == 0) return DSA_OK;
     if (!row_ok(q, q_stride, num_q_heads, cache->head_dim) || !out || !aligned16(out))
         return DSA_ERR_INVALID_ARG;

@@ -19,6 +19,11 @@ bool paged_attention_supported(const BatchArgs& bt, int kv_heads, int group) {
     return most_units(bt, kv_heads, group, 16) * (tiles + 1 + 8) < 2147483648.0;
 }
 
+// The factor of q . k codes, in units of log2.
+float paged_score_scale(float sm_scale, const dsa_kv_cache& cache) {
+    return sm_scale * cache.k_scale * kLog2e;
+}
+
 // Of the default plan, which needs more than the whole one.
 size_t paged_attention_workspace_bytes(int64_t max_rows, int head_dim) {
     return ws_layout(head_dim, row_tile(head_dim, max_rows, false)).total;
@@ -42,7 +47,7 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
     p.v_pages = cache.v_pages;
     p.out = out;
     p.lse = lse;
-    p.score_scale = sm_scale * cache.k_scale * kLog2e;
+    p.score_scale = paged_score_scale(sm_scale, cache);
     p.v_scale = cache.v_scale;
     const WsLayout w = ws_layout(
         cache.head_dim, row_tile(cache.head_dim, (int64_t)bt.max_q * p.group, false));

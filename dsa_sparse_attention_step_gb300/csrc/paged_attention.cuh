@@ -773,7 +773,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 float up = 1.f;
                 if (e >= 64 && e < 254) {
                     up = __uint_as_float((254 - e) << 23);
-                    factor *= __uint_as_float(e << 23);
+                    // (not below fp32's normal range, where the scores are 0 anyway: a
+                    // factor of 0 would make NaN of a masked -inf)
+                    factor = fmaxf(factor * __uint_as_float(e << 23), 0x1p-126f);
                 }
 #pragma unroll
                 for (int i = 0; i < kWords; ++i)

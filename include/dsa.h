@@ -537,6 +537,8 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
  * Device checks: a table entry outside [0, num_pages) is recorded as
  * DSA_ERR_DEVICE_CHECK and its positions are left out; a request whose arrays
  * contradict the host sizes is recorded too and its rows are not written.
+ * sm_scale is finite and > 0, and sm_scale * k_scale * log2 e a normal fp32 number
+ * (DSA_ERR_INVALID_ARG).
  * batch->num_pages must equal cache->num_pages.  Under
  * dsa_set_batch_invariant each (request, KV head) runs whole, as a token does in
  * dsa_sparse_mla.  One or two kernel launches. */

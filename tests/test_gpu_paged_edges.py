@@ -172,6 +172,16 @@ def test_rows_that_see_nothing_are_zero_whatever_the_values(kv, copies):
         assert out[seeing].isnan().all() and torch.isfinite(lse[seeing]).all()
 
 
+def test_scale_factors_below_fp32s_range():
+    """bf16 queries of 2^-60 over FP8 keys under sm_scale 2^-100: all scores are 0, and
+    positions past a row's view stay masked."""
+    c = Case([200, 90], [3, 1], 4, 2, 64, BF16, FP8, seed=45)
+    c.q *= 2.0**-60
+    c.sm_scale = 2.0**-100
+    out, lse = c.run()
+    c.check(out, lse)
+
+
 def test_buffers_of_another_shape_are_refused():
     c = Case([300, 64], [1, 1], 4, 2, 64, BF16, seed=46)
     batch, cache = c.batch(), c.cache()

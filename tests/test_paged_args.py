@@ -153,3 +153,8 @@ def test_build_tables_refuses_an_output_that_overlaps(lib, name, other):
         assert lib.dsa_build_tables(2, a["cached"], a["new"], a["free"], 8, 64, 4, 16, a["table"],
                                     a["q_offsets"], a["seq_lens"], a["slots"], a["positions"],
                                     a["requests"], a["taken"], a["status"], None) == INVALID
+
+
+@pytest.mark.parametrize("sm,k_scale", [(1e-25, 1e-25), (1e30, 1e30), (1e-38, 1e-3)])
+def test_paged_attention_refuses_score_factors_outside_fp32(lib, sm, k_scale):
+    assert _attention(lib, cache=_cache(format=2, k_scale=k_scale), sm=sm) == INVALID
