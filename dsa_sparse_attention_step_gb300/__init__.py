@@ -466,7 +466,7 @@ def dsa_append_cache(batch, new_keys, new_latent, kv_scale, index_pages, latent_
     _check(rc, "dsa_append_cache")
 
 
-# ---- dense attention over the same pages ----------------------------------------
+# ---- dense attention over paged keys and values ---------------------------------
 
 _FLOAT_FORMATS = {torch.bfloat16: 0, torch.float16: 1}
 _KV_FORMATS = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
@@ -583,7 +583,8 @@ def dsa_build_tables(cached_lens, new_lens, free_pages, num_pages, block_table, 
                      dev_status=None, stream=None):
     """Block table, query offsets, lengths and per-token cache slots of a step
     from the requests' cached and new lengths (see include/dsa.h).  The
-    capacity for tokens is the length of the per-token outputs given."""
+    capacity for tokens is the length of the shortest per-token output given;
+    pages_taken has to be given; outputs overlap nothing."""
     prepare_build_tables(cached_lens, new_lens, free_pages, num_pages, block_table, q_offsets,
                          seq_lens, slots, positions, token_requests, pages_taken, dev_status,
                          stream)()

@@ -9,8 +9,8 @@
 // lengths, read through L2) and keeps them in shared memory, then fills its own
 // tiles of tokens and its share of the new pages.  That repeats up to 32 KB of reads
 // per CTA but needs one launch and no ordering between CTAs.  A warp writes 64
-// consecutive tokens, two a lane so that all stores are whole 16-byte words; it
-// looks its request up once where one request holds them all.
+// consecutive tokens, two a lane (a 16-byte store of slots, 8-byte ones of positions
+// and requests); it looks its request up once where one request holds them all.
 //
 // Bound by latency up to some 100,000 tokens, then by the writes of 16 bytes a token.
 #include "common.cuh"

@@ -26,11 +26,11 @@
 // be seven eighths empty, and the fragments' register layout lets P go from scores
 // to operand without leaving the registers.  FP8 keys and values are lifted to f16
 // exactly; bf16 queries then are scaled by a power of two per row, so that f16 holds
-// them.
+// them.  f16 probabilities are held at 2^15 times their size.
 //
-// Measured: one token over 2^20 positions of 32/8 heads of 128, bf16, 592 us, 7.25
-// TB/s; 64 ragged FP8 requests, 64/8 heads, 334 us, 6.76 TB/s; five tokens to verify
-// in each of 16 requests of up to 131072, 583 us, 6.78 TB/s.
+// Measured: one token over 2^20 positions of 32/8 heads of 128, bf16, 593 us, 7.24
+// TB/s; 64 ragged FP8 requests, 64/8 heads, 335 us, 6.74 TB/s; five tokens to verify
+// in each of 16 requests of up to 131072, 587 us, 6.74 TB/s.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -961,8 +961,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         m[0] = top[0];
                         m[1] = top[1];
                     }
-                    // P rounded to the operand type, by half a step at most: 2^-9 of a
-                    // probability in bf16, 2^-12 in f16 (2^-40 of the row's largest for
+                    // P rounded to the operand type, by half a step at most: 2^-8 of a
+                    // probability in bf16, 2^-11 in f16 (2^-40 of the row's largest for
                     // those below 2^-29 of it).  The sums are of the unrounded values.
                     uint32_t pf[C::kSub / 16][4];
                     const float b0 = __fsub_ru(base_of(m[0]), kPExp);

@@ -132,7 +132,8 @@ uint64_t dsa_launch_count(void);
  * token depend on its own inputs alone, and equal the default plan's wherever
  * that plan runs the token whole.  Small batches then use fewer SMs.
  * Process-wide; read once by each later call of dsa_sparse_mla(_ex),
- * dsa_decode(_ex), dsa_decode_noalloc and dsa_paged_attention (see there).  Workspace sizes do not change.
+ * dsa_decode(_ex) and dsa_decode_noalloc, and by dsa_paged_attention, whose
+ * default plan differs (see there).  Workspace sizes do not change.
  * Returns the previous setting (0 or 1); the default is 0. */
 int32_t dsa_set_batch_invariant(int32_t enabled);
 
@@ -392,7 +393,7 @@ int32_t dsa_plan_token_shards(const int32_t* seq_lens, const int32_t* q_counts,
                               int32_t num_requests, int32_t world, int32_t rank,
                               dsa_shard_part* parts, int32_t max_parts);
 
-/* ---- dense attention over the same pages ------------------------------------------
+/* ---- dense attention over paged keys and values -----------------------------------
  * No counterpart on the pages: an addition of this library, for the layers of a
  * model that attend to every cached position (a draft model, a dense layer)
  * and for building the batch metadata of every other call on the GPU.  The
@@ -520,11 +521,18 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
  *   lse[t,i]   = log sum_s exp(z[s])          (natural log)
  * The new tokens' own keys and values must be in the cache already.  Any n_b
  * is taken; the kernel is made for decode and verification steps (a few
- * tokens per request).  DSA_ERR_UNSUPPORTED where the host sizes allow more than
- * about 2^31 pairs of 16 query rows and a page of keys.
+ * tokens per request), and the largest request sets the row tile of all, so a
+ * prompt chunk slows the one-token requests beside it.  DSA_ERR_UNSUPPORTED
+ * where the host sizes allow more than about 2^31 pairs of 16 query rows and a
+ * page of keys.
+ * Scores, maxima and sums are fp32.  The probabilities are rounded to bf16 for a
+ * bf16 cache and to f16 for the others before they meet the values: half a step
+ * each, at most 2^-8 and 2^-11 of a probability (in f16, of those below 2^-29 of
+ * the row's largest, 2^-40 of that).
  *   q    [T, num_q_heads, head_dim] of `format`, tokens q_stride elements apart
  *        (a multiple of 8), 16-byte aligned
- *   out  [T, num_q_heads, head_dim] of `format`, contiguous, 16-byte aligned
+ *   out  [T, num_q_heads, head_dim] of `format`, contiguous, 16-byte aligned;
+ *        overlaps no input
  *   lse  [T, num_q_heads] fp32 (may be NULL)
  *   ws   device scratch of dsa_paged_attention_workspace_size() bytes, 16-byte
  *        aligned; its contents need not be kept between calls
@@ -539,9 +547,12 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
  * contradict the host sizes is recorded too and its rows are not written.
  * sm_scale is finite and > 0, and sm_scale * k_scale * log2 e a normal fp32 number
  * (DSA_ERR_INVALID_ARG).
- * batch->num_pages must equal cache->num_pages.  Under
- * dsa_set_batch_invariant each (request, KV head) runs whole, as a token does in
- * dsa_sparse_mla.  One or two kernel launches. */
+ * batch->num_pages must equal cache->num_pages.  Rows of q that no request owns
+ * are not written.  One or two kernel launches.
+ * Under dsa_set_batch_invariant each (request, 16 rows, KV head) runs whole, with
+ * the same work per warp whatever the batch: a request's out and lse then do not
+ * depend on the other requests.  They need not equal the default plan's, which
+ * has other row tiles, to the last bit. */
 size_t dsa_paged_attention_workspace_size(const dsa_batch* batch, const dsa_kv_cache* cache,
                                           int32_t num_q_heads);
 dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache,
