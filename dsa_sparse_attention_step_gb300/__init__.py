@@ -23,7 +23,9 @@ __all__ = ["DsaError", "Batch", "KEYS_FP8", "KEYS_MXFP4", "TOPK", "library_path"
            "prepare_decode", "prepare_append_cache", "KvCache", "Rope", "dsa_build_tables",
            "prepare_build_tables", "dsa_rope_append", "prepare_rope_append",
            "dsa_paged_attention", "dsa_paged_attention_workspace_size",
-           "prepare_paged_attention"]
+           "prepare_paged_attention", "QuantCache", "dsa_quant_append", "prepare_quant_append",
+           "dsa_quant_read", "prepare_quant_read", "dsa_quant_attention",
+           "dsa_quant_attention_workspace_size", "prepare_quant_attention"]
 
 KEYS_FP8 = 0
 KEYS_MXFP4 = 1
@@ -74,6 +76,13 @@ class _CKvCache(ctypes.Structure):
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class _CQuantCache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
 class _CRope(ctypes.Structure):
     _fields_ = [("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3),
                 ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p)]
@@ -86,6 +95,7 @@ _f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 _bp = ctypes.POINTER(_CBatch)
 _kp = ctypes.POINTER(_CKvCache)
+_qp = ctypes.POINTER(_CQuantCache)
 
 _SIGS = {
     "dsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -123,6 +133,13 @@ _SIGS = {
                                        _vp]),
     "dsa_paged_attention_workspace_size": (_sz, [_bp, _kp, _i32]),
     "dsa_paged_attention": (ctypes.c_int, [_bp, _kp, ctypes.c_int, _i32, _vp, _i64, _f32, _vp, _vp,
+                                           _vp, _sz, _vp, _vp]),
+    "dsa_quant_append": (ctypes.c_int, [_i32, _qp, ctypes.c_int, ctypes.POINTER(_CRope), _vp, _vp,
+                                        _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                        _vp]),
+    "dsa_quant_read": (ctypes.c_int, [_bp, _qp, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "dsa_quant_attention_workspace_size": (_sz, [_bp, _qp, _i32]),
+    "dsa_quant_attention": (ctypes.c_int, [_bp, _qp, ctypes.c_int, _i32, _vp, _i64, _f32, _vp, _vp,
                                            _vp, _sz, _vp, _vp]),
     "dsa_test_paged_attention_wait_timeout": (ctypes.c_int, [
         _bp, _kp, ctypes.c_int, _i32, _vp, _i64, _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
@@ -661,3 +678,127 @@ def dsa_test_paged_attention_wait_timeout(batch, cache, q, sm_scale, out, lse=No
     call = prepare_paged_attention(batch, cache, q, sm_scale, out, lse, ws, dev_status, stream)
     _check(load().dsa_test_paged_attention_wait_timeout(*call._args),
            "dsa_test_paged_attention_wait_timeout")
+
+
+# ---- an 8-bit cache whose scales follow the data ---------------------------------
+
+_QUANT_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_QUANT_BLOCK = 16
+
+
+class QuantCache:
+    """One layer's paged keys and values in 8 bits (dsa_quant_cache): two CUDA tensors
+    [num_pages, num_kv_heads, 64, head_dim], float8_e4m3fn or int8, and their scales,
+    float32 [num_pages, num_kv_heads, 2, 4], one for every 16 tokens of a head (keys',
+    then values').  Nothing needs to be initialised: a block's scale is set when its
+    first token is written."""
+
+    def __init__(self, k_pages, v_pages, scales):
+        if k_pages.dim() != 4 or k_pages.shape[2] != PAGE or k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must be [num_pages, num_kv_heads, 64, head_dim]")
+        if k_pages.dtype not in _QUANT_FORMATS:
+            raise TypeError("k_pages has dtype %s" % k_pages.dtype)
+        if tuple(scales.shape) != (*k_pages.shape[:2], 2, PAGE // _QUANT_BLOCK):
+            raise ValueError("scales must be [num_pages, num_kv_heads, 2, 4]")
+        self.k_pages, self.v_pages, self.scales = k_pages, v_pages, scales
+        self.num_pages, self.num_kv_heads, _, self.head_dim = k_pages.shape
+        self._c = _CQuantCache(self.num_pages, self.num_kv_heads, self.head_dim,
+                               _QUANT_FORMATS[k_pages.dtype], _ptr(k_pages, None, "k_pages"),
+                               _ptr(v_pages, k_pages.dtype, "v_pages"),
+                               _ptr(scales, torch.float32, "scales"))
+
+    def ref(self):
+        return ctypes.byref(self._c)
+
+
+def prepare_quant_append(cache, rope, positions, slots, q, k, v, q_out, dev_status=None,
+                         stream=None):
+    """dsa_quant_append as a PreparedCall (same arguments)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    dtype, tokens, dim = k.dtype, k.shape[0], cache.head_dim
+    if dtype not in _FLOAT_FORMATS:
+        raise TypeError("k has dtype %s" % dtype)
+    hq = 0 if q is None else q.shape[1]
+    rows = [_rows(k, cache.num_kv_heads, dim, dtype, "k"),
+            _rows(v, cache.num_kv_heads, dim, dtype, "v")]
+    rows += [(None, 0)] * 2 if q is None else [_rows(q, hq, dim, dtype, "q"),
+                                               _rows(q_out, hq, dim, dtype, "q_out")]
+    if any(x is not None and x.shape[0] != tokens for x in (q, v, q_out)):
+        raise ValueError("q, k, v and q_out must have the same tokens")
+    (kp, ks), (vp, vs), (qp, qs), (op, os_) = rows
+    c_rope = _CRope(0, (ctypes.c_int32 * 3)(0, 0, 0), 0, None) if rope is None else rope._c
+    axes = 0 if rope is None else len(rope.sections)
+    args = (tokens, cache.ref(), _FLOAT_FORMATS[dtype], ctypes.byref(c_rope),
+            None if rope is None else _positions(positions, axes, tokens),
+            _sized(slots, tokens, torch.int64, "slots"), hq, qp, qs, kp, ks, vp, vs, op, os_,
+            _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    keep = (cache, rope, c_rope, positions, slots, q, k, v, q_out, dev_status, stream)
+    return PreparedCall("dsa_quant_append", load().dsa_quant_append, args, keep)
+
+
+def dsa_quant_append(cache, rope, positions, slots, q, k, v, q_out, dev_status=None, stream=None):
+    """Rotary positions on q (into q_out) and k (rope None: none), and the write of k
+    and v into the 8-bit cache at `slots` with the scales that they need (see
+    include/dsa.h).  Arguments as dsa_rope_append; tokens of one block of 16 stand next to
+    each other, their slots ascending, as dsa_build_tables makes them."""
+    prepare_quant_append(cache, rope, positions, slots, q, k, v, q_out, dev_status, stream)()
+
+
+def prepare_quant_read(batch, cache, k_out, v_out, dev_status=None, stream=None):
+    """dsa_quant_read as a PreparedCall (same arguments)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    outs = [x for x in (k_out, v_out) if x is not None]
+    if not outs:
+        raise ValueError("k_out or v_out must be given")
+    dtype, tokens = outs[0].dtype, batch.total_q
+    if dtype not in _FLOAT_FORMATS:
+        raise TypeError("k_out has dtype %s" % dtype)
+    if any(x.shape[0] < tokens for x in outs):
+        raise ValueError("the batch has %d tokens, the outputs fewer" % tokens)
+    (kp, ks), (vp, vs) = [
+        (None, 0) if x is None else _rows(x, cache.num_kv_heads, cache.head_dim, dtype, name)
+        for x, name in ((k_out, "k_out"), (v_out, "v_out"))]
+    args = (batch.ref(), cache.ref(), _FLOAT_FORMATS[dtype], kp, ks, vp, vs,
+            _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    keep = (batch, cache, k_out, v_out, dev_status, stream)
+    return PreparedCall("dsa_quant_read", load().dsa_quant_read, args, keep)
+
+
+def dsa_quant_read(batch, cache, k_out, v_out, dev_status=None, stream=None):
+    """The cached keys and values of the batch's tokens (each request's last ones) as rows
+    of k_out and v_out [tokens, num_kv_heads, head_dim], either of them None to leave it
+    out (see include/dsa.h)."""
+    prepare_quant_read(batch, cache, k_out, v_out, dev_status, stream)()
+
+
+def dsa_quant_attention_workspace_size(batch, cache, num_q_heads):
+    return int(load().dsa_quant_attention_workspace_size(batch.ref(), cache.ref(),
+                                                         int(num_q_heads)))
+
+
+def prepare_quant_attention(batch, cache, q, sm_scale, out, lse=None, ws=None, dev_status=None,
+                            stream=None):
+    """dsa_quant_attention as a PreparedCall (same arguments)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    if q.dtype not in _FLOAT_FORMATS:
+        raise TypeError("q has dtype %s" % q.dtype)
+    hq, dim, tokens = q.shape[1], cache.head_dim, batch.total_q
+    qp, qs = _rows(q, hq, dim, q.dtype, "q")
+    if q.shape[0] < tokens:
+        raise ValueError("q has %d tokens, the batch %d" % (q.shape[0], tokens))
+    args = (batch.ref(), cache.ref(), _FLOAT_FORMATS[q.dtype], hq, qp, qs, float(sm_scale),
+            _per_token(out, tokens, (hq, dim), q.dtype, "out"),
+            _per_token(lse, tokens, (hq,), torch.float32, "lse"), _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(),
+            _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    keep = (batch, cache, q, out, lse, ws, dev_status, stream)
+    return PreparedCall("dsa_quant_attention", load().dsa_quant_attention, args, keep)
+
+
+def dsa_quant_attention(batch, cache, q, sm_scale, out, lse=None, ws=None, dev_status=None,
+                        stream=None):
+    """dsa_paged_attention over a QuantCache (see include/dsa.h)."""
+    prepare_quant_attention(batch, cache, q, sm_scale, out, lse, ws, dev_status, stream)()

@@ -68,6 +68,21 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
                                    bool wait_test, int32_t* status, int* launches,
                                    cudaStream_t stream);
 
+cudaError_t launch_quant_append(int num_tokens, const dsa_quant_cache& cache, int format,
+                                const dsa_rope& rope, const int32_t* positions,
+                                const int64_t* slots, int num_q_heads, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, void* q_out, int64_t q_out_stride,
+                                int32_t* status, cudaStream_t stream);
+cudaError_t launch_quant_read(const BatchArgs& bt, const dsa_quant_cache& cache, int format,
+                              void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                              int32_t* status, cudaStream_t stream);
+float quant_score_scale(float sm_scale);
+cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& cache, int format,
+                                   int num_q_heads, const void* q, int64_t q_stride,
+                                   float sm_scale, void* out, float* lse, void* ws, bool whole,
+                                   int32_t* status, int* launches, cudaStream_t stream);
+
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int32_t> g_batch_invariant{0};  // dsa_set_batch_invariant
 }  // namespace dsa
@@ -164,6 +179,33 @@ dsa_status check_kv_cache(const dsa_kv_cache* c, dsa_float_format format) {
         !std::isfinite(c->v_scale))
         return DSA_ERR_INVALID_ARG;
     if (c->format != DSA_KV_FP8_E4M3 && (c->k_scale != 1.f || c->v_scale != 1.f))
+        return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+// Rotary positions that a head of these dims has room for; their pairs in *pairs.
+dsa_status check_rope(const dsa_rope* rope, int head_dim, int64_t* pairs) {
+    if (rope == nullptr) return DSA_ERR_INVALID_ARG;
+    if (rope->num_axes < 0 || rope->num_axes > 3) return DSA_ERR_UNSUPPORTED;
+    *pairs = 0;
+    for (int i = 0; i < rope->num_axes; ++i) {
+        if (rope->sections[i] < 0) return DSA_ERR_INVALID_ARG;
+        *pairs += rope->sections[i];
+    }
+    if (2 * *pairs > head_dim) return DSA_ERR_INVALID_ARG;
+    return *pairs % 8 != 0 ? DSA_ERR_UNSUPPORTED : DSA_OK;
+}
+
+dsa_status check_quant_cache(const dsa_quant_cache* c, dsa_float_format format) {
+    if (c == nullptr) return DSA_ERR_INVALID_ARG;
+    if (format != DSA_FLOAT_BF16 && format != DSA_FLOAT_F16) return DSA_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DSA_ERR_UNSUPPORTED;
+    if (c->format != DSA_QUANT_E4M3 && c->format != DSA_QUANT_INT8) return DSA_ERR_UNSUPPORTED;
+    if (c->num_pages < 1 || c->num_kv_heads < 1 ||
+        (int64_t)c->num_pages * c->num_kv_heads > INT32_MAX)
+        return DSA_ERR_INVALID_ARG;
+    if (!c->k_pages || !c->v_pages || !c->scales || !aligned16(c->k_pages) ||
+        !aligned16(c->v_pages) || !aligned16(c->scales))
         return DSA_ERR_INVALID_ARG;
     return DSA_OK;
 }
@@ -488,14 +530,9 @@ dsa_status dsa_rope_append(int32_t num_tokens, const dsa_kv_cache* cache, dsa_fl
     if (st != DSA_OK) return st;
     if (rope == nullptr || num_tokens < 0 || num_q_heads < 0) return DSA_ERR_INVALID_ARG;
     if (num_q_heads > kMaxHeads || cache->num_kv_heads > kMaxHeads) return DSA_ERR_UNSUPPORTED;
-    if (rope->num_axes < 0 || rope->num_axes > 3) return DSA_ERR_UNSUPPORTED;
     int64_t pairs = 0;
-    for (int i = 0; i < rope->num_axes; ++i) {
-        if (rope->sections[i] < 0) return DSA_ERR_INVALID_ARG;
-        pairs += rope->sections[i];
-    }
-    if (2 * pairs > cache->head_dim) return DSA_ERR_INVALID_ARG;
-    if (pairs % 8 != 0) return DSA_ERR_UNSUPPORTED;
+    const dsa_status rope_st = check_rope(rope, cache->head_dim, &pairs);
+    if (rope_st != DSA_OK) return rope_st;
     if (num_tokens == 0) return DSA_OK;
     if ((pairs > 0 && (!rope->inv_freq || !positions)) || !slots) return DSA_ERR_INVALID_ARG;
     const int dim = cache->head_dim;
@@ -570,6 +607,97 @@ dsa_status dsa_test_paged_attention_wait_timeout(const dsa_batch* batch, const d
                                                  int32_t* dev_status, dsa_stream_t stream) {
     return paged_attention(batch, cache, format, num_q_heads, q, q_stride, sm_scale, out, lse, ws,
                            ws_bytes, true, dev_status, stream);
+}
+
+dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
+                            dsa_float_format format, const dsa_rope* rope,
+                            const int32_t* positions, const int64_t* slots, int32_t num_q_heads,
+                            const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                            int32_t* dev_status, dsa_stream_t stream) {
+    dsa_status st = check_quant_cache(cache, format);
+    if (st != DSA_OK) return st;
+    if (num_tokens < 0 || num_q_heads < 0) return DSA_ERR_INVALID_ARG;
+    if (num_q_heads > kMaxHeads || cache->num_kv_heads > kMaxHeads) return DSA_ERR_UNSUPPORTED;
+    const int dim = cache->head_dim;
+    int64_t pairs = 0;
+    st = check_rope(rope, dim, &pairs);
+    if (st != DSA_OK) return st;
+    if (num_tokens == 0) return DSA_OK;
+    if ((pairs > 0 && (!rope->inv_freq || !positions)) || !slots) return DSA_ERR_INVALID_ARG;
+    if (!row_ok(k, k_stride, cache->num_kv_heads, dim) ||
+        !row_ok(v, v_stride, cache->num_kv_heads, dim))
+        return DSA_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (!row_ok(q, q_stride, num_q_heads, dim) ||
+                            !row_ok(q_out, q_out_stride, num_q_heads, dim)))
+        return DSA_ERR_INVALID_ARG;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(launch_quant_append(num_tokens, *cache, (int)format, *rope, positions,
+                                           slots, num_q_heads, q, q_stride, k, k_stride, v,
+                                           v_stride, q_out, q_out_stride, dev_status,
+                                           (cudaStream_t)stream));
+}
+
+dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
+                          dsa_float_format format, void* k_out, int64_t k_stride, void* v_out,
+                          int64_t v_stride, int32_t* dev_status, dsa_stream_t stream) {
+    dsa_status st = check_batch(batch, true);
+    if (st != DSA_OK) return st;
+    st = check_quant_cache(cache, format);
+    if (st != DSA_OK) return st;
+    if (batch->num_pages != cache->num_pages) return DSA_ERR_INVALID_ARG;
+    if (cache->num_kv_heads > kMaxHeads) return DSA_ERR_UNSUPPORTED;
+    const int heads = cache->num_kv_heads, dim = cache->head_dim;
+    if ((k_out && !row_ok(k_out, k_stride, heads, dim)) ||
+        (v_out && !row_ok(v_out, v_stride, heads, dim)))
+        return DSA_ERR_INVALID_ARG;
+    if (batch->total_q == 0 || (!k_out && !v_out)) return DSA_OK;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(launch_quant_read(to_args(batch), *cache, (int)format, k_out, k_stride,
+                                         v_out, v_stride, dev_status, (cudaStream_t)stream));
+}
+
+size_t dsa_quant_attention_workspace_size(const dsa_batch* batch, const dsa_quant_cache* cache,
+                                          int32_t num_q_heads) {
+    if (check_batch(batch, true) != DSA_OK || cache == nullptr || cache->num_kv_heads < 1 ||
+        num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0 ||
+        (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256))
+        return 0;
+    return paged_attention_workspace_bytes(
+        (int64_t)batch->max_q_per_request * (num_q_heads / cache->num_kv_heads), cache->head_dim);
+}
+
+dsa_status dsa_quant_attention(const dsa_batch* batch, const dsa_quant_cache* cache,
+                               dsa_float_format format, int32_t num_q_heads, const void* q,
+                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream) {
+    dsa_status st = check_batch(batch, true);
+    if (st != DSA_OK) return st;
+    st = check_quant_cache(cache, format);
+    if (st != DSA_OK) return st;
+    if (num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0 ||
+        batch->num_pages != cache->num_pages)
+        return DSA_ERR_INVALID_ARG;
+    const int group = num_q_heads / cache->num_kv_heads;
+    if (num_q_heads > kMaxHeads || (int64_t)batch->max_q_per_request * group > (1 << 30) ||
+        !paged_attention_supported(to_args(batch), cache->num_kv_heads, group))
+        return DSA_ERR_UNSUPPORTED;
+    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale) ||
+        !std::isnormal(quant_score_scale(sm_scale)))
+        return DSA_ERR_INVALID_ARG;
+    if (batch->total_q == 0) return DSA_OK;
+    if (!row_ok(q, q_stride, num_q_heads, cache->head_dim) || !out || !aligned16(out))
+        return DSA_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) ||
+        ws_bytes < dsa_quant_attention_workspace_size(batch, cache, num_q_heads))
+        return DSA_ERR_WORKSPACE;
+    const bool whole = g_batch_invariant.load(std::memory_order_relaxed) != 0;
+    int launches = 0;
+    const dsa_status rc = cuda_status(launch_quant_attention(
+        to_args(batch), *cache, (int)format, num_q_heads, q, q_stride, sm_scale, out, lse, ws,
+        whole, dev_status, &launches, (cudaStream_t)stream));
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    return rc;
 }
 
 }  // extern "C"

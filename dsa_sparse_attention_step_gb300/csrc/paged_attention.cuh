@@ -26,7 +26,9 @@
 // be seven eighths empty, and the fragments' register layout lets P go from scores
 // to operand without leaving the registers.  FP8 keys and values are lifted to f16
 // exactly; bf16 queries then are scaled by a power of two per row, so that f16 holds
-// them.  f16 probabilities are held at 2^15 times their size.
+// them.  f16 probabilities are held at 2^15 times their size.  So are INT8 codes, and
+// caches whose codes have a scale for every 16 tokens (kCode) bring the scales with each
+// page: the keys' multiply the scores, the values' go into the exponent.
 //
 // Measured: one token over 2^20 positions of 32/8 heads of 128, bf16, 593 us, 7.24
 // TB/s; 64 ragged FP8 requests, 64/8 heads, 335 us, 6.74 TB/s; five tokens to verify
@@ -61,6 +63,7 @@ struct AttnParams {
     int64_t q_stride;
     const void* q;
     const void* v_pages;
+    const float* scales;  // [pages][KV heads][2][4]: of 16 tokens' keys and values (kCode)
     void* out;
     float* lse;
     float score_scale;  // sm_scale * k_scale * log2 e
@@ -75,18 +78,27 @@ struct AttnParams {
 // The first four are read as one vector.
 enum { kJoinPieces, kJoinToken, kJoinRow, kJoinRows, kJoinHead, kJoinInts = 8 };
 
+// How a cache holds its elements: by the configuration's kFp8 with one scale for all, or
+// as 8-bit codes with a scale for every 16 tokens.
+enum { kCodePlain, kCodeE4m3, kCodeInt8 };
+constexpr int kBlock = DSA_QUANT_BLOCK;
+constexpr float kMinBlockScale = 0x1p-48f, kMaxBlockScale = 0x1p33f;
+
 // The consumer warps: kNG groups, each taking every kNG-th page of the CTA's run;
 // within a group kWM warps along the rows (16 each) by kWN warps along the page's
 // tokens.  8 or 12 warps, or 4 of each of an SM's two CTAs, as many as the
 // accumulators' registers allow: a warp's softmax is a chain of dependent
 // instructions, and only other warps fill its gaps.
+// kKvFp8: elements of one byte, lifted to f16.
 template <int kD, bool kKvFp8, int kWM_, int kWN_, int kNG_, bool kDirect_ = false,
-          int kCtas_ = 1>
+          int kCtas_ = 1, int kCode_ = kCodePlain>
 struct AttnCfg {
     static constexpr int kDim = kD;
     static constexpr bool kDirect = kDirect_;  // a cluster to a unit, no list
     static constexpr int kCtas = kCtas_;       // of an SM
-    using Direct = AttnCfg<kD, kKvFp8, kWM_, kWN_, kNG_, true>;
+    static constexpr int kCode = kCode_;
+    static constexpr bool kScaled = kCode != kCodePlain, kInt8 = kCode == kCodeInt8;
+    using Direct = AttnCfg<kD, kKvFp8, kWM_, kWN_, kNG_, true, 1, kCode>;
     static constexpr bool kFp8 = kKvFp8;
     static constexpr int kWM = kWM_, kWN = kWN_, kNG = kNG_;
     static constexpr int kRows = 16 * kWM;
@@ -98,6 +110,7 @@ struct AttnCfg {
     static constexpr int kBoxes = kRowBytes / kBoxBytes;
     static constexpr int kTileBytes = kPage * kRowBytes;  // keys or values of one page
     static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kScaleBytes = kScaled ? 2 * kPage / kBlock * 4 : 0;  // of a page
     static constexpr int kTokens = kPage / kWN;                       // of a page, per warp
     static constexpr int kSub = kD == 256 || kTokens < 32 ? 16 : 32;  // softmax step
     static constexpr int kPairs = kRowBytes / 32;  // pairs of 16-byte chunks in a row
@@ -434,8 +447,22 @@ __device__ __forceinline__ uint4 finite_part(const uint4& u) {
     return make_uint4(part(u.x), part(u.y), part(u.z), part(u.w));
 }
 
-// Four E4M3 codes as two pairs of f16, exact.
+// Four codes as two pairs of f16, exact.  INT8: with the sign bit flipped a code is c +
+// 128, as the low byte of an f16 in 1024 .. 2047 it is c + 1152.
+template <bool kInt8>
 __device__ __forceinline__ void lift(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    if (kInt8) {
+        const uint32_t u = codes ^ 0x80808080u;
+        const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+        auto pair = [&](uint32_t select) {
+            const uint32_t w = __byte_perm(u, 0x64646464u, select);
+            const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), bias);
+            return *reinterpret_cast<const uint32_t*>(&r);
+        };
+        lo = pair(0x4140);
+        hi = pair(0x4342);
+        return;
+    }
     asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
         : "=r"(lo), "=r"(hi)
@@ -455,6 +482,18 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -557,6 +596,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t s_full[C::kFull], s_empty[C::kStages];
     __shared__ int s_valid[C::kStages];
+    __shared__ alignas(16) float s_scale[C::kScaled ? C::kStages : 1][2 * kPage / kBlock];
     __shared__ uint32_t s_warp[C::kThreads / 32];
     __shared__ Share<C::kRows> s_share;
     __shared__ int s_abort;
@@ -630,9 +670,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     if (p.withhold && n == 0) {
                         // nobody will arrive on this page's barrier
                     } else if (valid) {
-                        mbar_arrive_expect_tx(&s_full[fb], C::kStageBytes);
+                        mbar_arrive_expect_tx(&s_full[fb], C::kStageBytes + C::kScaleBytes);
                         uint8_t* dst = ring + st * C::kStageBytes;
                         const int z = page * p.kv_heads + u.h;
+                        if constexpr (C::kScaled)
+                            bulk_copy_g2s(s_scale[st], p.scales + (int64_t)z * (2 * kPage / kBlock),
+                                          C::kScaleBytes, &s_full[fb]);
 #pragma unroll
                         for (int x = 0; x < C::kBoxes; ++x)
                             tma_load_3d(dst + x * (kPage * C::kBoxBytes), &tm_k, x * C::kBoxBytes,
@@ -782,6 +825,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     qw[x][i] = pack2<false>(__uint_as_float(qw[x][i] << 16) * up,
                                             __uint_as_float(qw[x][i] & 0xffff0000u) * up);
             }
+            // times any block's scale it stays within fp32's normal range
+            if (C::kScaled) factor = fminf(fmaxf(factor, 0x1p-78f), 0x1p94f);
             if (lane == 0) s_factor[r] = factor;
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
@@ -841,7 +886,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (s_valid[st]) {
                 const uint32_t stage = ring_u32 + st * C::kStageBytes;
                 const int first = t * kPage + wn * C::kTokens;  // this warp's first position
-                if (first + C::kTokens > u.r.seq) {
+                if (!C::kInt8 && first + C::kTokens > u.r.seq) {
                     // stale rows past the context may hold anything: p is 0 there, but
                     // 0 * NaN is not
                     const int keep = max(0, u.r.seq - first);
@@ -857,7 +902,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     __syncwarp();
                 }
                 const int shown = min(first + C::kTokens, u.r.seq);
-                if (kMany && max(first, vis_first) < shown) {
+                if (kMany && !C::kInt8 && max(first, vis_first) < shown) {
                     // the same for infinite and NaN values of new tokens that some of the
                     // row tile's rows do not see; the others get them when the unit is done
                     constexpr int kChunks = C::kRowBytes / 16, kPer = C::kBoxBytes / 16;
@@ -915,8 +960,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
                                     uint32_t k0, k1, k2, k3;
-                                    lift(k[x], k0, k1);
-                                    lift(k[2 + x], k2, k3);
+                                    lift<C::kInt8>(k[x], k0, k1);
+                                    lift<C::kInt8>(k[2 + x], k2, k3);
                                     mma16816<false>(s[2 * i], qa[x % kSteps], k0, k1);
                                     mma16816<false>(s[2 * i + 1], qa[x % kSteps], k2, k3);
                                 }
@@ -934,16 +979,52 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 if (first + sub + 8 * i + 2 * c + (x & 1) >= vis[x >> 1])
                                     s[i][x] = -INFINITY;
                     }
+                    // With a scale k, v to a block, z = s f k; the maximum is that of z +
+                    // log2 v, and what becomes the operand is p = 2^(z + log2 v - m), the
+                    // probability as the codes of the values want it.  p / v is summed.
+                    constexpr int kBlocks = C::kScaled ? C::kSub / kBlock : 1;
+                    float fk[kBlocks][2], lv[kBlocks], iv[kBlocks];
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i) {
+                        fk[i][0] = f[0];
+                        fk[i][1] = f[1];
+                        lv[i] = 0.f;
+                        iv[i] = 1.f;
+                        if (C::kScaled) {
+                            const float* at = s_scale[C::kScaled ? st : 0] +
+                                              (wn * C::kTokens + sub) / kBlock + i;
+                            const float k = fminf(fmaxf(at[0], kMinBlockScale), kMaxBlockScale);
+                            const float v = fminf(fmaxf(at[kPage / kBlock], kMinBlockScale),
+                                                  kMaxBlockScale);
+                            fk[i][0] *= k;
+                            fk[i][1] *= k;
+                            lv[i] = lg2(v);
+                            iv[i] = rcp(v);
+                        }
+                    }
                     float top[2];
                     bool grew = false;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        float y = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < kNt; ++i)
-                            y = fmaxf(y, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
                         // rounded up, as the bases below, so that no p exceeds 2^kPExp
-                        top[x] = fmaxf(m[x], __fmul_ru(quad_max(y), f[x]));
+                        if (C::kScaled) {
+                            float y = -INFINITY;
+#pragma unroll
+                            for (int b = 0; b < kBlocks; ++b) {
+                                const float(&u)[4] = s[2 * b];
+                                const float(&w)[4] = s[C::kScaled ? 2 * b + 1 : 0];
+                                y = fmaxf(y, __fmaf_ru(fmaxf(fmaxf(u[2 * x], u[2 * x + 1]),
+                                                             fmaxf(w[2 * x], w[2 * x + 1])),
+                                                       fk[b][x], lv[b]));
+                            }
+                            top[x] = fmaxf(m[x], quad_max(y));
+                        } else {
+                            float y = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < kNt; ++i)
+                                y = fmaxf(y, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
+                            top[x] = fmaxf(m[x], __fmul_ru(quad_max(y), f[x]));
+                        }
                         grew |= top[x] > m[x];
                     }
                     if (__any_sync(0xffffffffu, grew)) {
@@ -969,12 +1050,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const float b1 = __fsub_ru(base_of(m[1]), kPExp);
 #pragma unroll
                     for (int i = 0; i < kNt; ++i) {
-                        const float p0 = ex2(fmaf(s[i][0], f[0], -b0));
-                        const float p1 = ex2(fmaf(s[i][1], f[0], -b0));
-                        const float p2 = ex2(fmaf(s[i][2], f[1], -b1));
-                        const float p3 = ex2(fmaf(s[i][3], f[1], -b1));
-                        l[0] += p0 + p1;
-                        l[1] += p2 + p3;
+                        const int b = C::kScaled ? i / 2 : 0;
+                        const float c0 = C::kScaled ? __fsub_ru(b0, lv[b]) : b0;
+                        const float c1 = C::kScaled ? __fsub_ru(b1, lv[b]) : b1;
+                        const float p0 = ex2(fmaf(s[i][0], fk[b][0], -c0));
+                        const float p1 = ex2(fmaf(s[i][1], fk[b][0], -c0));
+                        const float p2 = ex2(fmaf(s[i][2], fk[b][1], -c1));
+                        const float p3 = ex2(fmaf(s[i][3], fk[b][1], -c1));
+                        if (C::kScaled) {
+                            l[0] = fmaf(p0 + p1, iv[b], l[0]);
+                            l[1] = fmaf(p2 + p3, iv[b], l[1]);
+                        } else {
+                            l[0] += p0 + p1;
+                            l[1] += p2 + p3;
+                        }
                         pf[i / 2][2 * (i & 1)] = pack2<kBf16>(p0, p1);
                         pf[i / 2][2 * (i & 1) + 1] = pack2<kBf16>(p2, p3);
                     }
@@ -990,8 +1079,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
                                     uint32_t v0, v1, v2, v3;
-                                    lift(__byte_perm(v[2 * x], 0, 0x3120), v0, v2);
-                                    lift(__byte_perm(v[2 * x + 1], 0, 0x3120), v1, v3);
+                                    lift<C::kInt8>(__byte_perm(v[2 * x], 0, 0x3120), v0, v2);
+                                    lift<C::kInt8>(__byte_perm(v[2 * x + 1], 0, 0x3120), v1, v3);
                                     constexpr int kStep = C::kFp8 ? 4 : 2;
                                     constexpr int kHalf = C::kFp8 ? 2 : 0;
                                     mma16816<false>(o[kStep * j + kHalf * x], pf[i], v0, v1);
@@ -1111,7 +1200,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                quad) = sum;
             }
         }
-        if (kMany && s_cleared == n - max(0, last - tile)) {
+        if (kMany && !C::kInt8 && s_cleared == n - max(0, last - tile)) {
             // values of this run's tiles were cleared: add them to the rows that see them
             consumer_sync<32 * C::kConsumers>();
 #pragma unroll 1
@@ -1349,7 +1438,7 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
         // shortest), else two groups of two (64 FP8 requests of 500: 9.2 us, with four
         // 10.9)
         constexpr int kWN = kWM == 1 && (C::kDim == 64 || C::kFp8) ? 2 : 4 / kWM;
-        using S = AttnCfg<C::kDim, C::kFp8, kWM, kWN, 4 / (kWM * kWN), true, 2>;
+        using S = AttnCfg<C::kDim, C::kFp8, kWM, kWN, 4 / (kWM * kWN), true, 2, C::kCode>;
         const int64_t small_tiles = ((int64_t)p.bt.max_q * p.group + S::kRows - 1) / S::kRows;
         const int64_t small_units = small_tiles * p.bt.num_requests * p.kv_heads;
         if (!p.whole && small_units > sms && small_units < (1 << 24) &&
@@ -1381,29 +1470,33 @@ cudaError_t launch_cfg(AttnParams p, const dsa_kv_cache& cache, int* launches,
                          true, 1, p, (int)C::kRows);
 }
 
-template <int kD, bool kFp8, bool kQBf16, bool kMany>
+// The plan with the list: a CTA to an SM.
+template <int kD, bool kFp8, int kCode, int kWM, int kWN, int kNG>
+using ListCfg = AttnCfg<kD, kFp8, kWM, kWN, kNG, false, 1, kCode>;
+
+template <int kD, bool kFp8, bool kQBf16, bool kMany, int kCode = kCodePlain>
 cudaError_t launch_rows(const AttnParams& p, const dsa_kv_cache& cache, int* launches,
                         cudaStream_t stream) {
     // D = 256 has 128 accumulators a thread for 16 rows and so eight warps.  At 16 rows
     // four warps to a page halve its latency where their 16-token steps are enough to
     // keep up (one wide FP8 head: 38.4 -> 35.3 us); 64 dims and FP8 need the longer
     // steps of two (64 ragged FP8 requests: 331 us, with four 381).
-    constexpr bool kFour = kD == 256 || (kD == 128 && !kFp8);
+    constexpr bool kFour = kD == 256 || (kD == 128 && !kFp8), kWide = kD == 256;
     switch (row_tile(kD, (int64_t)p.bt.max_q * p.group, p.whole != 0)) {
         case 16:
-            return launch_cfg<AttnCfg<kD, kFp8, 1, kFour ? 4 : 2, kFour ? 2 : 4>, kQBf16, kMany>(
-                p, cache, launches, stream);
+            return launch_cfg<ListCfg<kD, kFp8, kCode, 1, kFour ? 4 : 2, kFour ? 2 : 4>, kQBf16,
+                              kMany>(p, cache, launches, stream);
         case 32:
-            return launch_cfg<AttnCfg<kD, kFp8, 2, 2, kD == 256 ? 2 : 3>, kQBf16, kMany>(
+            return launch_cfg<ListCfg<kD, kFp8, kCode, 2, 2, kWide ? 2 : 3>, kQBf16, kMany>(
                 p, cache, launches, stream);
         case 48:
-            if constexpr (kD < 256)
-                return launch_cfg<AttnCfg<kD, kFp8, 3, kFour ? 2 : 1, kFour ? 2 : 4>, kQBf16, kMany>(
-                    p, cache, launches, stream);
+            if constexpr (!kWide)
+                return launch_cfg<ListCfg<kD, kFp8, kCode, 3, kFour ? 2 : 1, kFour ? 2 : 4>,
+                                  kQBf16, kMany>(p, cache, launches, stream);
             return cudaErrorInvalidValue;  // row_tile gives 256 dims no 48
         default:
-            return launch_cfg<AttnCfg<kD, kFp8, 4, kD == 256 ? 2 : 1, kD == 256 ? 1 : 3>, kQBf16, kMany>(
-                p, cache, launches, stream);
+            return launch_cfg<ListCfg<kD, kFp8, kCode, 4, kWide ? 2 : 1, kWide ? 1 : 3>, kQBf16,
+                              kMany>(p, cache, launches, stream);
     }
 }
 
@@ -1416,6 +1509,17 @@ cudaError_t launch_dim(const AttnParams& p, const dsa_kv_cache& cache, int forma
                    : launch_rows<kD, false, true, kMany>(p, cache, launches, stream);
     return fp8 ? launch_rows<kD, true, false, kMany>(p, cache, launches, stream)
                : launch_rows<kD, false, false, kMany>(p, cache, launches, stream);
+}
+
+// Caches of 8-bit codes with a scale for every 16 tokens.  INT8 has no NaN, so that kMany
+// changes nothing.
+template <int kD, int kCode>
+cudaError_t launch_codes(const AttnParams& p, const dsa_kv_cache& cache, int format, int* launches,
+                         cudaStream_t stream) {
+    constexpr bool kMany = kCode == kCodeE4m3;
+    return format == DSA_FLOAT_BF16
+               ? launch_rows<kD, true, true, kMany, kCode>(p, cache, launches, stream)
+               : launch_rows<kD, true, false, kMany, kCode>(p, cache, launches, stream);
 }
 
 }  // namespace paged

@@ -1,0 +1,510 @@
+// quant_cache.cu -- the 8-bit cache with a scale for every 16 tokens of a head: rotary
+// positions and quantisation as tokens are written, and the values read back.
+#include "rope.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlock = DSA_QUANT_BLOCK;
+constexpr int kPageBlocks = kPage / kBlock;
+constexpr int kMaxTokens = 16;  // of a CTA
+constexpr float kMinScale = 0x1p-48f, kMaxNeed = 0x1p32f, kMaxScale = 0x1p33f;
+
+struct QuantArgs {
+    int32_t num_tokens, q_heads, kv_heads, interleaved, pairs;
+    int32_t tokens;      // of a CTA
+    int32_t end0, end1;  // first pair of the second and of the third section
+    int64_t slot_end;
+    const double* inv_freq;
+    const int32_t* positions;
+    const int64_t* slots;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    uint8_t* k_pages;
+    uint8_t* v_pages;
+    float* scales;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    int32_t* status;
+};
+
+template <bool kInt8>
+__device__ __forceinline__ float largest() {
+    return kInt8 ? 127.f : 448.f;
+}
+
+// Four values as codes, the first in the low byte; INT8: within +-127.49 already, rounded
+// by the addition of 1.5 * 2^23, whose low bits then hold the integer.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    if (kInt8) {
+        constexpr float kMagic = 12582912.f;
+        const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a, kMagic)),
+                                        __float_as_uint(__fadd_rn(b, kMagic)), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(c, kMagic)),
+                                        __float_as_uint(__fadd_rn(d, kMagic)), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    }
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+template <bool kInt8>
+__device__ __forceinline__ void decode4(uint32_t codes, float (&x)[4]) {
+    if (kInt8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(codes >> (8 * i));
+    } else {
+        const float2 lo = e4m3x2_to_float2((uint16_t)codes);
+        const float2 hi = e4m3x2_to_float2((uint16_t)(codes >> 16));
+        x[0] = lo.x;
+        x[1] = lo.y;
+        x[2] = hi.x;
+        x[3] = hi.y;
+    }
+}
+
+template <bool kInt8>
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float by) {
+    return make_uint2(encode4<kInt8>(__fmul_rn(x[0], by), __fmul_rn(x[1], by),
+                                     __fmul_rn(x[2], by), __fmul_rn(x[3], by)),
+                      encode4<kInt8>(__fmul_rn(x[4], by), __fmul_rn(x[5], by),
+                                     __fmul_rn(x[6], by), __fmul_rn(x[7], by)));
+}
+
+// The least k >= 0 with scale * 2^k >= need (normal numbers).
+__device__ __forceinline__ int doublings(float scale, float need) {
+    const uint32_t s = __float_as_uint(scale), n = __float_as_uint(need);
+    return max(0, (int)(n >> 23) - (int)(s >> 23) + ((n & 0x7fffffu) > (s & 0x7fffffu)));
+}
+
+// A value that the scale does not cover, or NaN, which INT8 has no code for.
+template <bool kInt8>
+__device__ __forceinline__ float within(float x, float most) {
+    if (x != x) return kInt8 ? 0.f : x;
+    return fminf(fmaxf(x, -most), most);
+}
+
+// The tokens of one block that stand together: the first of them, from the CTA's first
+// token on, how many, and which of them are stored.
+struct Run {
+    int32_t first, count;
+    uint32_t stored;
+    int32_t pad;
+};
+
+template <typename T, bool kInt8, int kDim>
+__global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs a) {
+    constexpr int kUnits = kDim / 16;     // 16 values of a row to a lane
+    constexpr int kRows = 32 / kUnits;    // of a warp at a time
+    constexpr int kSteps = kBlock / kRows;
+    extern __shared__ float2 s_turn[];    // of each token, turn_at()
+    __shared__ int64_t s_slot[kMaxTokens + kBlock];  // from the token before the CTA's on
+    __shared__ Run s_run[kMaxTokens];
+    __shared__ int s_runs, s_reach;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t first = (int64_t)blockIdx.x * a.tokens;
+    const int count = (int)min((int64_t)a.tokens, a.num_tokens - first);
+    // a run may go on behind the CTA's tokens
+    const int reach = (int)min((int64_t)count + kBlock - 1, a.num_tokens - first);
+    grid_dependents_launch();
+    grid_dependency_wait();
+
+    if (warp == 0) {
+        int64_t slot = -1;
+        const int64_t t = first + lane - 1;
+        if (lane <= reach && t >= 0) {
+            slot = __ldg(a.slots + t);
+            if (slot >= a.slot_end) {
+                if (lane > 0 && lane <= count) record_error(a.status, DSA_ERR_DEVICE_CHECK);
+                slot = -1;
+            }
+        }
+        if (lane <= reach) s_slot[lane] = slot;
+        __syncwarp();
+        // lane i: the CTA's token i
+        const int64_t own = lane < reach ? s_slot[lane + 1] : -1;
+        const int64_t before = lane < reach ? s_slot[lane] : -1;
+        const bool joined = own >= 0 && before >= 0 && own / kBlock == before / kBlock;
+        const bool ascends = !joined || own > before;
+        if (lane < count && !ascends) record_error(a.status, DSA_ERR_DEVICE_CHECK);
+        const uint32_t all_joined = __ballot_sync(0xffffffffu, joined);
+        const uint32_t all_ascend = __ballot_sync(0xffffffffu, ascends);
+        const bool leads = lane < count && own >= 0 && !joined;
+        const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+        int end = 0;
+        if (leads) {
+            Run r;
+            r.first = lane;
+            // tokens behind this one that are joined to their predecessor
+            const uint32_t rest = lane < 31 ? ~(all_joined >> (lane + 1)) : 1u;
+            r.count = min(1 + __ffs(rest) - 1, kBlock);
+            r.stored = (all_ascend >> lane) & ((1u << r.count) - 1u);
+            end = lane + r.count;
+            s_run[__popc(leaders & ((1u << lane) - 1u))] = r;
+        }
+        end = __reduce_max_sync(0xffffffffu, end);
+        if (lane == 0) {
+            s_runs = __popc(leaders);
+            s_reach = max(end, a.q_heads > 0 ? count : 0);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < s_reach * a.pairs; i += kThreads) {
+        const int j = i / a.pairs, pair = i - j * a.pairs;
+        const int axis = (pair >= a.end0 ? 1 : 0) + (pair >= a.end1 ? 1 : 0);
+        const int pos = __ldg(a.positions + (int64_t)axis * a.num_tokens + first + j);
+        s_turn[j * a.pairs + turn_at(pair, a.pairs)] = turn_of(__ldg(a.inv_freq + pair), pos);
+    }
+    __syncthreads();
+
+    // Keys and values: a warp to a run's head.
+    const int items = s_runs * 2 * a.kv_heads;
+    for (int item = warp + kWarps * blockIdx.y; item < items; item += kWarps * gridDim.y) {
+        const int i_run = item / (2 * a.kv_heads), rest = item - i_run * 2 * a.kv_heads;
+        const int which = rest >= a.kv_heads, head = rest - which * a.kv_heads;
+        const Run run = s_run[i_run];
+        const int64_t slot0 = s_slot[run.first + 1];
+        const int64_t page_head = slot0 / kPage * a.kv_heads + head;
+        const int part = (int)(slot0 % kPage) / kBlock;
+        float* const scale_at = a.scales + (page_head * 2 + which) * kPageBlocks + part;
+        uint8_t* const block =
+            (which ? a.v_pages : a.k_pages) + (page_head * kPage + part * kBlock) * kDim;
+        const bool fresh = slot0 % kBlock == 0;
+        const float begun = *scale_at;
+        const T* const src = which ? static_cast<const T*>(a.v) : static_cast<const T*>(a.k);
+        const int64_t stride = which ? a.v_stride : a.k_stride;
+        const int unit = lane % kUnits, row0 = lane / kUnits;
+        const bool turned = !which && unit < a.pairs / 8;
+        const bool halves = turned && !a.interleaved;
+        const int at0 = halves ? unit * 8 : unit * 16;
+        const int at1 = halves ? unit * 8 + a.pairs : unit * 16 + 8;
+        uint4 lo[kSteps], hi[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int j = s * kRows + row0;
+            lo[s] = hi[s] = make_uint4(0, 0, 0, 0);
+            if (run.stored >> j & 1) {
+                const T* p = src + (first + run.first + j) * stride + head * kDim;
+                lo[s] = *reinterpret_cast<const uint4*>(p + at0);
+                hi[s] = *reinterpret_cast<const uint4*>(p + at1);
+            }
+        }
+        auto values = [&](int s, float (&x)[8], float (&y)[8]) {
+            unpack8<T>(lo[s], x);
+            unpack8<T>(hi[s], y);
+            if (turned)
+                turn16(x, y, s_turn + (run.first + s * kRows + row0) * a.pairs, a.pairs / 8, unit,
+                       a.interleaved);
+        };
+        // the largest magnitude as bits, above infinity's for a NaN
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+            if (run.stored >> (s * kRows + row0) & 1) {
+                float x[8], y[8];
+                values(s, x, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu,
+                                       __float_as_uint(y[i]) & 0x7fffffffu));
+            }
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool odd = top >= 0x7f800000u;
+        if (odd) {  // of the finite values only
+            if (lane == 0) record_error(a.status, DSA_ERR_DEVICE_CHECK);
+            top = 0;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                float x[8], y[8];
+                values(s, x, y);
+                if (run.stored >> (s * kRows + row0) & 1)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (isfinite(x[i])) top = max(top, __float_as_uint(fabsf(x[i])));
+                        if (isfinite(y[i])) top = max(top, __float_as_uint(fabsf(y[i])));
+                    }
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+        }
+        const float all = __fdiv_rn(__uint_as_float(top), largest<kInt8>());
+        const float need = fminf(fmaxf(all, kMinScale), kMaxNeed);
+        const bool saturates = odd || all > kMaxNeed;
+        if (!fresh && !(begun >= kMinScale && begun <= kMaxScale)) {
+            if (lane == 0) record_error(a.status, DSA_ERR_DEVICE_CHECK);
+            continue;
+        }
+        const int k = fresh ? 0 : doublings(begun, need);
+        const float scale = fresh ? need : __uint_as_float(__float_as_uint(begun) + (k << 23));
+        const float by = __frcp_rn(scale);
+
+        // which of the block's rows this call writes
+        uint32_t written = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int j = s * kRows + row0;
+            if (!(run.stored >> j & 1)) continue;
+            const int row = (int)(s_slot[run.first + j + 1] % kBlock);
+            written |= 1u << row;
+            float x[8], y[8];
+            values(s, x, y);
+            if (saturates)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = within<kInt8>(x[i], __fmul_rn(scale, largest<kInt8>()));
+                    y[i] = within<kInt8>(y[i], __fmul_rn(scale, largest<kInt8>()));
+                }
+            uint8_t* dst = block + row * kDim;
+            *reinterpret_cast<uint2*>(dst + at0) = encode8<kInt8>(x, by);
+            *reinterpret_cast<uint2*>(dst + at1) = encode8<kInt8>(y, by);
+        }
+        if (k > 0) {
+            written = __reduce_or_sync(0xffffffffu, written);
+            const float down = __uint_as_float((uint32_t)max(127 - k, 1) << 23);
+#pragma unroll 1
+            for (int s = 0; s < kSteps; ++s) {
+                const int row = s * kRows + row0;
+                if (written >> row & 1) continue;
+                uint4* at = reinterpret_cast<uint4*>(block + row * kDim) + unit;
+                uint4 u = *at;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float c[4];
+                    decode4<kInt8>(w[i], c);
+                    w[i] = encode4<kInt8>(c[0] * down, c[1] * down, c[2] * down, c[3] * down);
+                }
+                *at = u;
+            }
+        }
+        if (lane == 0 && (fresh || k > 0)) *scale_at = scale;
+    }
+
+    // Queries: a thread to 16 values.
+    const int units = count * a.q_heads * kUnits;
+    for (int i = tid + kThreads * blockIdx.y; i < units; i += kThreads * gridDim.y) {
+        const int j = i / (a.q_heads * kUnits), rest = i - j * (a.q_heads * kUnits);
+        const int head = rest / kUnits, unit = rest % kUnits;
+        const bool turned = unit < a.pairs / 8, halves = turned && !a.interleaved;
+        const int at0 = halves ? unit * 8 : unit * 16;
+        const int at1 = halves ? unit * 8 + a.pairs : unit * 16 + 8;
+        const T* src = static_cast<const T*>(a.q) + (first + j) * a.q_stride + head * kDim;
+        float x[8], y[8];
+        unpack8<T>(*reinterpret_cast<const uint4*>(src + at0), x);
+        unpack8<T>(*reinterpret_cast<const uint4*>(src + at1), y);
+        if (turned) turn16(x, y, s_turn + j * a.pairs, a.pairs / 8, unit, a.interleaved);
+        T* dst = static_cast<T*>(a.q_out) + (first + j) * a.q_out_stride + head * kDim;
+        store8(dst + at0, x);
+        store8(dst + at1, y);
+    }
+}
+
+template <typename T, bool kInt8, int kDim>
+cudaError_t launch_append(QuantArgs a, cudaStream_t stream) {
+    a.tokens = kMaxTokens;
+    while (a.tokens > 1 && a.num_tokens / a.tokens < 608) a.tokens /= 2;
+    const int ctas = (a.num_tokens + a.tokens - 1) / a.tokens;
+    // few tokens: several CTAs share the heads of each
+    const int most = max((2 * a.kv_heads + kWarps - 1) / kWarps,
+                         (a.q_heads * (kDim / 16) + kThreads - 1) / kThreads);
+    int splits = 1;
+    while (splits < most && splits < 16 && ctas * splits < 304) splits *= 2;
+    const size_t smem = (size_t)(a.tokens + kBlock - 1) * a.pairs * sizeof(float2);  // <= 32 KB
+    return launch_kernel(quant_append_kernel<T, kInt8, kDim>,
+                         dim3((unsigned)ctas, (unsigned)splits), dim3(kThreads), smem, stream,
+                         true, 1, a);
+}
+
+// ---- reading back ---------------------------------------------------------------
+
+constexpr int kReadTokens = 16;  // of a CTA
+
+struct ReadArgs {
+    BatchArgs bt;
+    int32_t kv_heads;
+    const uint8_t* k_pages;
+    const uint8_t* v_pages;
+    const float* scales;
+    void* k_out;
+    void* v_out;
+    int64_t k_stride, v_stride;
+    int32_t* status;
+};
+
+// A scale as the reading calls take it.
+__device__ __forceinline__ float taken_scale(float s) {
+    return fminf(fmaxf(s, kMinScale), kMaxScale);
+}
+
+template <typename T, bool kInt8, int kDim>
+__global__ void __launch_bounds__(kThreads) quant_read_kernel(const ReadArgs a) {
+    constexpr int kUnits = kDim / 16;
+    __shared__ int64_t s_slot[kReadTokens];
+    const int tid = threadIdx.x;
+    const int64_t first = (int64_t)blockIdx.x * kReadTokens;
+    const int count = (int)min((int64_t)kReadTokens, a.bt.total_q - first);
+    grid_dependents_launch();
+    grid_dependency_wait();
+    if (tid < count) {
+        const int t = (int)first + tid;
+        const int b = request_of(a.bt, t);
+        const int q0 = __ldg(a.bt.q_offsets + b), q1 = __ldg(a.bt.q_offsets + b + 1);
+        const int seq = __ldg(a.bt.seq_lens + b);
+        int64_t slot = -1;
+        if (q0 < 0 || t < q0 || t >= q1 || q1 > a.bt.total_q || q1 - q0 > a.bt.max_q || seq < 0 ||
+            seq > a.bt.max_seq) {
+            record_error(a.status, DSA_ERR_DEVICE_CHECK);
+        } else {
+            const int pos = seq - (q1 - t);
+            if (pos >= 0) {
+                const int page = page_lookup(a.bt, b, pos / kPage, a.status);
+                if (page >= 0) slot = (int64_t)page * kPage + pos % kPage;
+            }
+        }
+        s_slot[tid] = slot;
+    }
+    __syncthreads();
+    // neighbouring lanes: units of a row, then rows of a head, which lie together in a page
+    const int items = 2 * a.kv_heads * kReadTokens * kUnits;
+    for (int i = tid + kThreads * blockIdx.y; i < items; i += kThreads * gridDim.y) {
+        const int unit = i % kUnits, j = i / kUnits % kReadTokens;
+        const int rest = i / (kUnits * kReadTokens);
+        const int which = rest >= a.kv_heads, head = rest - which * a.kv_heads;
+        T* out = static_cast<T*>(which ? a.v_out : a.k_out);
+        const int64_t slot = j < count ? s_slot[j] : -1;
+        if (out == nullptr || slot < 0) continue;
+        const int64_t page_head = slot / kPage * a.kv_heads + head;
+        const int row = (int)(slot % kPage);
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(
+                                  (which ? a.v_pages : a.k_pages) +
+                                  (page_head * kPage + row) * kDim) + unit);
+        const float scale = taken_scale(
+            __ldg(a.scales + (page_head * 2 + which) * kPageBlocks + row / kBlock));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        float x[8], y[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float v[4];
+            decode4<kInt8>(w[c], v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) (c < 2 ? x : y)[4 * (c & 1) + e] = v[e] * scale;
+        }
+        T* dst = out + (first + j) * (which ? a.v_stride : a.k_stride) + head * kDim + unit * 16;
+        store8(dst, x);
+        store8(dst + 8, y);
+    }
+}
+
+template <typename T, bool kInt8, int kDim>
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t stream) {
+    const int ctas = (a.bt.total_q + kReadTokens - 1) / kReadTokens;
+    const int items = 2 * a.kv_heads * kReadTokens * (kDim / 16);
+    int splits = 1;
+    while (splits < 64 && ctas * splits < 608 && splits * kThreads < items) splits *= 2;
+    return launch_kernel(quant_read_kernel<T, kInt8, kDim>,
+                         dim3((unsigned)ctas, (unsigned)splits), dim3(kThreads), 0, stream, true, 1,
+                         a);
+}
+
+// f.run<T, kInt8, kDim>() for a cache and a 16-bit type.
+template <typename T, bool kInt8, typename F>
+cudaError_t by_dim(int head_dim, const F& f) {
+    switch (head_dim) {
+        case 64: return f.template run<T, kInt8, 64>();
+        case 128: return f.template run<T, kInt8, 128>();
+        default: return f.template run<T, kInt8, 256>();
+    }
+}
+
+template <typename F>
+cudaError_t by_type(const dsa_quant_cache& cache, int format, const F& f) {
+    const bool int8 = cache.format == DSA_QUANT_INT8;
+    if (format == DSA_FLOAT_BF16)
+        return int8 ? by_dim<__nv_bfloat16, true>(cache.head_dim, f)
+                    : by_dim<__nv_bfloat16, false>(cache.head_dim, f);
+    return int8 ? by_dim<__half, true>(cache.head_dim, f)
+                : by_dim<__half, false>(cache.head_dim, f);
+}
+
+struct Append {
+    QuantArgs a;
+    cudaStream_t stream;
+    template <typename T, bool kInt8, int kDim>
+    cudaError_t run() const {
+        return launch_append<T, kInt8, kDim>(a, stream);
+    }
+};
+
+struct Read {
+    ReadArgs a;
+    cudaStream_t stream;
+    template <typename T, bool kInt8, int kDim>
+    cudaError_t run() const {
+        return launch_read<T, kInt8, kDim>(a, stream);
+    }
+};
+
+}  // namespace
+
+cudaError_t launch_quant_append(int num_tokens, const dsa_quant_cache& cache, int format,
+                                const dsa_rope& rope, const int32_t* positions,
+                                const int64_t* slots, int num_q_heads, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, void* q_out, int64_t q_out_stride,
+                                int32_t* status, cudaStream_t stream) {
+    QuantArgs a;
+    a.num_tokens = num_tokens;
+    a.q_heads = num_q_heads;
+    a.kv_heads = cache.num_kv_heads;
+    a.interleaved = rope.interleaved != 0;
+    a.pairs = 0;
+    int ends[3] = {0, 0, 0};
+    for (int i = 0; i < 3; ++i) {
+        if (i < rope.num_axes) a.pairs += rope.sections[i];
+        ends[i] = a.pairs;
+    }
+    a.end0 = ends[0];
+    a.end1 = ends[1];
+    a.tokens = 0;  // set by the launch
+    a.slot_end = (int64_t)cache.num_pages * kPage;
+    a.inv_freq = rope.inv_freq;
+    a.positions = positions;
+    a.slots = slots;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_pages = static_cast<uint8_t*>(cache.k_pages);
+    a.v_pages = static_cast<uint8_t*>(cache.v_pages);
+    a.scales = cache.scales;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.status = status;
+    return by_type(cache, format, Append{a, stream});
+}
+
+cudaError_t launch_quant_read(const BatchArgs& bt, const dsa_quant_cache& cache, int format,
+                              void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                              int32_t* status, cudaStream_t stream) {
+    ReadArgs a;
+    a.bt = bt;
+    a.kv_heads = cache.num_kv_heads;
+    a.k_pages = static_cast<const uint8_t*>(cache.k_pages);
+    a.v_pages = static_cast<const uint8_t*>(cache.v_pages);
+    a.scales = cache.scales;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.status = status;
+    return by_type(cache, format, Read{a, stream});
+}
+
+}  // namespace dsa

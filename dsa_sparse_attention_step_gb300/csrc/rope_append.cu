@@ -3,12 +3,8 @@
 //
 // Pair i of a head is turned by positions[axis(i), t] * inv_freq[i]:
 //   (x, y) -> (x cos - y sin, y cos + x sin).
-// Positions reach 2^20 and beyond, where a 32-bit angle is off by 1/16 of a
-// radian, so the angle is reduced in fixed point: inv_freq / 2 pi as a fraction
-// of a turn in 64 bits, times the position, modulo 2^64, is the fraction of the
-// turn (the product wraps exactly; the rate is off by less than 2^-53 turns per
-// unit of position).  Its upper 32 bits go to sincospi.  Two double-precision
-// operations per pair, none per value.
+// The angle is reduced in fixed point (rope.cuh): two double-precision operations per
+// pair, none per value.
 //
 // Memory bound: every value is read and written once.  A thread moves units of 16
 // values (two 16-byte loads: the two halves of eight pairs, or 16 consecutive
@@ -20,7 +16,7 @@
 // one unit a thread, which leaves registers for a fifth CTA on the SM, is the faster
 // (32768 tokens of 40 heads of 256: 206 us, 6.5 TB/s, with two 213; 4096 tokens of 48
 // such heads: 44.7 and 39.4 us).
-#include "common.cuh"
+#include "rope.cuh"
 
 namespace dsa {
 
@@ -48,51 +44,6 @@ struct RopeArgs {
     float k_scale, v_scale;
     int32_t* status;
 };
-
-template <typename T>
-__device__ __forceinline__ float2 to_float2(uint32_t v);
-template <>
-__device__ __forceinline__ float2 to_float2<__nv_bfloat16>(uint32_t v) {
-    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v));
-}
-template <>
-__device__ __forceinline__ float2 to_float2<__half>(uint32_t v) {
-    return __half22float2(*reinterpret_cast<__half2*>(&v));
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t from_float2(float x, float y);
-template <>
-__device__ __forceinline__ uint32_t from_float2<__nv_bfloat16>(float x, float y) {
-    __nv_bfloat162 r = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<uint32_t*>(&r);
-}
-template <>
-__device__ __forceinline__ uint32_t from_float2<__half>(float x, float y) {
-    __half2 r = __floats2half2_rn(x, y);
-    return *reinterpret_cast<uint32_t*>(&r);
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = to_float2<T>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-    uint4 u;
-    u.x = from_float2<T>(x[0], x[1]);
-    u.y = from_float2<T>(x[2], x[3]);
-    u.z = from_float2<T>(x[4], x[5]);
-    u.w = from_float2<T>(x[6], x[7]);
-    *reinterpret_cast<uint4*>(p) = u;
-}
 
 // Eight values as E4M3 codes of x / scale (IEEE division, so that the codes are
 // those of the definition), round to nearest even, saturating.
@@ -167,35 +118,7 @@ __device__ __forceinline__ void finish_unit(const RopeArgs& a, const Unit<T>& u,
     unpack8<T>(u.a, x);
     unpack8<T>(u.b, y);
     if (u.kind != 2 && u.unit < a.pairs / 8) {
-        // two (cos, sin) pairs a load, neighbouring units in neighbouring banks
-        const int units = a.pairs / 8;
-        const float4* cs = reinterpret_cast<const float4*>(turns + u.token * a.pairs) + u.unit;
-        if (a.interleaved) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float4 c = cs[p * units], d = cs[(2 + p) * units];
-                const float x0 = x[4 * p], x1 = x[4 * p + 1], x2 = x[4 * p + 2], x3 = x[4 * p + 3];
-                const float y0 = y[4 * p], y1 = y[4 * p + 1], y2 = y[4 * p + 2], y3 = y[4 * p + 3];
-                x[4 * p] = x0 * c.x - x1 * c.y;
-                x[4 * p + 1] = x1 * c.x + x0 * c.y;
-                x[4 * p + 2] = x2 * c.z - x3 * c.w;
-                x[4 * p + 3] = x3 * c.z + x2 * c.w;
-                y[4 * p] = y0 * d.x - y1 * d.y;
-                y[4 * p + 1] = y1 * d.x + y0 * d.y;
-                y[4 * p + 2] = y2 * d.z - y3 * d.w;
-                y[4 * p + 3] = y3 * d.z + y2 * d.w;
-            }
-        } else {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const float4 c = cs[p * units];
-                const float x0 = x[2 * p], y0 = y[2 * p], x1 = x[2 * p + 1], y1 = y[2 * p + 1];
-                x[2 * p] = x0 * c.x - y0 * c.y;
-                y[2 * p] = y0 * c.x + x0 * c.y;
-                x[2 * p + 1] = x1 * c.z - y1 * c.w;
-                y[2 * p + 1] = y1 * c.z + x1 * c.w;
-            }
-        }
+        turn16(x, y, turns + u.token * a.pairs, a.pairs / 8, u.unit, a.interleaved);
     }
     if (u.kind == 0) {
         T* dst = static_cast<T*>(a.q_out) + u.row * a.q_out_stride + u.head * kDim;
@@ -233,15 +156,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
         const int j = i / a.pairs, pair = i - j * a.pairs;
         const int axis = (pair >= a.end0 ? 1 : 0) + (pair >= a.end1 ? 1 : 0);
         const int pos = __ldg(a.positions + (int64_t)axis * a.num_tokens + first + j);
-        // the fraction of a turn per unit of position, in units of 2^-64
-        double turns = __ldg(a.inv_freq + pair) * 0.15915494309189533577;
-        turns -= floor(turns);
-        const unsigned long long rate = (unsigned long long)(turns * 18446744073709551616.0);
-        const long long angle = (long long)((unsigned long long)(long long)pos * rate);
-        float sn, cs;
-        sincospif((float)(int)(angle >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
-        s_turn[j * a.pairs + (((pair >> 1 & 3) * (a.pairs >> 3) + (pair >> 3)) << 1) + (pair & 1)] =
-            make_float2(cs, sn);
+        s_turn[j * a.pairs + turn_at(pair, a.pairs)] = turn_of(__ldg(a.inv_freq + pair), pos);
     }
     __syncthreads();
     if constexpr (kAhead) {

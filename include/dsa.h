@@ -560,6 +560,106 @@ dsa_status dsa_paged_attention(const dsa_batch* batch, const dsa_kv_cache* cache
                                int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
                                size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream);
 
+/* ---- an 8-bit cache whose scales follow the data -----------------------------------
+ * No counterpart on the pages: an addition of this library.  Where the FP8 cache above
+ * has one scale for all keys of a layer and one for all values, to be known before the
+ * first token, this one has a scale for every 16 tokens of a head (a block), taken from
+ * the tokens as they are written.  A quarter of a page is a block.  The calls take the
+ * place of dsa_rope_append and dsa_paged_attention between dsa_build_tables and the rest
+ * of a layer; dsa_quant_read gives the cached values back.  They allocate nothing and may
+ * be captured into a CUDA graph. */
+
+/* Element type of the codes.  Largest magnitude L: 448 and 127. */
+typedef enum { DSA_QUANT_E4M3 = 0, DSA_QUANT_INT8 = 1 } dsa_quant_format;
+
+enum { DSA_QUANT_BLOCK = 16 };
+
+/* A paged 8-bit key/value cache of one layer.  The struct lives in host memory; the
+ * arrays are device pointers, 16-byte aligned:
+ *   k_pages, v_pages  [num_pages, num_kv_heads, 64, head_dim] codes
+ *   scales            [num_pages, num_kv_heads, 2, 4] fp32: of the keys' four blocks of
+ *                     16 rows, then of the values'
+ * Code c of row r stands for c * scale of block r / 16.  Scales lie in [2^-48, 2^33];
+ * the reading calls take one outside for the nearer end (NaN: the lower).
+ * head_dim is 64, 128 or 256; num_pages * num_kv_heads is below 2^31. */
+typedef struct {
+    int32_t num_pages;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    dsa_quant_format format;
+    void* k_pages;
+    void* v_pages;
+    float* scales;
+} dsa_quant_cache;
+
+/* dsa_rope_append into such a cache: rotary positions on queries and keys in fp32, the
+ * queries rounded once to the 16-bit type, keys and values quantised as they are
+ * written.  For each block and head, with x the values that the call writes there (keys
+ * after turning):
+ *   need = max |x| / L, at least 2^-48 and at most 2^32
+ *   scale = need               if the block's first row is among them: it starts anew
+ *   scale = scale * 2^k        else, with the least k >= 0 that makes it need or more;
+ *                              the codes c of the block's other rows become
+ *                              round(c * 2^-k)
+ *   code  = round(x * (1 / scale)), saturating at +-L
+ * Divisions and products are fp32, code roundings to nearest even.  For E4M3 the
+ * doubling of a scale loses nothing but what falls below the smallest codes; for INT8 it
+ * costs the older codes up to half a step each time.
+ *   positions, q, k, v, q_out, num_q_heads, strides: as dsa_rope_append; num_axes 0
+ *       means no turning
+ *   slots [T] int64, as dsa_build_tables writes them: page * 64 + row.  Negative: the
+ *       token's key and value are not stored.  Tokens of one block stand next to each
+ *       other in the call, their slots ascending, and each block comes up in one place
+ *       only.
+ * q_out may be q itself with the same stride, else it must not overlap the inputs.
+ * The call may be repeated on the same inputs: it writes the same scales and codes.
+ * Recorded as DSA_ERR_DEVICE_CHECK in *dev_status:
+ *   - a slot at or beyond num_pages * 64 (not stored);
+ *   - a slot that does not exceed its predecessor's in the same block (not stored);
+ *   - a block begun earlier whose scale lies outside [2^-48, 2^33] (its tokens are not
+ *     stored);
+ *   - infinite and NaN values.  need is that of the finite ones; infinite ones saturate,
+ *     a NaN becomes a NaN code of E4M3 and 0 in INT8.
+ * One kernel launch. */
+dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
+                            dsa_float_format format, const dsa_rope* rope,
+                            const int32_t* positions, const int64_t* slots, int32_t num_q_heads,
+                            const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                            int32_t* dev_status, dsa_stream_t stream);
+
+/* The cached keys and values of the batch's tokens as 16-bit rows: token t, at place j of
+ * request b's n_b, gets those of position seq_lens[b] - n_b + j, so a request with
+ * n_b = seq_lens[b] is read whole.
+ *   k_out[t,h,:] = code * scale, in fp32, rounded once to `format`; v_out likewise
+ *   k_out, v_out  [T, num_kv_heads, head_dim], tokens *_stride elements apart (a multiple
+ *                 of 8, at least a token's elements), 16-byte aligned; either may be NULL.
+ *                 They overlap neither each other, unless as slices of one row, nor the
+ *                 cache.
+ * A token before position 0 (seq_lens[b] < n_b, a padding request), one whose page lies
+ * outside [0, num_pages) and one of a request whose arrays contradict the host sizes keep
+ * the rows that they had; the last two are recorded as DSA_ERR_DEVICE_CHECK.
+ * batch->num_pages must equal cache->num_pages.  One kernel launch. */
+dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
+                          dsa_float_format format, void* k_out, int64_t k_stride, void* v_out,
+                          int64_t v_stride, int32_t* dev_status, dsa_stream_t stream);
+
+/* dsa_paged_attention over such a cache: the same definition, arguments, padding, device
+ * checks, limits and batch-invariant plan, with key(s) and value(s) a code times its
+ * block's scale.  Codes are lifted to f16 exactly; bf16 queries are scaled by a power of
+ * two per row so that f16 holds them.  Scores, maxima and sums are fp32.  What meets the
+ * values' codes is probability times the block's scale, rounded to f16: half a step each,
+ * 2^-11 of it (of those below 2^-29 of the row's largest such product, 2^-40 of that).
+ * NaN codes of E4M3 reach the tokens that see them, in their own dim.
+ * sm_scale is finite and > 0, and sm_scale * log2 e a normal fp32 number
+ * (DSA_ERR_INVALID_ARG); it counts as no less than 2^-78 and no more than 2^94. */
+size_t dsa_quant_attention_workspace_size(const dsa_batch* batch, const dsa_quant_cache* cache,
+                                          int32_t num_q_heads);
+dsa_status dsa_quant_attention(const dsa_batch* batch, const dsa_quant_cache* cache,
+                               dsa_float_format format, int32_t num_q_heads, const void* q,
+                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

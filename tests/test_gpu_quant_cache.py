@@ -1,0 +1,451 @@
+"""dsa_quant_append and dsa_quant_read on the GPU against their definitions.
+
+Without turning everything after the 16-bit inputs is one fp32 operation after another, so
+scales and codes are compared bit for bit.  With turning, a key differs from its 64-bit
+value by e <= 2^-21 of the sum of its two products' sizes; a scale, fp32 quotient of the
+largest, by 2^-21 of the block's largest such sum over L (and a rounding, 2^-24); a decoded
+key by half a step of its code, e, and the scale's and its reciprocal's roundings
+(2^-22 of the value)."""
+import pytest
+import torch
+
+import dsa_sparse_attention_step_gb300 as dsa
+from paged_helpers import DEV, PAGE, turn_reference
+from quant_helpers import (BLOCK, E4M3, INT8, LARGEST, append_reference, decoded, encode,
+                           random_cache, slots_of, tables_of)
+
+pytestmark = pytest.mark.gpu
+
+DEVICE_CHECK = 5
+BF16, F16 = torch.bfloat16, torch.float16
+NAN, INF = float("nan"), float("inf")
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def generator(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+class Append:
+    """Requests that bring new tokens to a cache of random codes and scales."""
+
+    def __init__(self, cached, new, hq, hkv, d, dtype, code, seed=0, pad=0):
+        g = generator(7000 + seed)
+        self.cached, self.new, self.hkv, self.d, self.dtype = cached, new, hkv, d, dtype
+        self.lens = [a + b for a, b in zip(cached, new)]
+        self.table, self.pages = tables_of(g, self.lens)
+        self.slots = slots_of(self.table, cached, new)
+        self.slots = torch.cat([self.slots, self.slots.new_full((pad,), -1)])
+        tokens = len(self.slots)
+        qkv = torch.randn(tokens, hq + 2 * hkv, d, generator=g, device=DEV)
+        qkv *= torch.exp(torch.randn(tokens, 1, 1, generator=g, device=DEV))  # scales have to grow
+        self.q, self.k, self.v = qkv.to(dtype).split([hq, hkv, hkv], dim=1)
+        self.k_pages, self.v_pages, self.scales = random_cache(g, self.pages, hkv, d, code)
+        self.q_out = torch.full((tokens, hq, d), NAN, dtype=dtype, device=DEV)
+
+    def run(self, rope=None, positions=None, status=0, **kw):
+        cache = dsa.QuantCache(self.k_pages, self.v_pages, self.scales)
+        st = i32([0])
+        args = dict(q=self.q, k=self.k, v=self.v, q_out=self.q_out, slots=self.slots)
+        args.update(kw)
+        if self.q.shape[1] == 0:
+            args["q"] = args["q_out"] = None
+        dsa.dsa_quant_append(cache, rope, positions, args["slots"], args["q"], args["k"],
+                             args["v"], args["q_out"], st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == status
+
+    def reference(self, slots=None):
+        slots = self.slots if slots is None else slots
+        k, scales, _ = append_reference(self.k_pages, self.scales, 0, slots, self.k.float())
+        v, scales, _ = append_reference(self.v_pages, scales, 1, slots, self.v.float())
+        return k, v, scales
+
+    def state(self):
+        return [x.view(torch.uint8).clone() for x in (self.k_pages, self.v_pages)] + [
+            self.scales.clone()]
+
+    def check(self, want):
+        for x, y in zip((self.k_pages, self.v_pages), want[:2]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+        assert torch.equal(self.scales, want[2])
+
+
+@pytest.mark.parametrize("dtype,code", [(BF16, E4M3), (F16, E4M3), (BF16, INT8), (F16, INT8)])
+@pytest.mark.parametrize("cached,new,hq,hkv,d,pad", [
+    ([0], [1], 1, 1, 64, 0), ([699], [1], 32, 8, 128, 0), ([15, 16, 17, 0], [1, 1, 1, 1], 4, 2, 256, 1),
+    ([3, 60, 0], [5, 9, 40], 0, 3, 64, 0), ([37], [300], 8, 2, 128, 3), ([0, 7], [64, 57], 2, 1, 256, 0),
+    ([1000 + 3 * b for b in range(90)], [1 + b % 5 for b in range(90)], 8, 4, 128, 2),
+    ([31 * b % 50 for b in range(40)], [b * 13 % 70 for b in range(40)], 3, 5, 64, 5)])
+def test_append_without_turning_is_exact(dtype, code, cached, new, hq, hkv, d, pad):
+    c = Append(cached, new, hq, hkv, d, dtype, code, seed=d + hq, pad=pad)
+    want = c.reference()
+    c.run()
+    c.check(want)
+    assert torch.equal(c.q_out, c.q)
+    # once more: the same scales and codes
+    c.run()
+    c.check(want)
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+def test_a_block_written_token_by_token(code):
+    """The scale doubles whenever a token does not fit; the older codes follow, and what
+    they stand for stays within half a step for each doubling (INT8: half a step of the
+    new scale; E4M3: half of the smallest code, the others lose nothing)."""
+    c = Append([0], [64], 2, 3, 128, BF16, code, seed=3)
+    slots, x = c.slots.clone(), [c.k.clone(), c.v.clone()]
+    for t in range(64):
+        want = append_reference(c.k_pages, c.scales, 0, slots[t:t + 1], x[0][t:t + 1].float())
+        want_v = append_reference(c.v_pages, want[1], 1, slots[t:t + 1], x[1][t:t + 1].float())
+        c.run(slots=slots[t:t + 1], q=c.q[t:t + 1], k=x[0][t:t + 1], v=x[1][t:t + 1],
+              q_out=c.q_out[t:t + 1])
+        c.check((want[0], want_v[0], want_v[1]))
+    page, row = slots // PAGE, slots % PAGE
+    for which, pool in ((0, c.k_pages), (1, c.v_pages)):
+        got = decoded(pool, c.scales, which)[page, :, row]
+        scale = c.scales[page, :, which, row // BLOCK].double()[..., None]
+        exact = x[which].double()
+        if code == INT8:  # at most six halvings of steps: 1/2 + 1/2 + 1/4 ..
+            tol = 1.01 * scale
+        else:
+            tol = 2.0**-4 * exact.abs() + 2.0**-9 * scale
+        assert ((got - exact).abs() <= tol + 2.0**-21 * exact.abs()).all()
+        top = exact.abs().amax(-1).view(4, BLOCK, 3).amax(1)  # the scale is at most twice need
+        need = top / LARGEST[code]
+        s = c.scales[page[::BLOCK], :, which, (row // BLOCK)[::BLOCK]].double()
+        assert (s >= need * (1 - 2.0**-22)).all()
+        first = exact.abs().amax(-1).view(4, BLOCK, 3)[:, 0] / LARGEST[code]
+        assert (s <= torch.maximum(2 * need, first) * (1 + 2.0**-22)).all()
+
+
+@pytest.mark.parametrize("cached,new,hq,hkv,d,dtype,code,sections,interleaved,start", [
+    ([0], [1], 1, 1, 64, BF16, E4M3, [32], False, 0),
+    ([699], [1], 32, 8, 128, F16, INT8, [64], False, (1 << 20) - 1),
+    ([5, 0], [3, 18], 12, 1, 256, BF16, E4M3, [128], False, 1 << 24),
+    ([0, 33], [65, 20], 6, 3, 128, F16, INT8, [16, 24, 24], True, 3),
+    ([0], [130], 5, 5, 64, BF16, INT8, [8, 0, 8], False, 9),
+    ([10, 16], [33, 48], 8, 2, 256, F16, E4M3, [24, 40], True, 77),
+    ([0, 1], [3, 2], 0, 2, 128, BF16, E4M3, [32], True, 5),
+    ([64] * 20, [7] * 20, 16, 16, 64, F16, E4M3, [5, 7, 4], False, 2**31 - 6000)])
+def test_append_with_turning(cached, new, hq, hkv, d, dtype, code, sections, interleaved, start):
+    c = Append(cached, new, hq, hkv, d, dtype, code, seed=d + 50, pad=2)
+    g = generator(d + hq)
+    T, pairs = len(c.slots), sum(sections)
+    freq = 10000.0 ** (-torch.arange(pairs, device=DEV, dtype=torch.float64) / pairs)
+    pos = (start + torch.randint(0, 5000, (len(sections), T), generator=g, device=DEV)).int()
+    # fresh scales only: the tokens before in a begun block hold little
+    for b, a in enumerate(cached):
+        if a % BLOCK:
+            page = int(c.table[b, a // PAGE])
+            c.scales[page, :, :, a % PAGE // BLOCK] = 2.0**-40
+    v_want, v_scales, _ = append_reference(c.v_pages, c.scales, 1, c.slots, c.v.float())
+    before = c.state()
+    c.run(dsa.Rope(freq, sections, interleaved), pos)
+    if hq:
+        ref, size = turn_reference(c.q, pos, freq, sections, interleaved)
+        small = 2.0**-25 if dtype == F16 else 0.0
+        tol = torch.finfo(dtype).eps / 2 * ref.abs() + small + 2.0**-21 * size
+        assert ((c.q_out.double() - ref).abs() <= tol).all()
+    # values are not turned
+    assert torch.equal(c.v_pages.view(torch.uint8), v_want.view(torch.uint8))
+    assert torch.equal(c.scales[:, :, 1], v_scales[:, :, 1])
+    live = c.slots >= 0
+    slots = c.slots[live]
+    ref, size = turn_reference(c.k, pos, freq, sections, interleaved)
+    ref, size = ref[live], size[live]
+    page, row = slots // PAGE, slots % PAGE
+    scale = c.scales[page, :, 0, row // BLOCK].double()
+    blocks = slots // BLOCK
+    for block in blocks.unique().tolist():
+        at = blocks == block
+        need = ref[at].abs().amax((0, 2)) / LARGEST[code]
+        slack = 2.0**-21 * size[at].amax((0, 2)) / LARGEST[code] + 2.0**-23 * need
+        s = scale[at][0]
+        assert (s >= need - slack).all()
+        if int(slots[at][0]) % BLOCK == 0:
+            assert (s <= need + slack).all()
+        else:
+            k = torch.log2(s) + 40
+            assert (k == k.round()).all() and (s <= 2 * (need + slack)).all()
+    got = decoded(c.k_pages, c.scales, 0)[page, :, row]
+    scale = scale[..., None]
+    step = scale / 2 if code == INT8 else 2.0**-4 * ref.abs() + 2.0**-10 * scale
+    assert ((got - ref).abs() <= step + 2.0**-21 * size * 1.07 + 2.0**-22 * ref.abs()).all()
+    # rows of other blocks are as they were
+    touched = torch.zeros(c.pages, PAGE, dtype=torch.bool, device=DEV)
+    touched[page, row // BLOCK * BLOCK] = True
+    touched = touched.view(c.pages, -1, BLOCK)[:, :, :1].expand(-1, -1, BLOCK).reshape(c.pages, PAGE)
+    keep = ~touched[:, None, :, None].expand_as(c.k_pages)
+    assert torch.equal(c.k_pages.view(torch.uint8)[keep], before[0][keep])
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+def test_infinite_and_nan_values_are_recorded(code):
+    c = Append([3], [4], 2, 2, 64, BF16, code, seed=4)
+    c.k[1, 0, 5] = INF
+    c.k[2, 1, 7] = NAN
+    c.v[0, 0, 0] = -INF
+    clean = [x.clone() for x in (c.k, c.v)]
+    for x in clean:
+        x[~torch.isfinite(x)] = 0
+    want_k, scales, _ = append_reference(c.k_pages, c.scales, 0, c.slots, clean[0].float())
+    want_v, scales, _ = append_reference(c.v_pages, scales, 1, c.slots, clean[1].float())
+    c.run(status=DEVICE_CHECK)
+    assert torch.equal(c.scales, scales)
+    page, row = c.slots // PAGE, c.slots % PAGE
+    assert float(c.k_pages[page[1], 0, row[1], 5]) == LARGEST[code]
+    assert float(c.v_pages[page[0], 0, row[0], 0]) == -LARGEST[code]
+    nan = float(c.k_pages[page[2], 1, row[2], 7])
+    assert nan != nan if code == E4M3 else nan == 0
+    for got, want, at in ((c.k_pages, want_k, ((1, 0, 5), (2, 1, 7))), (c.v_pages, want_v, ((0, 0, 0),))):
+        got, want = got.view(torch.uint8).clone(), want.view(torch.uint8)
+        for t, h, i in at:
+            got[page[t], h, row[t], i] = want[page[t], h, row[t], i]
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+def test_zeros_and_sizes_beyond_the_scales(code):
+    """A block of zeros takes the smallest scale and grows out of it; values above L * 2^32
+    saturate."""
+    c = Append([0, 0, 16], [3, 2, 2], 1, 1, 64, BF16, code, seed=5)
+    c.k[:3] = 0
+    c.v[3:5] = 2.0**60
+    c.v[4, 0, 1] = -(2.0**100)
+    want = c.reference()
+    c.run()
+    c.check(want)
+    assert float(c.scales[c.slots[0] // PAGE, 0, 0, 0]) == 2.0**-48
+    assert float(c.scales[c.slots[3] // PAGE, 0, 1, 0]) == 2.0**32
+    at = c.slots[4:5]
+    assert float(c.v_pages[at // PAGE, 0, at % PAGE, 1]) == -LARGEST[code]
+    # the next token of the block of zeros
+    nxt = c.slots[2:3] + 1
+    k, v = torch.randn(2, 1, 1, 64, device=DEV).to(BF16)
+    want_k, scales, _ = append_reference(c.k_pages, c.scales, 0, nxt, k.float())
+    want_v, scales, _ = append_reference(c.v_pages, scales, 1, nxt, v.float())
+    c.run(slots=nxt, q=c.q[:1], k=k, v=v, q_out=c.q_out[:1])
+    c.check((want_k, want_v, scales))
+
+
+@pytest.mark.parametrize("bad", [0.0, -1.0, NAN, INF, 2.0**-60, 2.0**40])
+def test_a_begun_block_without_a_scale_is_recorded_and_left(bad):
+    c = Append([5, 64], [3, 20], 2, 2, 64, BF16, INT8, seed=6)
+    page = int(c.table[0, 0])
+    c.scales[page, 1, 0, 0] = bad
+    want = c.reference(torch.where(torch.arange(23, device=DEV) < 3, -1, c.slots))
+    first = c.reference(torch.where(torch.arange(23, device=DEV) < 3, c.slots, -1))
+    c.run(status=DEVICE_CHECK)
+    # head 1's keys of the first request's block stay; all else is written
+    for got, w, f, old in ((c.k_pages, want[0], first[0], True), (c.v_pages, want[1], first[1], False)):
+        for h in range(2):
+            for p in range(c.pages):
+                src = w if p != page or (h == 1 and old) else f
+                assert torch.equal(got[p, h], src[p, h])
+
+
+def test_slots_out_of_order_or_range_are_recorded_and_skipped():
+    c = Append([0], [12], 2, 2, 128, F16, INT8, seed=8)
+    base = int(c.slots[0])
+    slots = c.slots.clone()
+    slots[2] = c.pages * PAGE      # beyond the pool; ends the run of rows 0, 1
+    slots[3:] = -1
+    want = c.reference(torch.where(torch.arange(12, device=DEV) < 2, slots, -1))
+    c.run(status=DEVICE_CHECK, slots=slots)
+    c.check(want)
+    c = Append([0], [12], 2, 2, 128, F16, INT8, seed=8)
+    slots = c.slots.clone()
+    slots[5] = base + 2            # a second time: it and nothing else is left out
+    keep = slots.clone()
+    keep[5] = -1
+    want = c.reference(keep)
+    c.run(status=DEVICE_CHECK, slots=slots)
+    c.check(want)
+    c = Append([0], [40], 2, 2, 128, F16, INT8, seed=9)
+    slots = c.slots.clone()
+    slots[:] = base                # always the same row: the first is kept
+    keep = slots.clone()
+    keep[1:] = -1
+    want = c.reference(keep)
+    c.run(status=DEVICE_CHECK, slots=slots)
+    c.check(want)
+
+
+def test_append_in_place_and_from_separate_tensors():
+    results = []
+    for fused in (True, False):
+        c = Append([9], [40], 4, 2, 128, BF16, E4M3, seed=10)
+        freq = 10000.0 ** (-torch.arange(64, device=DEV, dtype=torch.float64) / 64)
+        pos = torch.arange(40, dtype=torch.int32, device=DEV)
+        kw = dict(q_out=c.q) if fused else dict(q=c.q.contiguous(), k=c.k.contiguous(),
+                                                v=c.v.contiguous())
+        c.run(dsa.Rope(freq), pos, **kw)
+        results.append(c.state() + [(c.q if fused else c.q_out).contiguous()])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("dtype,code", [(BF16, E4M3), (F16, E4M3), (BF16, INT8), (F16, INT8)])
+@pytest.mark.parametrize("d,hkv", [(64, 1), (128, 8), (256, 3)])
+@pytest.mark.parametrize("lens,new", [([1], [1]), ([700, 64, 65, 3], [700, 64, 65, 3]),
+                                      ([300, 17, 90], [5, 0, 90]), ([4, 1000], [7, 100])])
+def test_read(dtype, code, d, hkv, lens, new):
+    """Whole requests, their last tokens, and more tokens than there is context: those rows,
+    and the rows behind the last token, stay."""
+    g = generator(d + len(lens))
+    table, pages = tables_of(g, lens)
+    k, v, scales = random_cache(g, pages, hkv, d, code)
+    offsets = [0]
+    for n in new:
+        offsets.append(offsets[-1] + n)
+    T = offsets[-1]
+    wide = torch.full((T + 2, 2 * hkv + 1, d), 7.0, dtype=dtype, device=DEV)
+    want = wide.clone()
+    for b, (length, n) in enumerate(zip(lens, new)):
+        for j in range(n):
+            p = length - n + j
+            if p >= 0:
+                page, row = table[b, p // PAGE].long(), p % PAGE
+                for which, x in ((0, k), (1, v)):
+                    # fp32 product, rounded once
+                    y = x[page, :, row].float() * scales[page, :, which, row // BLOCK][..., None]
+                    want[offsets[b] + j, which * hkv:(which + 1) * hkv] = y.to(dtype)
+    batch = dsa.Batch(i32(offsets), i32(lens), table, pages, lens, new)
+    cache, st = dsa.QuantCache(k, v, scales), i32([0])
+    dsa.dsa_quant_read(batch, cache, wide[:, :hkv], wide[:, hkv:2 * hkv], st)
+    assert torch.equal(wide, want) and int(st.item()) == 0
+    for which in (0, 1):  # one of the two
+        one = torch.full((T, hkv, d), 7.0, dtype=dtype, device=DEV)
+        dsa.dsa_quant_read(batch, cache, *((one, None) if which == 0 else (None, one)))
+        assert torch.equal(one, want[:T, which * hkv:(which + 1) * hkv])
+
+
+def test_read_records_bad_pages_and_requests():
+    g = generator(77)
+    lens = [200, 100, 70]
+    table, pages = tables_of(g, lens)
+    k, v, scales = random_cache(g, pages, 2, 64, INT8)
+    cache, T = dsa.QuantCache(k, v, scales), sum(lens)
+    offsets = [0, 200, 300, 370]
+
+    def read(table, seq_lens, status):
+        out = torch.full((T, 2, 64), 7.0, dtype=BF16, device=DEV)
+        st = i32([0])
+        dsa.dsa_quant_read(dsa.Batch(i32(offsets), i32(seq_lens), table, pages, lens, lens), cache,
+                           out, None, st)
+        assert int(st.item()) == status
+        return out
+    want = read(table, lens, 0)
+    bad = table.clone()
+    bad[0, 1], bad[1, 0] = pages, -3
+    out = read(bad, lens, DEVICE_CHECK)
+    skipped = torch.zeros(T, dtype=torch.bool, device=DEV)
+    skipped[64:128] = skipped[200:264] = True
+    assert (out[skipped] == 7).all() and torch.equal(out[~skipped], want[~skipped])
+    out = read(table, [200, 1 << 20, 70], DEVICE_CHECK)
+    skipped[:] = False
+    skipped[200:300] = True
+    assert (out[skipped] == 7).all() and torch.equal(out[~skipped], want[~skipped])
+
+
+def test_scales_outside_their_range_count_as_its_ends():
+    g = generator(78)
+    table, pages = tables_of(g, [64])
+    k, v, scales = random_cache(g, pages, 1, 64, INT8)
+    page = int(table[0, 0])
+    scales[page, 0, 0] = torch.tensor([0.0, NAN, -3.0, INF], device=DEV)
+    out = torch.empty(64, 1, 64, dtype=BF16, device=DEV)
+    dsa.dsa_quant_read(dsa.Batch(i32([0, 64]), i32([64]), table, pages, [64], [64]),
+                       dsa.QuantCache(k, v, scales), out, None)
+    ends = torch.tensor([2.0**-48] * 3 + [2.0**33], device=DEV).repeat_interleave(16)
+    assert torch.equal(out[:, 0], (k[page, 0].float() * ends[:, None]).to(BF16))
+
+
+def test_a_pool_beyond_32_bit_offsets():
+    """More than 2^32 bytes of codes and 2^31 of elements, the last pages in use."""
+    c = Append([5, 40], [30, 90], 2, 8, 128, BF16, E4M3, seed=11)
+    want = c.reference()
+    n = c.pages
+    pages = (1 << 32) // (8 * PAGE * 128) + 50
+    big = [torch.empty(pages, 8, PAGE, 128, dtype=E4M3, device=DEV) for _ in range(2)]
+    scales = torch.empty(pages, 8, 2, 4, dtype=torch.float32, device=DEV)
+    for x, y in zip(big + [scales], (c.k_pages, c.v_pages, c.scales)):
+        x[pages - n:] = y
+    c.k_pages, c.v_pages, c.scales = *big, scales
+    c.run(slots=torch.where(c.slots >= 0, c.slots + (pages - n) * PAGE, -1))
+    batch = dsa.Batch(i32([0, 35, 165]), i32(c.lens), c.table + (pages - n), pages, c.lens, c.lens)
+    out = torch.empty(165, 8, 128, dtype=BF16, device=DEV)
+    dsa.dsa_quant_read(batch, dsa.QuantCache(*big, scales), out, None)
+    c.k_pages, c.v_pages, c.scales = (x[pages - n:] for x in (*big, scales))
+    c.check(want)
+    ref = decoded(want[0], want[2], 0)
+    rows = torch.cat([slots_of(c.table, [0], [n]) if b == 0 else slots_of(c.table[1:], [0], [n])
+                      for b, n in enumerate(c.lens)])
+    assert torch.equal(out, ref[rows // PAGE, :, rows % PAGE].float().to(BF16))
+
+
+def test_on_another_stream_and_in_a_graph():
+    c = Append([9, 64], [40, 1], 4, 2, 128, BF16, INT8, seed=12)
+    start = c.state()
+    want = c.reference()
+    cache = dsa.QuantCache(c.k_pages, c.v_pages, c.scales)
+    batch = dsa.Batch(i32([0, 49, 114]), i32(c.lens), c.table, c.pages, c.lens, c.lens)
+    out = torch.zeros(114, 2, 128, dtype=BF16, device=DEV)
+
+    def reset():
+        c.k_pages.view(torch.uint8).copy_(start[0])
+        c.v_pages.view(torch.uint8).copy_(start[1])
+        c.scales.copy_(start[2])
+        out.zero_()
+
+    def calls(stream=None):
+        dsa.dsa_quant_append(cache, None, None, c.slots, c.q, c.k, c.v, c.q_out, stream=stream)
+        dsa.dsa_quant_read(batch, cache, out, None, stream=stream)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    calls(s)
+    s.synchronize()
+    c.check(want)
+    read = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    reset()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(2):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(want)
+        assert torch.equal(out, read)
+
+
+def test_python_checks():
+    c = Append([0], [6], 4, 2, 64, BF16, E4M3, seed=13)
+    cache = dsa.QuantCache(c.k_pages, c.v_pages, c.scales)
+    pos = torch.zeros(1, 6, dtype=torch.int32, device=DEV)
+    rope = dsa.Rope(torch.ones(32, dtype=torch.float64, device=DEV))
+    for bad in (dict(q=c.q[:3]), dict(k=c.k[..., ::2]), dict(k=c.k.transpose(1, 2)),
+                dict(v=c.v.float()), dict(slots=c.slots[:5]), dict(slots=c.slots.int()),
+                dict(positions=pos.view(-1)[:5]), dict(q=c.q.cpu())):
+        kw = dict(positions=pos, slots=c.slots, q=c.q, k=c.k, v=c.v, q_out=c.q_out)
+        kw.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            dsa.dsa_quant_append(cache, rope, **kw)
+    for k, v, s in ((c.k_pages[:, :, :32], c.v_pages[:, :, :32], c.scales),
+                    (c.k_pages, c.v_pages[:1], c.scales), (c.k_pages, c.v_pages, c.scales[:, :, :1]),
+                    (c.k_pages.float(), c.v_pages.float(), c.scales),
+                    (c.k_pages, c.v_pages, c.scales.half()), (c.k_pages, c.v_pages.view(INT8), c.scales)):
+        with pytest.raises((TypeError, ValueError)):
+            dsa.QuantCache(k, v, s)
+    batch = dsa.Batch(i32([0, 6]), i32([6]), c.table, c.pages, [6], [6])
+    out = torch.empty(6, 2, 64, dtype=BF16, device=DEV)
+    for k, v in ((out[:5], None), (out.float(), None), (out, out.half()), (out[..., ::2], None),
+                 (None, None), (out.view(6, 1, 128), None)):
+        with pytest.raises((TypeError, ValueError)):
+            dsa.dsa_quant_read(batch, cache, k, v)
+    assert encode(torch.tensor([0.5]), INT8).item() == 0  # the oracle's ties go to even

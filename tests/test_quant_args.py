@@ -1,0 +1,126 @@
+"""Argument checks of the 8-bit cache's entry points (CPU only: every call here is refused
+before anything is launched)."""
+import ctypes
+
+import pytest
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+FAKE = ctypes.c_void_p(4096)  # never dereferenced
+ODD = ctypes.c_void_p(4100)   # not 16-byte aligned
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dsa_sparse_attention_step_gb300 import _build
+    _build.build()
+    import dsa_sparse_attention_step_gb300 as dsa
+    return dsa.load()
+
+
+def _cache(**kw):
+    import dsa_sparse_attention_step_gb300 as dsa
+    c = dsa._CQuantCache(8, 2, 128, 0, 1 << 20, 2 << 20, 3 << 20)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def _batch(**kw):
+    import dsa_sparse_attention_step_gb300 as dsa
+    b = dsa._CBatch(1, 1, 1, 4096, 8, 64, 64, 16, 32, 48)
+    for k, v in kw.items():
+        setattr(b, k, v)
+    return b
+
+
+def _append(lib, cache=None, fmt=0, tokens=3, axes=1, sections=(64, 0, 0), freq=4096,
+            positions=FAKE, slots=FAKE, hq=4, q=FAKE, qs=512, k=FAKE, ks=256, v=FAKE, vs=256,
+            out=FAKE, os=512, rope=True):
+    import dsa_sparse_attention_step_gb300 as dsa
+    r = dsa._CRope(axes, (ctypes.c_int32 * 3)(*sections), 0, freq)
+    c = _cache() if cache is None else cache
+    return lib.dsa_quant_append(tokens, ctypes.byref(c), fmt, ctypes.byref(r) if rope else None,
+                                positions, slots, hq, q, qs, k, ks, v, vs, out, os, None, None)
+
+
+def _read(lib, cache=None, batch=None, fmt=0, k=FAKE, ks=256, v=FAKE, vs=256):
+    c = _cache() if cache is None else cache
+    return lib.dsa_quant_read(ctypes.byref(_batch(**(batch or {}))), ctypes.byref(c), fmt, k, ks,
+                              v, vs, None, None)
+
+
+def _attention(lib, cache=None, batch=None, fmt=0, hq=4, q=FAKE, qs=512, sm=0.1, out=FAKE,
+               ws=FAKE, ws_bytes=1 << 40):
+    c = _cache() if cache is None else cache
+    return lib.dsa_quant_attention(ctypes.byref(_batch(**(batch or {}))), ctypes.byref(c), fmt, hq,
+                                   q, qs, sm, out, None, ws, ws_bytes, None, None)
+
+
+CACHE_REFUSALS = [
+    (dict(head_dim=96), UNSUPPORTED), (dict(format=2), UNSUPPORTED), (dict(format=-1), UNSUPPORTED),
+    (dict(num_pages=0), INVALID), (dict(num_kv_heads=0), INVALID),
+    (dict(num_pages=1 << 20, num_kv_heads=1 << 11), INVALID), (dict(k_pages=0), INVALID),
+    (dict(k_pages=8200), INVALID), (dict(v_pages=8200), INVALID), (dict(scales=0), INVALID),
+    (dict(scales=8196), INVALID)]
+
+
+@pytest.mark.parametrize("kw,code", CACHE_REFUSALS)
+def test_cache_refusals(lib, kw, code):
+    for call in (_append, _read, _attention):
+        assert call(lib, cache=_cache(**kw)) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(fmt=2), UNSUPPORTED), (dict(tokens=-1), INVALID), (dict(axes=4), UNSUPPORTED),
+    (dict(axes=-1), UNSUPPORTED), (dict(sections=(-8, 0, 0)), INVALID),
+    (dict(sections=(72, 0, 0)), INVALID), (dict(sections=(12, 0, 0)), UNSUPPORTED),
+    (dict(rope=False), INVALID), (dict(freq=0), INVALID), (dict(positions=None), INVALID),
+    (dict(slots=None), INVALID), (dict(q=None), INVALID), (dict(q=ODD), INVALID),
+    (dict(qs=516), INVALID), (dict(qs=504), INVALID), (dict(ks=248), INVALID),
+    (dict(vs=260), INVALID), (dict(k=ODD), INVALID), (dict(v=None), INVALID),
+    (dict(out=None), INVALID), (dict(os=500), INVALID), (dict(hq=-1), INVALID),
+    (dict(hq=1 << 15, qs=1 << 22, os=1 << 22), UNSUPPORTED)])
+def test_append_refusals(lib, kw, code):
+    assert _append(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(fmt=3), UNSUPPORTED), (dict(batch=dict(page_size=16)), UNSUPPORTED),
+    (dict(batch=dict(num_pages=9)), INVALID), (dict(batch=dict(max_pages=3)), INVALID),
+    (dict(k=ODD), INVALID), (dict(v=ODD), INVALID), (dict(ks=250), INVALID),
+    (dict(vs=248), INVALID)])
+def test_read_refusals(lib, kw, code):
+    assert _read(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=dict(page_size=32)), UNSUPPORTED), (dict(batch=dict(max_pages=10)), INVALID),
+    (dict(batch=dict(num_pages=9)), INVALID), (dict(fmt=2), UNSUPPORTED), (dict(hq=0), INVALID),
+    (dict(hq=5), INVALID), (dict(hq=1 << 15, qs=1 << 22), UNSUPPORTED), (dict(q=None), INVALID),
+    (dict(q=ODD), INVALID), (dict(qs=500), INVALID), (dict(sm=0.0), INVALID),
+    (dict(sm=float("nan")), INVALID), (dict(sm=float("inf")), INVALID), (dict(sm=1e-39), INVALID),
+    (dict(sm=3e38), INVALID), (dict(out=None), INVALID), (dict(out=ODD), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws=ODD), WORKSPACE), (dict(ws_bytes=1000), WORKSPACE),
+    # 2^20 new tokens of one request, each over up to 2^20 positions
+    (dict(batch=dict(total_q=1 << 20, max_q_per_request=1 << 20, max_seq_len=1 << 20,
+                     max_pages=1 << 14)), UNSUPPORTED)])
+def test_attention_refusals(lib, kw, code):
+    assert _attention(lib, **kw) == code
+
+
+def test_calls_without_tokens_are_no_ops(lib):
+    assert _append(lib, tokens=0) == 0
+    assert _read(lib, batch=dict(total_q=0), k=None) == 0
+    assert _read(lib, k=None, v=None) == 0
+    assert _attention(lib, batch=dict(total_q=0), q=None, out=None, ws=None) == 0
+
+
+def test_attention_workspace_follows_rows_and_head_dim(lib):
+    b = _batch(num_requests=4, total_q=4)
+
+    def size(hq, **kw):
+        return lib.dsa_quant_attention_workspace_size(ctypes.byref(b), ctypes.byref(_cache(**kw)),
+                                                      hq)
+    assert 0 < size(4) <= size(64) <= size(128)
+    assert size(4, head_dim=256) > size(4) > size(4, head_dim=64)
+    assert size(5) == 0 and size(0) == 0 and size(4, head_dim=96) == 0
