@@ -11,11 +11,14 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = DSA_QUANT_BLOCK;
 constexpr int kPageBlocks = kPage / kBlock;
 constexpr int kMaxTokens = 16;  // of a CTA
+constexpr int kSpan = kMaxTokens + kBlock - 1;  // tokens whose angles a CTA may need
+constexpr int kAhead = 2;       // 16-value units of queries that a thread has in flight
 constexpr float kMinScale = 0x1p-48f, kMaxNeed = 0x1p32f, kMaxScale = 0x1p33f;
 
 struct QuantArgs {
     int32_t num_tokens, q_heads, kv_heads, interleaved, pairs;
     int32_t tokens;      // of a CTA
+    int32_t axes;
     int32_t end0, end1;  // first pair of the second and of the third section
     int64_t slot_end;
     const double* inv_freq;
@@ -83,11 +86,18 @@ __device__ __forceinline__ int doublings(float scale, float need) {
     return max(0, (int)(n >> 23) - (int)(s >> 23) + ((n & 0x7fffffu) > (s & 0x7fffffu)));
 }
 
-// A value that the scale does not cover, or NaN, which INT8 has no code for.
-template <bool kInt8>
-__device__ __forceinline__ float within(float x, float most) {
-    if (x != x) return kInt8 ? 0.f : x;
-    return fminf(fmaxf(x, -most), most);
+// The larger, or NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Nothing; but values formed from these before are not known to be those formed after, and
+// so not kept, at twice the registers.
+__device__ __forceinline__ void opaque(uint4& a, uint4& b) {
+    asm volatile("" : "+r"(a.x), "+r"(a.y), "+r"(a.z), "+r"(a.w), "+r"(b.x), "+r"(b.y), "+r"(b.z),
+                      "+r"(b.w));
 }
 
 // The tokens of one block that stand together: the first of them, from the CTA's first
@@ -98,15 +108,76 @@ struct Run {
     int32_t pad;
 };
 
+// A way through [tokens][each] in steps, without a division for each.
+struct Stride2 {
+    int token, rest, each, step_token, step_rest;
+    __device__ __forceinline__ Stride2(int each_, int begin, int step) : each(each_) {
+        token = begin / each;
+        rest = begin - token * each;
+        step_token = step / each;
+        step_rest = step - step_token * each;
+    }
+    __device__ __forceinline__ bool next() {  // whether it has wrapped
+        token += step_token;
+        rest += step_rest;
+        if (rest < each) return false;
+        rest -= each;
+        ++token;
+        return true;
+    }
+};
+
+// A thread's way over the queries of a CTA's tokens, 16 values of a head at a time (the two
+// halves of eight pairs, or neighbours): its unit of the heads stays the same, as the steps
+// are multiples of a head's units.
+template <typename T, int kDim>
+struct Queries {
+    static constexpr int kUnits = kDim / 16;
+    Stride2 way;
+    T* p;
+    int64_t step, wrap;  // of p
+    __device__ __forceinline__ Queries(const T* base, int64_t stride, int heads, int begin,
+                                       int by)
+        : way(heads * kUnits, begin, by) {
+        p = const_cast<T*>(base) + way.token * stride + way.rest / kUnits * kDim;
+        step = way.step_token * stride + way.step_rest / kUnits * kDim;
+        wrap = stride - (int64_t)heads * kDim;
+    }
+    __device__ __forceinline__ void next() { p += way.next() ? step + wrap : step; }
+};
+
+// The largest magnitude of 8 values, NaN if there is one, in both halves of a pair.
+template <typename T>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t max_abs2<__nv_bfloat16>(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t max_abs2<__half>(uint32_t a, uint32_t b) {
+    const __half2 r = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(&a)),
+                                  __habs2(*reinterpret_cast<const __half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max_abs8(uint32_t m, const uint4& u) {
+    return max_abs2<T>(max_abs2<T>(max_abs2<T>(max_abs2<T>(m, u.x), u.y), u.z), u.w);
+}
+
 template <typename T, bool kInt8, int kDim>
-__global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantArgs a) {
     constexpr int kUnits = kDim / 16;     // 16 values of a row to a lane
     constexpr int kRows = 32 / kUnits;    // of a warp at a time
     constexpr int kSteps = kBlock / kRows;
+    constexpr int kLoads = kSteps < 4 ? kSteps : 4;  // steps in flight
     extern __shared__ float2 s_turn[];    // of each token, turn_at()
     __shared__ int64_t s_slot[kMaxTokens + kBlock];  // from the token before the CTA's on
     __shared__ Run s_run[kMaxTokens];
     __shared__ int s_runs, s_reach;
+    __shared__ unsigned long long s_rate[kDim / 2];
+    __shared__ int32_t s_pos[3 * kSpan];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t first = (int64_t)blockIdx.x * a.tokens;
     const int count = (int)min((int64_t)a.tokens, a.num_tokens - first);
@@ -115,7 +186,28 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
     grid_dependents_launch();
     grid_dependency_wait();
 
+    // the first queries are on their way while slots are looked at and angles formed
+    const int q_end = a.q_heads > 0 ? count : 0;
+    const int begin = tid + kThreads * blockIdx.y, step = kThreads * gridDim.y;
+    const int q_unit = tid % kUnits;
+    const bool q_turned = q_unit < a.pairs / 8, q_halves = q_turned && !a.interleaved;
+    const int q_at0 = q_halves ? q_unit * 8 : q_unit * 16;
+    const int q_at1 = q_halves ? q_unit * 8 + a.pairs : q_unit * 16 + 8;
+    Queries<T, kDim> ahead(static_cast<const T*>(a.q) + first * a.q_stride, a.q_stride,
+                           max(a.q_heads, 1), begin, step);
+    uint4 q_lo[kAhead], q_hi[kAhead];
+    auto load_query = [&](int x) {
+        if (ahead.way.token < q_end) {
+            q_lo[x] = *reinterpret_cast<const uint4*>(ahead.p + q_at0);
+            q_hi[x] = *reinterpret_cast<const uint4*>(ahead.p + q_at1);
+        }
+        ahead.next();
+    };
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) load_query(x);
+
     if (warp == 0) {
+        static_assert(kSpan < 32, "a lane to each token");
         int64_t slot = -1;
         const int64_t t = first + lane - 1;
         if (lane <= reach && t >= 0) {
@@ -142,8 +234,7 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
             Run r;
             r.first = lane;
             // tokens behind this one that are joined to their predecessor
-            const uint32_t rest = lane < 31 ? ~(all_joined >> (lane + 1)) : 1u;
-            r.count = min(1 + __ffs(rest) - 1, kBlock);
+            r.count = min(__ffs(~(all_joined >> (lane + 1))), kBlock);
             r.stored = (all_ascend >> lane) & ((1u << r.count) - 1u);
             end = lane + r.count;
             s_run[__popc(leaders & ((1u << lane) - 1u))] = r;
@@ -153,20 +244,61 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
             s_runs = __popc(leaders);
             s_reach = max(end, a.q_heads > 0 ? count : 0);
         }
+    } else if (warp < kWarps / 2) {
+        if (a.pairs > 0)
+            for (int i = tid - 32; i < a.axes * kSpan; i += kThreads / 2 - 32)
+                if (i % kSpan < reach)
+                    s_pos[i] = __ldg(a.positions + (int64_t)(i / kSpan) * a.num_tokens + first +
+                                     i % kSpan);
+    } else {
+        // double precision is slow here: once for a pair, not for each of its angles
+        for (int i = tid - kThreads / 2; i < a.pairs; i += kThreads / 2)
+            s_rate[i] = turn_rate(__ldg(a.inv_freq + i));
     }
     __syncthreads();
-    for (int i = tid; i < s_reach * a.pairs; i += kThreads) {
-        const int j = i / a.pairs, pair = i - j * a.pairs;
-        const int axis = (pair >= a.end0 ? 1 : 0) + (pair >= a.end1 ? 1 : 0);
-        const int pos = __ldg(a.positions + (int64_t)axis * a.num_tokens + first + j);
-        s_turn[j * a.pairs + turn_at(pair, a.pairs)] = turn_of(__ldg(a.inv_freq + pair), pos);
+    if (a.pairs > 0) {
+        int j = tid / a.pairs, pair = tid - j * a.pairs;
+        const int step_j = kThreads / a.pairs, step_pair = kThreads - step_j * a.pairs;
+        while (j < s_reach) {
+            const int axis = (pair >= a.end0 ? 1 : 0) + (pair >= a.end1 ? 1 : 0);
+            s_turn[j * a.pairs + turn_at(pair, a.pairs)] =
+                fine_turn_of(s_rate[pair], s_pos[axis * kSpan + j]);
+            j += step_j;
+            pair += step_pair;
+            if (pair >= a.pairs) {
+                pair -= a.pairs;
+                ++j;
+            }
+        }
     }
     __syncthreads();
 
+    // Queries: a thread to 16 values.
+    Queries<T, kDim> here(static_cast<const T*>(a.q_out) + first * a.q_out_stride, a.q_out_stride,
+                          max(a.q_heads, 1), begin, step);
+    while (here.way.token < q_end) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            if (here.way.token < q_end) {
+                float v[8], w[8];
+                unpack8<T>(q_lo[x], v);
+                unpack8<T>(q_hi[x], w);
+                if (q_turned)
+                    turn16(v, w, s_turn + here.way.token * a.pairs, a.pairs / 8, q_unit,
+                           a.interleaved);
+                store8(here.p + q_at0, v);
+                store8(here.p + q_at1, w);
+            }
+            here.next();
+            load_query(x);
+        }
+    }
+
     // Keys and values: a warp to a run's head.
-    const int items = s_runs * 2 * a.kv_heads;
-    for (int item = warp + kWarps * blockIdx.y; item < items; item += kWarps * gridDim.y) {
-        const int i_run = item / (2 * a.kv_heads), rest = item - i_run * 2 * a.kv_heads;
+    const int unit = lane % kUnits, row0 = lane / kUnits;
+    for (Stride2 item(2 * a.kv_heads, warp + kWarps * blockIdx.y, kWarps * gridDim.y);
+         item.token < s_runs; item.next()) {
+        const int i_run = item.token, rest = item.rest;
         const int which = rest >= a.kv_heads, head = rest - which * a.kv_heads;
         const Run run = s_run[i_run];
         const int64_t slot0 = s_slot[run.first + 1];
@@ -179,50 +311,68 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
         const float begun = *scale_at;
         const T* const src = which ? static_cast<const T*>(a.v) : static_cast<const T*>(a.k);
         const int64_t stride = which ? a.v_stride : a.k_stride;
-        const int unit = lane % kUnits, row0 = lane / kUnits;
         const bool turned = !which && unit < a.pairs / 8;
         const bool halves = turned && !a.interleaved;
         const int at0 = halves ? unit * 8 : unit * 16;
         const int at1 = halves ? unit * 8 + a.pairs : unit * 16 + 8;
-        uint4 lo[kSteps], hi[kSteps];
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int j = s * kRows + row0;
-            lo[s] = hi[s] = make_uint4(0, 0, 0, 0);
-            if (run.stored >> j & 1) {
-                const T* p = src + (first + run.first + j) * stride + head * kDim;
-                lo[s] = *reinterpret_cast<const uint4*>(p + at0);
-                hi[s] = *reinterpret_cast<const uint4*>(p + at1);
+        // Two passes over the values.  Up to 128 dims their 16-bit forms stay in registers
+        // in between; 256 read them once more, from the caches.
+        const T* const from = src + (first + run.first + row0) * stride + head * kDim;
+        auto load = [&](int s, uint4& lo, uint4& hi) {
+            lo = hi = make_uint4(0, 0, 0, 0);
+            if (run.stored >> (s * kRows + row0) & 1) {
+                const T* p = from + s * kRows * stride;
+                lo = *reinterpret_cast<const uint4*>(p + at0);
+                hi = *reinterpret_cast<const uint4*>(p + at1);
             }
-        }
-        auto values = [&](int s, float (&x)[8], float (&y)[8]) {
-            unpack8<T>(lo[s], x);
-            unpack8<T>(hi[s], y);
+        };
+        auto values = [&](int s, const uint4& lo, const uint4& hi, float (&x)[8], float (&y)[8]) {
+            unpack8<T>(lo, x);
+            unpack8<T>(hi, y);
             if (turned)
                 turn16(x, y, s_turn + (run.first + s * kRows + row0) * a.pairs, a.pairs / 8, unit,
                        a.interleaved);
         };
-        // the largest magnitude as bits, above infinity's for a NaN
-        uint32_t top = 0;
+        // the largest magnitude; NaN if there is one
+        float most = 0.f;
+        uint32_t most2 = 0;  // of a pair of values as they are
+        const bool as_is = which || a.pairs == 0;
+        uint4 lo[kLoads], hi[kLoads];
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-            if (run.stored >> (s * kRows + row0) & 1) {
+        for (int s0 = 0; s0 < kSteps; s0 += kLoads) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) load(s0 + i, lo[i], hi[i]);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                if (as_is) {
+                    most2 = max_abs8<T>(max_abs8<T>(most2, lo[i]), hi[i]);
+                    continue;
+                }
                 float x[8], y[8];
-                values(s, x, y);
+                values(s0 + i, lo[i], hi[i], x, y);
+                // of a row that is not stored the values are 0, or 0 turned by what its
+                // place in shared memory holds
+                if (run.stored >> ((s0 + i) * kRows + row0) & 1)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu,
-                                       __float_as_uint(y[i]) & 0x7fffffffu));
+                    for (int e = 0; e < 8; ++e)
+                        most = max_nan(most, max_nan(fabsf(x[e]), fabsf(y[e])));
             }
-        top = __reduce_max_sync(0xffffffffu, top);
+        }
+        if (as_is) {
+            const float2 m = to_float2<T>(most2);
+            most = max_nan(m.x, m.y);
+        }
+        uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu);
         const bool odd = top >= 0x7f800000u;
         if (odd) {  // of the finite values only
             if (lane == 0) record_error(a.status, DSA_ERR_DEVICE_CHECK);
             top = 0;
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < kSteps; ++s) {
+                uint4 l, h;
+                load(s, l, h);
                 float x[8], y[8];
-                values(s, x, y);
+                values(s, l, h, x, y);
                 if (run.stored >> (s * kRows + row0) & 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -234,7 +384,6 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
         }
         const float all = __fdiv_rn(__uint_as_float(top), largest<kInt8>());
         const float need = fminf(fmaxf(all, kMinScale), kMaxNeed);
-        const bool saturates = odd || all > kMaxNeed;
         if (!fresh && !(begun >= kMinScale && begun <= kMaxScale)) {
             if (lane == 0) record_error(a.status, DSA_ERR_DEVICE_CHECK);
             continue;
@@ -243,25 +392,47 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
         const float scale = fresh ? need : __uint_as_float(__float_as_uint(begun) + (k << 23));
         const float by = __frcp_rn(scale);
 
-        // which of the block's rows this call writes
-        uint32_t written = 0;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int j = s * kRows + row0;
-            if (!(run.stored >> j & 1)) continue;
-            const int row = (int)(s_slot[run.first + j + 1] % kBlock);
+        uint32_t written = 0;  // which of the block's rows this call writes
+        auto write = [&](int s, const float (&x)[8], const float (&y)[8]) {
+            const int row = (int)(s_slot[run.first + s * kRows + row0 + 1]) % kBlock;
             written |= 1u << row;
-            float x[8], y[8];
-            values(s, x, y);
-            if (saturates)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = within<kInt8>(x[i], __fmul_rn(scale, largest<kInt8>()));
-                    y[i] = within<kInt8>(y[i], __fmul_rn(scale, largest<kInt8>()));
-                }
             uint8_t* dst = block + row * kDim;
             *reinterpret_cast<uint2*>(dst + at0) = encode8<kInt8>(x, by);
             *reinterpret_cast<uint2*>(dst + at1) = encode8<kInt8>(y, by);
+        };
+        if (kInt8 && (odd || all > kMaxNeed)) {
+            // values that have no code (E4M3's conversion knows what to do with them)
+            const float most = __fmul_rn(scale, largest<kInt8>());
+#pragma unroll 1
+            for (int s = 0; s < kSteps; ++s) {
+                if (!(run.stored >> (s * kRows + row0) & 1)) continue;
+                uint4 l, h;
+                load(s, l, h);
+                float x[8], y[8];
+                values(s, l, h, x, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = x[e] != x[e] ? 0.f : fminf(fmaxf(x[e], -most), most);
+                    y[e] = y[e] != y[e] ? 0.f : fminf(fmaxf(y[e], -most), most);
+                }
+                write(s, x, y);
+            }
+        } else {
+#pragma unroll
+            for (int s0 = 0; s0 < kSteps; s0 += kLoads) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    if (kSteps > kLoads) load(s0 + i, lo[i], hi[i]);
+                    else opaque(lo[i], hi[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    if (run.stored >> ((s0 + i) * kRows + row0) & 1) {
+                        float x[8], y[8];
+                        values(s0 + i, lo[i], hi[i], x, y);
+                        write(s0 + i, x, y);
+                    }
+            }
         }
         if (k > 0) {
             written = __reduce_or_sync(0xffffffffu, written);
@@ -283,24 +454,6 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const QuantArgs 
             }
         }
         if (lane == 0 && (fresh || k > 0)) *scale_at = scale;
-    }
-
-    // Queries: a thread to 16 values.
-    const int units = count * a.q_heads * kUnits;
-    for (int i = tid + kThreads * blockIdx.y; i < units; i += kThreads * gridDim.y) {
-        const int j = i / (a.q_heads * kUnits), rest = i - j * (a.q_heads * kUnits);
-        const int head = rest / kUnits, unit = rest % kUnits;
-        const bool turned = unit < a.pairs / 8, halves = turned && !a.interleaved;
-        const int at0 = halves ? unit * 8 : unit * 16;
-        const int at1 = halves ? unit * 8 + a.pairs : unit * 16 + 8;
-        const T* src = static_cast<const T*>(a.q) + (first + j) * a.q_stride + head * kDim;
-        float x[8], y[8];
-        unpack8<T>(*reinterpret_cast<const uint4*>(src + at0), x);
-        unpack8<T>(*reinterpret_cast<const uint4*>(src + at1), y);
-        if (turned) turn16(x, y, s_turn + j * a.pairs, a.pairs / 8, unit, a.interleaved);
-        T* dst = static_cast<T*>(a.q_out) + (first + j) * a.q_out_stride + head * kDim;
-        store8(dst + at0, x);
-        store8(dst + at1, y);
     }
 }
 
@@ -471,6 +624,7 @@ cudaError_t launch_quant_append(int num_tokens, const dsa_quant_cache& cache, in
     a.end0 = ends[0];
     a.end1 = ends[1];
     a.tokens = 0;  // set by the launch
+    a.axes = rope.num_axes;
     a.slot_end = (int64_t)cache.num_pages * kPage;
     a.inv_freq = rope.inv_freq;
     a.positions = positions;

@@ -56,15 +56,35 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
 // fraction of a turn in 64 bits, times the position, modulo 2^64, is the fraction of the
 // turn (the product wraps exactly; the rate is off by less than 2^-53 turns per unit of
 // position).  Its upper 32 bits go to sincospi.
-__device__ __forceinline__ float2 turn_of(double inv_freq, int pos) {
-    // the fraction of a turn per unit of position, in units of 2^-64
+// The fraction of a turn per unit of position, in units of 2^-64.
+__device__ __forceinline__ unsigned long long turn_rate(double inv_freq) {
     double turns = inv_freq * 0.15915494309189533577;
     turns -= floor(turns);
-    const unsigned long long rate = (unsigned long long)(turns * 18446744073709551616.0);
+    return (unsigned long long)(turns * 18446744073709551616.0);
+}
+
+// In units of 2^-31 half turns.
+__device__ __forceinline__ int turn_angle(unsigned long long rate, int pos) {
     const long long angle = (long long)((unsigned long long)(long long)pos * rate);
+    return (int)(angle >> 32);
+}
+
+__device__ __forceinline__ float2 turn_of(double inv_freq, int pos) {
     float sn, cs;
-    sincospif((float)(int)(angle >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+    sincospif((float)turn_angle(turn_rate(inv_freq), pos) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
     return make_float2(cs, sn);
+}
+
+// The same from the rate, with what the angle loses as a float (up to 2^-25 half turns) given back, to
+// within 2^-31: cos(a + d) = cos a - d sin a, sin(a + d) = sin a + d cos a.
+__device__ __forceinline__ float2 fine_turn_of(unsigned long long rate, int pos) {
+    const int angle = turn_angle(rate, pos);
+    const float rounded = (float)angle;
+    const int lost = (int)((unsigned)angle - (unsigned)__float2int_rz(rounded * 0.5f) * 2u);
+    const float d = (float)lost * 1.4629180792671596e-9f;  // 2^-31 pi
+    float sn, cs;
+    sincospif(rounded * 4.656612873077393e-10f, &sn, &cs);
+    return make_float2(fmaf(-d, sn, cs), fmaf(d, cs, sn));
 }
 
 // A token's (cos, sin) in shared memory as [4][pairs / 8][2]: pair 8 u + 2 p + e at
