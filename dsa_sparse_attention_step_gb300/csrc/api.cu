@@ -78,6 +78,7 @@ cudaError_t launch_quant_read(const BatchArgs& bt, const dsa_quant_cache& cache,
                               void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
                               int32_t* status, cudaStream_t stream);
 float quant_score_scale(float sm_scale);
+size_t quant_attention_workspace_bytes(int64_t max_rows, int head_dim);
 cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
                                    float sm_scale, void* out, float* lse, void* ws, bool whole,
@@ -663,7 +664,7 @@ size_t dsa_quant_attention_workspace_size(const dsa_batch* batch, const dsa_quan
         num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0 ||
         (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256))
         return 0;
-    return paged_attention_workspace_bytes(
+    return quant_attention_workspace_bytes(
         (int64_t)batch->max_q_per_request * (num_q_heads / cache->num_kv_heads), cache->head_dim);
 }
 

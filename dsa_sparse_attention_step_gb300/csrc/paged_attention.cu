@@ -1,15 +1,16 @@
 // paged_attention.cu -- workspace, limits and dispatch of the paged attention
 // kernels (paged_attention.cuh), which are compiled per head dim.
-#include "paged_attention.cuh"
+#include "quant_attention_tc.cuh"
 
 namespace dsa {
 
 using namespace paged;
 
-// The parameters that do not depend on how the cache holds its elements.
+// The parameters that do not depend on how the cache holds its elements; part_rows: rows of
+// a tile that pieces are kept for.
 AttnParams attention_params(const BatchArgs& bt, int kv_heads, int head_dim, int num_q_heads,
                             const void* q, int64_t q_stride, void* out, float* lse, void* ws,
-                            bool whole, bool wait_test, int32_t* status) {
+                            int part_rows, bool whole, bool wait_test, int32_t* status) {
     AttnParams p;
     p.bt = bt;
     p.kv_heads = kv_heads;
@@ -23,8 +24,7 @@ AttnParams attention_params(const BatchArgs& bt, int kv_heads, int head_dim, int
     p.scales = nullptr;
     p.out = out;
     p.lse = lse;
-    const WsLayout w =
-        ws_layout(head_dim, row_tile(head_dim, (int64_t)bt.max_q * p.group, false));
+    const WsLayout w = ws_layout(head_dim, part_rows);
     uint8_t* base = static_cast<uint8_t*>(ws);
     p.part_o = reinterpret_cast<float*>(base);
     p.part_ml = reinterpret_cast<float*>(base + w.ml);
@@ -61,8 +61,10 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
                                    float sm_scale, void* out, float* lse, void* ws, bool whole,
                                    bool wait_test, int32_t* status, int* launches,
                                    cudaStream_t stream) {
+    const int64_t rows = (int64_t)bt.max_q * (num_q_heads / cache.num_kv_heads);
     AttnParams p = attention_params(bt, cache.num_kv_heads, cache.head_dim, num_q_heads, q,
-                                    q_stride, out, lse, ws, whole, wait_test, status);
+                                    q_stride, out, lse, ws, row_tile(cache.head_dim, rows, false),
+                                    whole, wait_test, status);
     p.v_pages = cache.v_pages;
     p.score_scale = paged_score_scale(sm_scale, cache);
     p.v_scale = cache.v_scale;
@@ -85,14 +87,30 @@ Launch launch_quant_attention_64_e4m3, launch_quant_attention_128_e4m3,
 Launch launch_quant_attention_64_int8, launch_quant_attention_128_int8,
     launch_quant_attention_256_int8;
 
+using TensorLaunch = cudaError_t(const AttnParams& p, const dsa_kv_cache& cache, int format,
+                                 bool int8, int* launches, cudaStream_t stream);
+TensorLaunch launch_quant_attention_tc_64, launch_quant_attention_tc_128,
+    launch_quant_attention_tc_256;
+
 float quant_score_scale(float sm_scale) { return sm_scale * kLog2e; }
+
+// Rows of a tile whose pieces the workspace has room for, whatever the switch says.
+static int quant_part_rows(int64_t max_rows, int head_dim) {
+    return tensor_rows(max_rows, false) ? 128 : row_tile(head_dim, max_rows, false);
+}
+
+size_t quant_attention_workspace_bytes(int64_t max_rows, int head_dim) {
+    return ws_layout(head_dim, quant_part_rows(max_rows, head_dim)).total;
+}
 
 cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
                                    float sm_scale, void* out, float* lse, void* ws, bool whole,
                                    int32_t* status, int* launches, cudaStream_t stream) {
+    const int64_t rows = (int64_t)bt.max_q * (num_q_heads / cache.num_kv_heads);
     AttnParams p = attention_params(bt, cache.num_kv_heads, cache.head_dim, num_q_heads, q,
-                                    q_stride, out, lse, ws, whole, false, status);
+                                    q_stride, out, lse, ws, quant_part_rows(rows, cache.head_dim),
+                                    whole, false, status);
     p.v_pages = cache.v_pages;
     p.scales = cache.scales;
     p.score_scale = quant_score_scale(sm_scale);
@@ -102,6 +120,12 @@ cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& c
     const dsa_kv_cache bytes = {cache.num_pages, cache.num_kv_heads, cache.head_dim,
                                 DSA_KV_FP8_E4M3, cache.k_pages, cache.v_pages, 1.f, 1.f};
     const bool int8 = cache.format == DSA_QUANT_INT8;
+    if (tensor_rows(rows, whole)) {
+        TensorLaunch* launch = cache.head_dim == 64    ? launch_quant_attention_tc_64
+                               : cache.head_dim == 128 ? launch_quant_attention_tc_128
+                                                       : launch_quant_attention_tc_256;
+        return launch(p, bytes, format, int8, launches, stream);
+    }
     Launch* launch;
     switch (cache.head_dim) {
         case 64: launch = int8 ? launch_quant_attention_64_int8 : launch_quant_attention_64_e4m3; break;

@@ -294,9 +294,13 @@ def test_requests_that_contradict_the_host_sizes_are_reported_and_not_written(ne
     out, lse = c.run(status=DEVICE_CHECK, batch=b)
     rows = slice(new, 2 * new)
     assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all()
-    ok, _ = c.run()
+    # the others as ever (to the last bit only where the plan runs them whole: without the
+    # second request the list is cut in other places)
+    r = c.reference()
+    tol, lse_tol = c.tolerances(r)
     keep = [t for t in range(3 * new) if not new <= t < 2 * new]
-    assert torch.equal(out[keep], ok[keep])
+    assert ((out.double() - r["out"]).abs() <= tol)[keep].all()
+    assert ((lse.double() - r["lse"]).abs() <= lse_tol)[keep].all()
 
 
 @pytest.mark.parametrize("lens,new", [([130, 700], [2, 1]), ([130, 700], [2, 300])])
