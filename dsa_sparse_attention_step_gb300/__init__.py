@@ -141,6 +141,8 @@ _SIGS = {
     "dsa_quant_attention_workspace_size": (_sz, [_bp, _qp, _i32]),
     "dsa_quant_attention": (ctypes.c_int, [_bp, _qp, ctypes.c_int, _i32, _vp, _i64, _f32, _vp, _vp,
                                            _vp, _sz, _vp, _vp]),
+    "dsa_test_quant_attention_wait_timeout": (ctypes.c_int, [
+        _bp, _qp, ctypes.c_int, _i32, _vp, _i64, _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "dsa_test_paged_attention_wait_timeout": (ctypes.c_int, [
         _bp, _kp, ctypes.c_int, _i32, _vp, _i64, _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "dsa_test_sparse_mla_wait_timeout": (ctypes.c_int, [_bp, _vp, _vp, _f32, _f32, _vp, _i32, _vp,
@@ -802,3 +804,12 @@ def dsa_quant_attention(batch, cache, q, sm_scale, out, lse=None, ws=None, dev_s
                         stream=None):
     """dsa_paged_attention over a QuantCache (see include/dsa.h)."""
     prepare_quant_attention(batch, cache, q, sm_scale, out, lse, ws, dev_status, stream)()
+
+
+def dsa_test_quant_attention_wait_timeout(batch, cache, q, sm_scale, out, lse=None, ws=None,
+                                          dev_status=None, stream=None):
+    """Test-only (include/dsa_testing.h): dsa_quant_attention with the kernel's
+    bounded-wait failure path forced; the device status becomes 6."""
+    call = prepare_quant_attention(batch, cache, q, sm_scale, out, lse, ws, dev_status, stream)
+    _check(load().dsa_test_quant_attention_wait_timeout(*call._args),
+           "dsa_test_quant_attention_wait_timeout")

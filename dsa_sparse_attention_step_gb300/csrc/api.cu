@@ -78,11 +78,13 @@ cudaError_t launch_quant_read(const BatchArgs& bt, const dsa_quant_cache& cache,
                               void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
                               int32_t* status, cudaStream_t stream);
 float quant_score_scale(float sm_scale);
-size_t quant_attention_workspace_bytes(int64_t max_rows, int head_dim);
+size_t quant_attention_workspace_bytes(const BatchArgs& bt, int num_q_heads, int kv_heads,
+                                       int head_dim);
 cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
                                    float sm_scale, void* out, float* lse, void* ws, bool whole,
-                                   int32_t* status, int* launches, cudaStream_t stream);
+                                   bool wait_test, int32_t* status, int* launches,
+                                   cudaStream_t stream);
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int32_t> g_batch_invariant{0};  // dsa_set_batch_invariant
@@ -664,14 +666,15 @@ size_t dsa_quant_attention_workspace_size(const dsa_batch* batch, const dsa_quan
         num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0 ||
         (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256))
         return 0;
-    return quant_attention_workspace_bytes(
-        (int64_t)batch->max_q_per_request * (num_q_heads / cache->num_kv_heads), cache->head_dim);
+    return quant_attention_workspace_bytes(to_args(batch), num_q_heads, cache->num_kv_heads,
+                                           cache->head_dim);
 }
 
-dsa_status dsa_quant_attention(const dsa_batch* batch, const dsa_quant_cache* cache,
-                               dsa_float_format format, int32_t num_q_heads, const void* q,
-                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
-                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream) {
+static dsa_status quant_attention(const dsa_batch* batch, const dsa_quant_cache* cache,
+                                  dsa_float_format format, int32_t num_q_heads, const void* q,
+                                  int64_t q_stride, float sm_scale, void* out, float* lse,
+                                  void* ws, size_t ws_bytes, bool wait_test, int32_t* dev_status,
+                                  dsa_stream_t stream) {
     dsa_status st = check_batch(batch, true);
     if (st != DSA_OK) return st;
     st = check_quant_cache(cache, format);
@@ -696,9 +699,25 @@ dsa_status dsa_quant_attention(const dsa_batch* batch, const dsa_quant_cache* ca
     int launches = 0;
     const dsa_status rc = cuda_status(launch_quant_attention(
         to_args(batch), *cache, (int)format, num_q_heads, q, q_stride, sm_scale, out, lse, ws,
-        whole, dev_status, &launches, (cudaStream_t)stream));
+        whole, wait_test, dev_status, &launches, (cudaStream_t)stream));
     g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
     return rc;
+}
+
+dsa_status dsa_quant_attention(const dsa_batch* batch, const dsa_quant_cache* cache,
+                               dsa_float_format format, int32_t num_q_heads, const void* q,
+                               int64_t q_stride, float sm_scale, void* out, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream) {
+    return quant_attention(batch, cache, format, num_q_heads, q, q_stride, sm_scale, out, lse, ws,
+                           ws_bytes, false, dev_status, stream);
+}
+
+dsa_status dsa_test_quant_attention_wait_timeout(
+    const dsa_batch* batch, const dsa_quant_cache* cache, dsa_float_format format,
+    int32_t num_q_heads, const void* q, int64_t q_stride, float sm_scale, void* out, float* lse,
+    void* ws, size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream) {
+    return quant_attention(batch, cache, format, num_q_heads, q, q_stride, sm_scale, out, lse, ws,
+                           ws_bytes, true, dev_status, stream);
 }
 
 }  // extern "C"

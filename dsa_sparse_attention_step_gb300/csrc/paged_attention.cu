@@ -95,22 +95,26 @@ TensorLaunch launch_quant_attention_tc_64, launch_quant_attention_tc_128,
 float quant_score_scale(float sm_scale) { return sm_scale * kLog2e; }
 
 // Rows of a tile whose pieces the workspace has room for, whatever the switch says.
-static int quant_part_rows(int64_t max_rows, int head_dim) {
-    return tensor_rows(max_rows, false) ? 128 : row_tile(head_dim, max_rows, false);
+static int quant_part_rows(const BatchArgs& bt, int num_q_heads, int kv_heads, int head_dim) {
+    return takes_tensor_cores(bt, num_q_heads, kv_heads, head_dim, false)
+               ? 128
+               : row_tile(head_dim, (int64_t)bt.max_q * (num_q_heads / kv_heads), false);
 }
 
-size_t quant_attention_workspace_bytes(int64_t max_rows, int head_dim) {
-    return ws_layout(head_dim, quant_part_rows(max_rows, head_dim)).total;
+size_t quant_attention_workspace_bytes(const BatchArgs& bt, int num_q_heads, int kv_heads,
+                                       int head_dim) {
+    return ws_layout(head_dim, quant_part_rows(bt, num_q_heads, kv_heads, head_dim)).total;
 }
 
 cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& cache, int format,
                                    int num_q_heads, const void* q, int64_t q_stride,
                                    float sm_scale, void* out, float* lse, void* ws, bool whole,
-                                   int32_t* status, int* launches, cudaStream_t stream) {
-    const int64_t rows = (int64_t)bt.max_q * (num_q_heads / cache.num_kv_heads);
-    AttnParams p = attention_params(bt, cache.num_kv_heads, cache.head_dim, num_q_heads, q,
-                                    q_stride, out, lse, ws, quant_part_rows(rows, cache.head_dim),
-                                    whole, false, status);
+                                   bool wait_test, int32_t* status, int* launches,
+                                   cudaStream_t stream) {
+    AttnParams p = attention_params(
+        bt, cache.num_kv_heads, cache.head_dim, num_q_heads, q, q_stride, out, lse, ws,
+        quant_part_rows(bt, num_q_heads, cache.num_kv_heads, cache.head_dim), whole,
+        wait_test, status);
     p.v_pages = cache.v_pages;
     p.scales = cache.scales;
     p.score_scale = quant_score_scale(sm_scale);
@@ -120,7 +124,7 @@ cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& c
     const dsa_kv_cache bytes = {cache.num_pages, cache.num_kv_heads, cache.head_dim,
                                 DSA_KV_FP8_E4M3, cache.k_pages, cache.v_pages, 1.f, 1.f};
     const bool int8 = cache.format == DSA_QUANT_INT8;
-    if (tensor_rows(rows, whole)) {
+    if (takes_tensor_cores(bt, num_q_heads, cache.num_kv_heads, cache.head_dim, whole)) {
         TensorLaunch* launch = cache.head_dim == 64    ? launch_quant_attention_tc_64
                                : cache.head_dim == 128 ? launch_quant_attention_tc_128
                                                        : launch_quant_attention_tc_256;

@@ -7,14 +7,14 @@
 //   O += P V     A = P from TMEM (f16, where S was), B = V; O in TMEM
 //
 // Codes are lifted to f16 once for all 128 rows: where mma.sync has every warp of 16 rows
-// lift for itself, which bounds it (40 rows over INT8 codes: 746 us where HBM takes 313),
+// lift for itself, which bounds it (40 rows over INT8 codes: 746 us where HBM takes 313; here 620),
 // eight warps here write the lifted tiles into the swizzled layout that both products read
 // (K as K-major, V as MN-major operand).  A thread of the softmax has half a row of S to
 // itself: no shuffles.  A block's key scale multiplies its 16 columns of S, its value scale goes
 // into the exponent, as in paged_attention.cuh.
 //
 // Warps: 0-7 softmax and epilogue (two threads to a row), 8-11 lift K (and bring Q), 12-15
-// lift V, 16 copies (TMA into a ring of code tiles, K and V in turn), 17 issues the MMAs: S
+// lift V, 16 and 18 copy (TMA into a ring of code tiles, K and V in turn), 17 issues the MMAs: S
 // of the next step before O of this one, so that the tensor cores run while the softmax
 // does.
 #pragma once
@@ -52,7 +52,7 @@ struct TcCfg {
     // a unit's queries, its first step alone and its epilogue: about 6000 cycles, in pages
     static constexpr int kUnitCost = kD == 64 ? 8 : 7;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kSoftmaxRegs = 144, kLiftRegs = 64, kControlRegs = 64;
+    static constexpr int kSoftmaxRegs = 104, kLiftRegs = 96, kControlRegs = 80;
     static_assert(256 * kSoftmaxRegs + 256 * kLiftRegs + 128 * kControlRegs <=
                       kThreads * kLaunchRegs, "setmaxnreg.inc would wait forever");
     static constexpr int kHalf = kStep / 2;  // positions of a softmax warp
@@ -68,8 +68,8 @@ template <typename C>
 struct TcShared {
     uint64_t code_full[C::kRing], code_empty[C::kRing];
     uint64_t k_full[C::kKBufs], k_empty[C::kKBufs], v_full[C::kVBufs], v_empty[C::kVBufs];
-    uint64_t meta_full[C::kMeta], v_seen[C::kMeta], s_full[2], p_full[2];
-    uint64_t o_done, o_free, q_free, all_done;
+    uint64_t v_seen[C::kMeta], s_full[2], p_full[2], o_done[2];
+    uint64_t o_free, q_free, all_done;
     uint64_t pair[4];                // the two softmax warps of 32 rows
     uint32_t tmem;
     int abort;
@@ -94,6 +94,28 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// Wait for a phase of a barrier, as mbar_wait, in few instructions: what the warps of an SM
+// quarter run has to fit its instruction cache.  Up to 2^15 attempts of kSuspendNs each.
+__device__ __forceinline__ bool phase_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 32768;\n\t"
+        "again: mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra done;\n\tsub.u32 n, n, 1;\n\tsetp.ne.u32 p, n, 0;\n\t@p bra again;\n\t"
+        "done: selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0;
+}
+
 // The wait for TMEM loads, tied to what was loaded.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -105,11 +127,7 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                    "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// 32 or 16 columns of a lane.
-__device__ __forceinline__ void tmem_st_half(uint32_t taddr, const uint32_t (&r)[32]) {
-    tmem_st32(taddr, r);
-}
-__device__ __forceinline__ void tmem_st_half(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -170,7 +188,7 @@ __device__ __forceinline__ bool lift_tile(const uint8_t* entry, uint8_t* tile, c
     const int half = kRowBytes == 64 ? 0 : row0 & 4 ? 64 : 0;  // where slab 0 of a box is
     const int to = row0 * 128 + (((2 * c4) ^ (row0 & 7)) << 4);
     bool bad = false;
-#pragma unroll
+#pragma unroll 1
     for (int slab = 0; slab < C::kSlabs; ++slab) {
         const uint8_t* src = entry + slab / 2 * (kPage * 128) + at + (slab % 2 ? half ^ 64 : half);
         uint8_t* dst = tile + slab * C::kSlabBytes + to;
@@ -238,15 +256,14 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
             mbar_init(&sh.v_empty[i], 1);
         }
         for (int i = 0; i < C::kMeta; ++i) {
-            mbar_init(&sh.meta_full[i], 4);
             mbar_init(&sh.v_seen[i], 4);
             sh.cleared[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_full[i], 2);
+            mbar_init(&sh.o_done[i], 1);
             mbar_init(&sh.p_full[i], 8);
         }
-        mbar_init(&sh.o_done, 1);
         mbar_init(&sh.o_free, 8);
         mbar_init(&sh.q_free, 1);
         mbar_init(&sh.all_done, 1);
@@ -259,7 +276,6 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     grid_dependents_launch();
     grid_dependency_wait();
     find_share<C>(p, &sh.share, sh.warp_sums);
-    volatile int* abort_flag = &sh.abort;
     if (sh.share.begin >= sh.share.end) {
         if (tid == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = 0;
         return;
@@ -276,10 +292,12 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     if (warp >= kCopyWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kControlRegs));
-        if (warp == kCopyWarp) {
-            // ---- copies: the codes of a step's keys, with all its scales, then its values'
+        if (warp == kCopyWarp || warp == kCopyWarp + 2) {
+            // ---- copies: one warp brings the codes of a step's keys, with all its scales, one
+            // those of its values (an entry takes a warp about 1400 cycles to issue)
+            const int kind = warp != kCopyWarp;
             Walk<C> walk(p, sh.share);
-            int n = 0;  // entries so far
+            int n = kind;  // the warp's next entry
             int pieces = 0;
             auto entries = [&](const Cursor<C::kRows>& x, int t) {
                 return t + lane < x.tiles
@@ -303,40 +321,38 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                         page[x] = __shfl_sync(0xffffffffu, ahead, (i + x) % 32);
                         here[x] = i + x < count && page[x] >= 0 && page[x] < p.bt.num_pages;
                         there += here[x];
-                        if (i + x < count && !here[x] && lane == 0)
+                        if (i + x < count && !here[x] && lane == 0 && kind == 0)
                             record_error(p.status, DSA_ERR_DEVICE_CHECK);
                     }
-#pragma unroll
-                    for (int kind = 0; kind < 2; ++kind, ++n) {
-                        const int st = n % C::kRing;
-                        if (lane != 0 || !ok ||
-                            !(ok = mbar_wait(&sh.code_empty[st], (n / C::kRing & 1) ^ 1,
-                                             abort_flag)))
-                            continue;
+                    const int st = n % C::kRing;
+                    if (lane == 0 && ok &&
+                        (ok = phase_wait(&sh.code_empty[st], (n / C::kRing & 1) ^ 1))) {
 #pragma unroll
                         for (int x = 0; x < C::kPages; ++x) sh.valid[st][x] = here[x];
-                        mbar_arrive_expect_tx(
+                        const bool withheld = p.withhold && n == 0;  // by the test only
+                        if (!withheld) mbar_arrive_expect_tx(
                             &sh.code_full[st],
                             there * (C::kPageBytes + (kind == 0 ? 2 * kPage / kBlock * 4 : 0)));
 #pragma unroll
                         for (int x = 0; x < C::kPages; ++x) {
-                            if (!here[x]) continue;
+                            if (!here[x] || withheld) continue;
                             const int z = page[x] * p.kv_heads + u.h;
-                            if (kind == 0)
-                                bulk_copy_g2s(sh.scales[st][x],
-                                              p.scales + (int64_t)z * (2 * kPage / kBlock),
-                                              2 * kPage / kBlock * 4, &sh.code_full[st]);
                             uint8_t* dst = ring + st * C::kEntryBytes + x * C::kPageBytes;
 #pragma unroll
                             for (int b = 0; b < C::kBoxes; ++b)
                                 tma_load_3d(dst + b * (kPage * C::kBoxBytes),
                                             kind == 0 ? &tm_k : &tm_v, b * C::kBoxBytes, 0, z,
                                             &sh.code_full[st]);
+                            if (kind == 0)
+                                bulk_copy_g2s(sh.scales[st][x],
+                                              p.scales + (int64_t)z * (2 * kPage / kBlock),
+                                              2 * kPage / kBlock * 4, &sh.code_full[st]);
                         }
                     }
+                    n += 2;
                     __syncwarp();
                 }
-                if (lane == 0 && tile == 0 && !walk.complete(p)) {
+                if (lane == 0 && kind == 0 && tile == 0 && !walk.complete(p)) {
                     // first piece of a row tile that other CTAs finish
                     int32_t* j = p.joins + blockIdx.x * kJoinInts;
                     pieces =
@@ -350,30 +366,42 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                 walk = v;
                 ahead = ahead_v;
             }
-            if (lane == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
-        } else if (warp == kMmaWarp && lane == 0) {
-            // ---- MMAs
+            if (lane == 0 && kind == 0) p.joins[blockIdx.x * kJoinInts + kJoinPieces] = pieces;
+        } else if (warp == kMmaWarp) {
+            // ---- MMAs: the warp goes along as one, so that what it computes stays in uniform
+            // registers, and one lane issues
             const uint64_t qd = smem_desc(smem_u32(s_q), 16, 1024, kSwizzle128B);
             const uint64_t kd = smem_desc(smem_u32(s_k), 16, 1024, kSwizzle128B);
             const uint64_t vd = smem_desc(smem_u32(s_v), C::kSlabBytes, 1024, kSwizzle128B);
+            const bool leader = elect_one();
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, phase_wait(bar, parity)) != 0;
+            };
             auto issue_s = [&](const Steps<C>& x) {
                 const int b = x.g % C::kKBufs;
                 // the buffer's P has been read: MMAs of other accumulators and shapes are
                 // not kept in order
-                if (x.g >= 2 && !mbar_wait(&sh.o_done, x.g & 1, abort_flag)) return false;
-                if (!mbar_wait(&sh.k_full[b], x.g / C::kKBufs & 1, abort_flag)) return false;
+                if (x.g >= 2 && !wait(&sh.o_done[x.g & 1], (x.g - 2) >> 1 & 1)) return false;
+                if (!wait(&sh.k_full[b], x.g / C::kKBufs & 1)) return false;
                 tc_fence_after();
+                const uint32_t d = tmem + (x.g & 1) * C::kStep;
+                const uint64_t kb = kd + (uint64_t)(b * C::kTileBytes >> 4);
+                const bool last = x.last();
+                if (leader) {
 #pragma unroll
-                for (int s = 0; s < C::kSlabs; ++s)
+                    for (int s = 0; s < C::kSlabs; ++s)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + (x.g & 1) * C::kStep,
-                                qd + (uint64_t)((s * C::kQSlabBytes + k * 32) >> 4),
-                                kd + (uint64_t)((b * C::kTileBytes + s * C::kSlabBytes + k * 32) >> 4),
-                                C::kIdescS, s + k > 0);
-                mma_commit(&sh.s_full[x.g & 1]);
-                mma_commit(&sh.k_empty[b]);
-                if (x.last()) mma_commit(&sh.q_free);
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(d, qd + (uint64_t)((s * C::kQSlabBytes + k * 32) >> 4),
+                                    kb + (uint64_t)((s * C::kSlabBytes + k * 32) >> 4),
+                                    C::kIdescS, s + k > 0);
+                    mma_commit(&sh.s_full[x.g & 1]);
+                    mma_commit(&sh.k_empty[b]);
+                    // and what this warp has seen through k_full: the scales and factors
+                    mbar_arrive(&sh.s_full[x.g & 1]);
+                    if (last) mma_commit(&sh.q_free);
+                }
+                __syncwarp();
                 return true;
             };
             Steps<C> now(p, sh.share), ahead = now;
@@ -387,22 +415,28 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                     ahead.next(p);
                 }
                 const int b = now.g % C::kVBufs;
-                if (now.step == 0 && now.unit > 0)
-                    ok = mbar_wait(&sh.o_free, (now.unit - 1) & 1, abort_flag);
-                ok = ok && mbar_wait(&sh.v_full[b], now.g / C::kVBufs & 1, abort_flag) &&
-                     mbar_wait(&sh.p_full[now.g & 1], now.g >> 1 & 1, abort_flag);
+                if (now.step == 0 && now.unit > 0) ok = wait(&sh.o_free, (now.unit - 1) & 1);
+                ok = ok && wait(&sh.v_full[b], now.g / C::kVBufs & 1) &&
+                     wait(&sh.p_full[now.g & 1], now.g >> 1 & 1);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t pt = tmem + (now.g & 1) * C::kStep;
+                const uint64_t vb = vd + (uint64_t)(b * C::kTileBytes >> 4);
+                const uint32_t more = now.step > 0;
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < C::kStep / 16; ++k)
-                    mma_f16_ta(tmem + C::kColO, tmem + (now.g & 1) * C::kStep + 8 * k,
-                               vd + (uint64_t)((b * C::kTileBytes + k * 2048) >> 4), C::kIdescO,
-                               now.step + k > 0);
-                mma_commit(&sh.v_empty[b]);
-                mma_commit(&sh.o_done);
+                    for (int k = 0; k < C::kStep / 16; ++k)
+                        mma_f16_ta(tmem + C::kColO,
+                                   pt + k * 16 / C::kHalf * C::kHalf + k * 16 % C::kHalf / 2,
+                                   vb + (uint64_t)(k * 2048 >> 4), C::kIdescO, k > 0 ? 1 : more);
+                    mma_commit(&sh.v_empty[b]);
+                    mma_commit(&sh.o_done[now.g & 1]);
+                }
+                __syncwarp();
             }
             // TMEM and shared memory stay until the last MMA is done
-            mma_commit(&sh.all_done);
+            if (leader) mma_commit(&sh.all_done);
+            __syncwarp();
             mbar_drain(&sh.all_done, 0);
         }
     } else if (warp >= kLiftWarp) {
@@ -415,10 +449,10 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int tile_row = u.rt * C::kRows;
             if (!values && x.step == 0) {
                 // Queries, a warp to a row; their scaling as in paged_attention.cuh.
-                if (x.unit > 0 && !(ok = mbar_wait(&sh.q_free, (x.unit - 1) & 1, abort_flag)))
+                if (x.unit > 0 && !(ok = phase_wait(&sh.q_free, (x.unit - 1) & 1)))
                     break;
                 constexpr int kWords = kD / 64;
-#pragma unroll 4
+#pragma unroll 8
                 for (int r = warp - kLiftWarp; r < C::kRows; r += 4) {
                     const int row = tile_row + r, j = token_of(p, row);
                     uint32_t w[kWords];
@@ -480,53 +514,44 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
             uint64_t* const full = values ? &sh.v_full[b] : &sh.k_full[b];
             uint64_t* const empty = values ? &sh.v_empty[b] : &sh.k_empty[b];
             uint8_t* const tile = (values ? s_v : s_k) + b * C::kTileBytes;
-            ok = mbar_wait(empty, (x.g / bufs & 1) ^ 1, abort_flag) &&
-                 mbar_wait(&sh.code_full[st], n / C::kRing & 1, abort_flag);
-            ok = !__any_sync(0xffffffffu, !ok);
+            ok = phase_wait(empty, (x.g / bufs & 1) ^ 1) &&
+                 phase_wait(&sh.code_full[st], n / C::kRing & 1);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t* entry = ring + st * C::kEntryBytes;
             const int first = x.first_position();
             bool there = true;  // all pages
 #pragma unroll
             for (int i = 0; i < C::kPages; ++i) there = there && sh.valid[st][i];
-            if (values) {
-                // rows past the context may hold anything, and p there is 0; E4M3 has NaN,
-                // which not all rows may see: cleared here, given back in the epilogue
-                const int vis_first = u.r.seq - u.r.nb + token_of(p, tile_row) + 1;
-                const int from = max(0, vis_first - first);
-                const bool plain = u.r.seq - first >= C::kStep && there &&
-                                   (C::kInt8 || from >= C::kStep);
-                const bool bad =
-                    plain ? lift_tile<C, false>(entry, tile, nullptr, 0, 0, thread)
-                          : lift_tile<C, true>(entry, tile, sh.valid[st], u.r.seq - first, from,
-                                               thread);
-                if (bad)
-                    *static_cast<volatile int*>(&sh.cleared[x.unit % C::kMeta]) = x.unit + 1;
-            } else {
-                if (there)
-                    lift_tile<C, false>(entry, tile, nullptr, 0, 0, thread);
-                else
-                    lift_tile<C, true>(entry, tile, sh.valid[st], C::kStep, C::kStep, thread);
-                if (thread < C::kBlocks) {
-                    const int page = thread / (kPage / kBlock), i = thread % (kPage / kBlock);
-                    // positions of a page that is not there are left out: 2^-infinity
-                    float4 m = make_float4(1.f, -INFINITY, 1.f, 0.f);
-                    if (sh.valid[st][page]) {
-                        const float* s = sh.scales[st][page];
-                        const float v =
-                            fminf(fmaxf(s[kPage / kBlock + i], kMinBlockScale), kMaxBlockScale);
-                        m = make_float4(fminf(fmaxf(s[i], kMinBlockScale), kMaxBlockScale), lg2(v),
-                                        rcp(v), 0.f);
-                    }
-                    sh.meta[x.g % C::kMeta][thread] = m;
+            // Values past the context may hold anything, and p there is 0; E4M3 has NaN, which
+            // not all rows may see: cleared here, given back in the epilogue.  (Keys there are
+            // masked.)
+            const int rows = values ? u.r.seq - first : C::kStep;
+            const int vis_first = u.r.seq - u.r.nb + token_of(p, tile_row) + 1;
+            const int from = values && !C::kInt8 ? max(0, vis_first - first) : C::kStep;
+            if (there && rows >= C::kStep && from >= C::kStep)
+                lift_tile<C, false>(entry, tile, nullptr, 0, 0, thread);
+            else if (lift_tile<C, true>(entry, tile, sh.valid[st], rows, from, thread))
+                *static_cast<volatile int*>(&sh.cleared[x.unit % C::kMeta]) = x.unit + 1;
+            if (!values && thread < C::kBlocks) {
+                const int page = thread / (kPage / kBlock), i = thread % (kPage / kBlock);
+                // positions of a page that is not there are left out: 2^-infinity
+                float4 m = make_float4(1.f, -INFINITY, 1.f, 0.f);
+                if (sh.valid[st][page]) {
+                    const float* s = sh.scales[st][page];
+                    const float v =
+                        fminf(fmaxf(s[kPage / kBlock + i], kMinBlockScale), kMaxBlockScale);
+                    m = make_float4(fminf(fmaxf(s[i], kMinBlockScale), kMaxBlockScale), lg2(v),
+                                    rcp(v), 0.f);
                 }
+                sh.meta[x.g % C::kMeta][thread] = m;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(full);
                 mbar_arrive(&sh.code_empty[st]);
-                mbar_arrive(values ? &sh.v_seen[x.g % C::kMeta] : &sh.meta_full[x.g % C::kMeta]);
+                if (values) mbar_arrive(&sh.v_seen[x.g % C::kMeta]);
             }
             __syncwarp();
         }
@@ -534,7 +559,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         // Two threads to a row: warps w and w + 4 take a half of a step's positions each,
         // with one reference maximum and sums of their own, and a half of the dims.
-        constexpr int kBlocks = C::kHalf / kBlock;
+        constexpr int kBlocks = C::kHalf / kBlock;  // of a half
         const int half = warp >> 2, r = tid & 127;
         const uint32_t lanes = tmem_addr(tmem, (warp & 3) * 32, 0);
         int g = 0, unit = 0, meetings = 0;
@@ -544,8 +569,8 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.pair[warp & 3]);
-            ok = mbar_wait(&sh.pair[warp & 3], meetings++ & 1, abort_flag);
-            ok = !__any_sync(0xffffffffu, !ok);
+            ok = phase_wait(&sh.pair[warp & 3], meetings++ & 1);
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
         for (Walk<C> walk(p, sh.share); ok && walk.pos < walk.end; walk.next(p)) {
@@ -558,59 +583,47 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
             const bool idle = (warp & 3) * 32 >= rows;  // a warp without a row
             float m = -INFINITY, l = 0.f, f = 0.f;
             for (int step = 0; step < steps; ++step, ++g) {
-                ok = mbar_wait(&sh.meta_full[g % C::kMeta], g / C::kMeta & 1, abort_flag) &&
-                     mbar_wait(&sh.s_full[g & 1], g >> 1 & 1, abort_flag);
-                ok = !__any_sync(0xffffffffu, !ok);
+                ok = phase_wait(&sh.s_full[g & 1], g >> 1 & 1);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 if (!idle) {
                     if (step == 0) f = sh.factor[unit % C::kMeta][r];
-                    const uint32_t s_at = lanes + (g & 1) * C::kStep;
-                    uint32_t s[C::kHalf / 32][32];
-#pragma unroll
-                    for (int i = 0; i < C::kHalf / 32; ++i)
-                        tmem_ld32(s_at + half * C::kHalf + 32 * i, s[i]);
-#pragma unroll
-                    for (int i = 0; i < C::kHalf / 32; ++i) tmem_wait_ld(s[i]);
+                    // Two passes, 32 positions at a time: the loops have to stay small (the
+                    // warps of an SM quarter run four programs, and what they run of them
+                    // has to fit its instruction cache), so S is loaded twice.
+                    const uint32_t s_at = lanes + (g & 1) * C::kStep + half * C::kHalf;
                     const int first = (walk.tile + step * C::kPages) * kPage + half * C::kHalf;
-                    if (first + C::kHalf > vis_first) {
-#pragma unroll
-                        for (int i = 0; i < C::kHalf; ++i)
-                            if (first + i >= vis) s[i / 32][i % 32] = 0xff800000u;
-                    }
                     const float4* meta = sh.meta[g % C::kMeta] + half * kBlocks;
-                    // all blocks side by side: a warp has little but its own instructions to
-                    // wait behind
-                    float most[kBlocks];
+                    float most = -INFINITY;
+#pragma unroll 1
+                    for (int i = 0; i < C::kHalf / 32; ++i) {
+                        uint32_t s[32];
+                        tmem_ld32(s_at + 32 * i, s);
+                        tmem_wait_ld(s);
+                        if (first + 32 * i + 32 > vis_first) {
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) most[b] = -INFINITY;
+                            for (int e = 0; e < 32; ++e)
+                                if (first + 32 * i + e >= vis) s[e] = 0xff800000u;
+                            tmem_st32(s_at + 32 * i, s);
+                            tmem_wait_st();
+                        }
+                        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < kBlock; i += 2)
+                        for (int e = 0; e < kBlock; e += 2)
 #pragma unroll
-                        for (int b = 0; b < kBlocks; ++b)
-                            most[b] = max3(most[b],
-                                           __uint_as_float(s[b / 2][b % 2 * kBlock + i]),
-                                           __uint_as_float(s[b / 2][b % 2 * kBlock + i + 1]));
+                            for (int b = 0; b < 2; ++b)
+                                top[b] = max3(top[b], __uint_as_float(s[b * kBlock + e]),
+                                              __uint_as_float(s[b * kBlock + e + 1]));
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b)
-                        most[b] = __fmaf_ru(most[b], f * meta[b].x, meta[b].y);
-#pragma unroll
-                    for (int w = kBlocks / 2; w > 0; w /= 2)
-#pragma unroll
-                        for (int b = 0; b < w; ++b) most[b] = fmaxf(most[b], most[b + w]);
-                    // the other half's; also: it has taken its S, of which P takes the place
-                    sh.top[g & 1][half][r] = most[0];
+                        for (int b = 0; b < 2; ++b)
+                            most = fmaxf(most, __fmaf_ru(top[b], f * meta[2 * i + b].x,
+                                                         meta[2 * i + b].y));
+                    }
+                    sh.top[g & 1][half][r] = most;
                     meet();
                     if (!ok) break;
-                    const float top = fmaxf(most[0], sh.top[g & 1][half ^ 1][r]);
-                    // O as of the last step, which is done by now or soon: waited for in each
-                    // step, for the barrier says no more than whether one phase has passed
-                    if (step > 0) {
-                        ok = mbar_wait(&sh.o_done, (g - 1) & 1, abort_flag);
-                        ok = !__any_sync(0xffffffffu, !ok);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
+                    const float top = fmaxf(most, sh.top[g & 1][half ^ 1][r]);
                     // the reference moves rarely, and O with it
                     const bool grew = top > m + kTcLag;
                     if (__any_sync(0xffffffffu, grew)) {
@@ -618,6 +631,10 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                         l *= a;
                         if (grew) m = top;
                         if (step > 0) {
+                            ok = phase_wait(&sh.o_done[(g - 1) & 1], (g - 1) >> 1 & 1);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll 1
                             for (int d = half * (kD / 2); d < (half + 1) * (kD / 2); d += 32) {
                                 uint32_t o[32];
@@ -631,29 +648,32 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                     const float base = __fsub_ru(base_of(m), kTcPExp);
-                    uint32_t pk[C::kHalf / 2];
-                    float fk[kBlocks], c[kBlocks], iv[kBlocks], sum[kBlocks];
+#pragma unroll 1
+                    for (int i = 0; i < C::kHalf / 32; ++i) {
+                        uint32_t s[32], pk[16];
+                        tmem_ld32(s_at + 32 * i, s);
+                        float fk[2], c[2], sum[2];
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) {
-                        const float4 sc = meta[b];
-                        fk[b] = f * sc.x;
-                        c[b] = -__fsub_ru(base, sc.y);
-                        iv[b] = sc.z;
-                        sum[b] = 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBlock; i += 2)
-#pragma unroll
-                        for (int b = 0; b < kBlocks; ++b) {
-                            const uint32_t* z = &s[b / 2][b % 2 * kBlock + i];
-                            const float x = ex2(fmaf(__uint_as_float(z[0]), fk[b], c[b]));
-                            const float y = ex2(fmaf(__uint_as_float(z[1]), fk[b], c[b]));
-                            sum[b] += x + y;
-                            pk[(b * kBlock + i) / 2] = pack2<false>(x, y);
+                        for (int b = 0; b < 2; ++b) {
+                            fk[b] = f * meta[2 * i + b].x;
+                            c[b] = -__fsub_ru(base, meta[2 * i + b].y);
+                            sum[b] = 0.f;
                         }
+                        tmem_wait_ld(s);
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) l = fmaf(sum[b], iv[b], l);
-                    tmem_st_half(s_at + half * (C::kHalf / 2), pk);
+                        for (int e = 0; e < kBlock; e += 2)
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                const uint32_t* z = s + b * kBlock + e;
+                                const float x = ex2(fmaf(__uint_as_float(z[0]), fk[b], c[b]));
+                                const float y = ex2(fmaf(__uint_as_float(z[1]), fk[b], c[b]));
+                                sum[b] += x + y;
+                                pk[(b * kBlock + e) / 2] = pack2<false>(x, y);
+                            }
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) l = fmaf(sum[b], meta[2 * i + b].z, l);
+                        tmem_st16(s_at + 16 * i, pk);
+                    }
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -667,9 +687,9 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int i = 0; i < kD / 64; ++i) nan[i] = 0;
             if (steps > 0) {
-                ok = mbar_wait(&sh.o_done, (g - 1) & 1, abort_flag) &&
-                     mbar_wait(&sh.v_seen[(g - 1) % C::kMeta], (g - 1) / C::kMeta & 1, abort_flag);
-                ok = !__any_sync(0xffffffffu, !ok);
+                ok = phase_wait(&sh.o_done[(g - 1) & 1], (g - 1) >> 1 & 1) &&
+                     phase_wait(&sh.v_seen[(g - 1) % C::kMeta], (g - 1) / C::kMeta & 1);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 if (!C::kInt8 &&
@@ -787,8 +807,19 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
 }
 
-// Whether requests of so many rows take this kernel.
-inline bool tensor_rows(int64_t max_rows, bool whole) { return !whole && max_rows > 32; }
+// Whether a call takes this kernel.  mma.sync takes a request's rows in tiles of up to 64,
+// each of which lifts for itself; it is the faster up to 32 rows (48 of 64 dims: 886 us and
+// here 1005 for five tokens of eight heads over 16 x 131072 positions of INT8; 128 dims
+// 1494 and 1210, with four tokens 1109 and 1189).  A launch here costs some 35 us more
+// (first steps alone, 128 rows to join), which it makes up for at 2.2 times the rate: the
+// sides meet at 1.3 to 2.5 * 10^10 operations by the host's sizes (16 requests of 4000
+// positions, 64 rows: 91 and 83 us; of 1000: 29 and 48; 1000 new tokens over 1000: 61 and 71).
+inline bool takes_tensor_cores(const BatchArgs& bt, int num_q_heads, int kv_heads, int head_dim,
+                               bool whole) {
+    const int64_t rows = (int64_t)bt.max_q * (num_q_heads / kv_heads);
+    const double work = 4.0 * bt.total_q * num_q_heads * head_dim * (double)bt.max_seq;
+    return !whole && rows > (head_dim == 64 ? 48 : 32) && work >= 2.5e10;
+}
 
 template <typename C, bool kQBf16>
 cudaError_t launch_tc(AttnParams p, const dsa_kv_cache& cache, int* launches,

@@ -649,10 +649,13 @@ dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
  * block's scale.  Codes are lifted to f16 exactly; bf16 queries are scaled by a power of
  * two per row so that f16 holds them.  Scores, maxima and sums are fp32.  What meets the
  * values' codes is probability times the block's scale, rounded to f16: half a step each,
- * 2^-11 of it (of those below 2^-29 of the row's largest such product, 2^-40 of that).
+ * 2^-11 of it (of those below 2^-26 of the row's largest such product, 2^-37 of that).
  * NaN codes of E4M3 reach the tokens that see them, in their own dim.
  * sm_scale is finite and > 0, and sm_scale * log2 e a normal fp32 number
- * (DSA_ERR_INVALID_ARG); it counts as no less than 2^-78 and no more than 2^94. */
+ * (DSA_ERR_INVALID_ARG).  Times log2 e and the row's power of two it counts as no less than
+ * 2^-78 and no more than 2^94.
+ * Large calls of many rows (a few tokens of 8 heads a KV head, prompt chunks) run on the
+ * fifth-generation tensor cores, whose row tile is 128; the workspace follows. */
 size_t dsa_quant_attention_workspace_size(const dsa_batch* batch, const dsa_quant_cache* cache,
                                           int32_t num_q_heads);
 dsa_status dsa_quant_attention(const dsa_batch* batch, const dsa_quant_cache* cache,

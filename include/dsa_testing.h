@@ -40,6 +40,14 @@ dsa_status dsa_test_paged_attention_wait_timeout(const dsa_batch* batch, const d
                                                  void* out, float* lse, void* ws, size_t ws_bytes,
                                                  int32_t* dev_status, dsa_stream_t stream);
 
+/* dsa_quant_attention in the same way: the first page of keys of every CTA is withheld
+ * (waits of up to 2^30 cycles, or of 2^15 attempts of 50 us where the call runs on the
+ * fifth-generation tensor cores). */
+dsa_status dsa_test_quant_attention_wait_timeout(
+    const dsa_batch* batch, const dsa_quant_cache* cache, dsa_float_format format,
+    int32_t num_q_heads, const void* q, int64_t q_stride, float sm_scale, void* out, float* lse,
+    void* ws, size_t ws_bytes, int32_t* dev_status, dsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
