@@ -166,12 +166,18 @@ __device__ __forceinline__ uint32_t max_abs8(uint32_t m, const uint4& u) {
     return max_abs2<T>(max_abs2<T>(max_abs2<T>(max_abs2<T>(m, u.x), u.y), u.z), u.w);
 }
 
-template <typename T, bool kInt8, int kDim>
+// kOne: a CTA to a token, for small calls.  Then the token's keys and values are on their
+// way, too, before it is known where they go.
+template <typename T, bool kInt8, int kDim, bool kOne>
 __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantArgs a) {
     constexpr int kUnits = kDim / 16;     // 16 values of a row to a lane
     constexpr int kRows = 32 / kUnits;    // of a warp at a time
     constexpr int kSteps = kBlock / kRows;
-    constexpr int kLoads = kSteps < 4 ? kSteps : 4;  // steps in flight
+    // Steps in flight.  Of 256 dims two (prompts of 7 requests 80 us, with four and so 200
+    // bytes spilled 86); in a small call, which mostly has one row to a run, one: short code,
+    // which has to be fetched, is the faster.
+    constexpr int kLoads = kOne ? 1 : kDim == 256 ? 2 : kSteps < 4 ? kSteps : 4;
+    constexpr int kUnroll = kOne ? 1 : kSteps / kLoads;
     extern __shared__ float2 s_turn[];    // of each token, turn_at()
     __shared__ int64_t s_slot[kMaxTokens + kBlock];  // from the token before the CTA's on
     __shared__ Run s_run[kMaxTokens];
@@ -187,6 +193,33 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
     grid_dependency_wait();
 
     // the first queries are on their way while slots are looked at and angles formed
+    const int unit = lane % kUnits, row0 = lane / kUnits;  // of a block's rows
+    struct Source {
+        const void* base;
+        int64_t stride;
+        int head, at0, at1;
+        bool turned;
+    };
+    auto source = [&](int which, int head) {
+        Source x;
+        x.base = which ? a.v : a.k;
+        x.stride = which ? a.v_stride : a.k_stride;
+        x.head = head;
+        x.turned = !which && unit < a.pairs / 8;
+        const bool halves = x.turned && !a.interleaved;
+        x.at0 = halves ? unit * 8 : unit * 16;
+        x.at1 = halves ? unit * 8 + a.pairs : unit * 16 + 8;
+        return x;
+    };
+    uint4 own_lo, own_hi;
+    const int own = warp + kWarps * blockIdx.y;  // first item
+    if (kOne && row0 == 0 && own < 2 * a.kv_heads) {
+        const int which = own >= a.kv_heads;
+        const Source x = source(which, own - which * a.kv_heads);
+        const T* p = static_cast<const T*>(x.base) + first * x.stride + x.head * kDim;
+        own_lo = *reinterpret_cast<const uint4*>(p + x.at0);
+        own_hi = *reinterpret_cast<const uint4*>(p + x.at1);
+    }
     const int q_end = a.q_heads > 0 ? count : 0;
     const int begin = tid + kThreads * blockIdx.y, step = kThreads * gridDim.y;
     const int q_unit = tid % kUnits;
@@ -295,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
     }
 
     // Keys and values: a warp to a run's head.
-    const int unit = lane % kUnits, row0 = lane / kUnits;
+    bool loaded = kOne;  // the first row of the first item
     for (Stride2 item(2 * a.kv_heads, warp + kWarps * blockIdx.y, kWarps * gridDim.y);
          item.token < s_runs; item.next()) {
         const int i_run = item.token, rest = item.rest;
@@ -309,19 +342,20 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
             (which ? a.v_pages : a.k_pages) + (page_head * kPage + part * kBlock) * kDim;
         const bool fresh = slot0 % kBlock == 0;
         const float begun = *scale_at;
-        const T* const src = which ? static_cast<const T*>(a.v) : static_cast<const T*>(a.k);
-        const int64_t stride = which ? a.v_stride : a.k_stride;
-        const bool turned = !which && unit < a.pairs / 8;
-        const bool halves = turned && !a.interleaved;
-        const int at0 = halves ? unit * 8 : unit * 16;
-        const int at1 = halves ? unit * 8 + a.pairs : unit * 16 + 8;
+        const Source x = source(which, head);
+        const bool turned = x.turned;
+        const int at0 = x.at0, at1 = x.at1;
         // Two passes over the values.  Up to 128 dims their 16-bit forms stay in registers
         // in between; 256 read them once more, from the caches.
-        const T* const from = src + (first + run.first + row0) * stride + head * kDim;
+        const T* const from = static_cast<const T*>(x.base) +
+                              (first + run.first + row0) * x.stride + head * kDim;
         auto load = [&](int s, uint4& lo, uint4& hi) {
             lo = hi = make_uint4(0, 0, 0, 0);
-            if (run.stored >> (s * kRows + row0) & 1) {
-                const T* p = from + s * kRows * stride;
+            if (kOne && loaded && s == 0 && row0 == 0) {
+                lo = own_lo;
+                hi = own_hi;
+            } else if (run.stored >> (s * kRows + row0) & 1) {
+                const T* p = from + s * kRows * x.stride;
                 lo = *reinterpret_cast<const uint4*>(p + at0);
                 hi = *reinterpret_cast<const uint4*>(p + at1);
             }
@@ -333,13 +367,14 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
                 turn16(x, y, s_turn + (run.first + s * kRows + row0) * a.pairs, a.pairs / 8, unit,
                        a.interleaved);
         };
+        const int steps = kOne ? (run.count + kRows - 1) / kRows : kSteps;
         // the largest magnitude; NaN if there is one
         float most = 0.f;
         uint32_t most2 = 0;  // of a pair of values as they are
         const bool as_is = which || a.pairs == 0;
         uint4 lo[kLoads], hi[kLoads];
-#pragma unroll
-        for (int s0 = 0; s0 < kSteps; s0 += kLoads) {
+#pragma unroll kUnroll
+        for (int s0 = 0; s0 < steps; s0 += kLoads) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) load(s0 + i, lo[i], hi[i]);
 #pragma unroll
@@ -386,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
         const float need = fminf(fmaxf(all, kMinScale), kMaxNeed);
         if (!fresh && !(begun >= kMinScale && begun <= kMaxScale)) {
             if (lane == 0) record_error(a.status, DSA_ERR_DEVICE_CHECK);
+            loaded = false;
             continue;
         }
         const int k = fresh ? 0 : doublings(begun, need);
@@ -418,8 +454,8 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
                 write(s, x, y);
             }
         } else {
-#pragma unroll
-            for (int s0 = 0; s0 < kSteps; s0 += kLoads) {
+#pragma unroll kUnroll
+            for (int s0 = 0; s0 < steps; s0 += kLoads) {
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
                     if (kSteps > kLoads) load(s0 + i, lo[i], hi[i]);
@@ -454,13 +490,19 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
             }
         }
         if (lane == 0 && (fresh || k > 0)) *scale_at = scale;
+        loaded = false;
     }
 }
 
 template <typename T, bool kInt8, int kDim>
 cudaError_t launch_append(QuantArgs a, cudaStream_t stream) {
-    a.tokens = kMaxTokens;
-    while (a.tokens > 1 && a.num_tokens / a.tokens < 608) a.tokens /= 2;
+    // As few tokens to a CTA as one wave of three CTAs an SM holds, up to eight, from 16384
+    // on sixteen: more spare angles, which tokens of a block behind a CTA's last cost twice,
+    // fewer keep the last wave full (32768 tokens: 135 us with eight, 134 with sixteen; 8192:
+    // 41 and 46; 773 tokens of 256 requests: with one 13.1, two 11.6, four 16.6).
+    a.tokens = 1;
+    const int most_tokens = a.num_tokens < 16384 ? 8 : kMaxTokens;
+    while (a.tokens < most_tokens && (a.num_tokens + a.tokens - 1) / a.tokens > 456) a.tokens *= 2;
     const int ctas = (a.num_tokens + a.tokens - 1) / a.tokens;
     // few tokens: several CTAs share the heads of each
     const int most = max((2 * a.kv_heads + kWarps - 1) / kWarps,
@@ -468,7 +510,8 @@ cudaError_t launch_append(QuantArgs a, cudaStream_t stream) {
     int splits = 1;
     while (splits < most && splits < 16 && ctas * splits < 304) splits *= 2;
     const size_t smem = (size_t)(a.tokens + kBlock - 1) * a.pairs * sizeof(float2);  // <= 32 KB
-    return launch_kernel(quant_append_kernel<T, kInt8, kDim>,
+    return launch_kernel(a.tokens == 1 ? quant_append_kernel<T, kInt8, kDim, true>
+                                       : quant_append_kernel<T, kInt8, kDim, false>,
                          dim3((unsigned)ctas, (unsigned)splits), dim3(kThreads), smem, stream,
                          true, 1, a);
 }
