@@ -166,18 +166,19 @@ __device__ __forceinline__ uint32_t max_abs8(uint32_t m, const uint4& u) {
     return max_abs2<T>(max_abs2<T>(max_abs2<T>(max_abs2<T>(m, u.x), u.y), u.z), u.w);
 }
 
-// kOne: a CTA to a token, for small calls.  Then the token's keys and values are on their
-// way, too, before it is known where they go.
-template <typename T, bool kInt8, int kDim, bool kOne>
+// kShort: for small calls, a token or two to a CTA.  With one its keys and values are on
+// their way, too, before it is known where they go.
+template <typename T, bool kInt8, int kDim, bool kShort>
 __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantArgs a) {
     constexpr int kUnits = kDim / 16;     // 16 values of a row to a lane
     constexpr int kRows = 32 / kUnits;    // of a warp at a time
     constexpr int kSteps = kBlock / kRows;
     // Steps in flight.  Of 256 dims two (prompts of 7 requests 80 us, with four and so 200
     // bytes spilled 86); in a small call, which mostly has one row to a run, one: short code,
-    // which has to be fetched, is the faster.
-    constexpr int kLoads = kOne ? 1 : kDim == 256 ? 2 : kSteps < 4 ? kSteps : 4;
-    constexpr int kUnroll = kOne ? 1 : kSteps / kLoads;
+    // which has to be fetched, is the faster (one token: 5.6 -> 3.95 us; 256 requests of up
+    // to five tokens 11.5 -> 10.4, a prompt of 500 alone 8.5 -> 9.5).
+    constexpr int kLoads = kShort ? 1 : kDim == 256 ? 2 : kSteps < 4 ? kSteps : 4;
+    constexpr int kUnroll = kShort ? 1 : kSteps / kLoads;
     extern __shared__ float2 s_turn[];    // of each token, turn_at()
     __shared__ int64_t s_slot[kMaxTokens + kBlock];  // from the token before the CTA's on
     __shared__ Run s_run[kMaxTokens];
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
     };
     uint4 own_lo, own_hi;
     const int own = warp + kWarps * blockIdx.y;  // first item
-    if (kOne && row0 == 0 && own < 2 * a.kv_heads) {
+    if (kShort && a.tokens == 1 && row0 == 0 && own < 2 * a.kv_heads) {
         const int which = own >= a.kv_heads;
         const Source x = source(which, own - which * a.kv_heads);
         const T* p = static_cast<const T*>(x.base) + first * x.stride + x.head * kDim;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
     }
 
     // Keys and values: a warp to a run's head.
-    bool loaded = kOne;  // the first row of the first item
+    bool loaded = kShort && a.tokens == 1;  // the first row of the first item
     for (Stride2 item(2 * a.kv_heads, warp + kWarps * blockIdx.y, kWarps * gridDim.y);
          item.token < s_runs; item.next()) {
         const int i_run = item.token, rest = item.rest;
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
                               (first + run.first + row0) * x.stride + head * kDim;
         auto load = [&](int s, uint4& lo, uint4& hi) {
             lo = hi = make_uint4(0, 0, 0, 0);
-            if (kOne && loaded && s == 0 && row0 == 0) {
+            if (kShort && loaded && s == 0 && row0 == 0) {
                 lo = own_lo;
                 hi = own_hi;
             } else if (run.stored >> (s * kRows + row0) & 1) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
                 turn16(x, y, s_turn + (run.first + s * kRows + row0) * a.pairs, a.pairs / 8, unit,
                        a.interleaved);
         };
-        const int steps = kOne ? (run.count + kRows - 1) / kRows : kSteps;
+        const int steps = kShort ? (run.count + kRows - 1) / kRows : kSteps;
         // the largest magnitude; NaN if there is one
         float most = 0.f;
         uint32_t most2 = 0;  // of a pair of values as they are
@@ -510,7 +511,7 @@ cudaError_t launch_append(QuantArgs a, cudaStream_t stream) {
     int splits = 1;
     while (splits < most && splits < 16 && ctas * splits < 304) splits *= 2;
     const size_t smem = (size_t)(a.tokens + kBlock - 1) * a.pairs * sizeof(float2);  // <= 32 KB
-    return launch_kernel(a.tokens == 1 ? quant_append_kernel<T, kInt8, kDim, true>
+    return launch_kernel(a.tokens <= 2 ? quant_append_kernel<T, kInt8, kDim, true>
                                        : quant_append_kernel<T, kInt8, kDim, false>,
                          dim3((unsigned)ctas, (unsigned)splits), dim3(kThreads), smem, stream,
                          true, 1, a);
@@ -546,23 +547,42 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const ReadArgs a) 
     const int count = (int)min((int64_t)kReadTokens, a.bt.total_q - first);
     grid_dependents_launch();
     grid_dependency_wait();
-    if (tid < count) {
-        const int t = (int)first + tid;
-        const int b = request_of(a.bt, t);
+    if (tid < 32) {
+        // the requests of the CTA's first and last token, by 32 at a time, and between them
+        // each token's own: a binary search of 256 would wait eight times
+        auto request = [&](int t) {
+            int lo = 0, n = a.bt.num_requests;
+            while (n > 1) {
+                const int step = (n + 31) / 32, at = lo + min(tid * step, n - 1);
+                const bool below = __ldg(a.bt.q_offsets + at) <= t;
+                const int part = max(__popc(__ballot_sync(0xffffffffu, below && tid * step < n)), 1);
+                lo += (part - 1) * step;
+                n = min(step, n - (part - 1) * step);
+            }
+            return lo;
+        };
+        const int from = request((int)first), to = request((int)first + count - 1);
+        const int t = (int)first + min(tid, count - 1);
+        int b = from, last = to;
+        while (b < last) {
+            const int mid = (b + last + 1) >> 1;
+            if (__ldg(a.bt.q_offsets + mid) <= t) b = mid;
+            else last = mid - 1;
+        }
         const int q0 = __ldg(a.bt.q_offsets + b), q1 = __ldg(a.bt.q_offsets + b + 1);
         const int seq = __ldg(a.bt.seq_lens + b);
         int64_t slot = -1;
         if (q0 < 0 || t < q0 || t >= q1 || q1 > a.bt.total_q || q1 - q0 > a.bt.max_q || seq < 0 ||
             seq > a.bt.max_seq) {
-            record_error(a.status, DSA_ERR_DEVICE_CHECK);
-        } else {
+            if (tid < count) record_error(a.status, DSA_ERR_DEVICE_CHECK);
+        } else if (tid < count) {
             const int pos = seq - (q1 - t);
             if (pos >= 0) {
                 const int page = page_lookup(a.bt, b, pos / kPage, a.status);
                 if (page >= 0) slot = (int64_t)page * kPage + pos % kPage;
             }
         }
-        s_slot[tid] = slot;
+        if (tid < count) s_slot[tid] = slot;
     }
     __syncthreads();
     // neighbouring lanes: units of a row, then rows of a head, which lie together in a page
