@@ -228,6 +228,16 @@ bool overlap(const Span& a, const Span& b) {
     return a.begin < b.end && b.begin < a.end && a.begin < a.end && b.begin < b.end;
 }
 
+// Whether token rows of 16-bit outputs share bytes with a quantised cache.
+bool rows_in_cache(const void* p, int64_t tokens, int64_t stride, int64_t heads,
+                   const dsa_quant_cache& c) {
+    const Span rows(p, (tokens - 1) * stride + heads * c.head_dim, 2);
+    const int64_t pages = (int64_t)c.num_pages * c.num_kv_heads;
+    return overlap(rows, Span(c.k_pages, pages * kPage * c.head_dim, 1)) ||
+           overlap(rows, Span(c.v_pages, pages * kPage * c.head_dim, 1)) ||
+           overlap(rows, Span(c.scales, pages * (2 * kPage / DSA_QUANT_BLOCK), 4));
+}
+
 constexpr int kMaxHeads = 1 << 14;  // query heads, and KV heads, of one layer
 
 }  // namespace
@@ -632,7 +642,8 @@ dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
         !row_ok(v, v_stride, cache->num_kv_heads, dim))
         return DSA_ERR_INVALID_ARG;
     if (num_q_heads > 0 && (!row_ok(q, q_stride, num_q_heads, dim) ||
-                            !row_ok(q_out, q_out_stride, num_q_heads, dim)))
+                            !row_ok(q_out, q_out_stride, num_q_heads, dim) ||
+                            rows_in_cache(q_out, num_tokens, q_out_stride, num_q_heads, *cache)))
         return DSA_ERR_INVALID_ARG;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(launch_quant_append(num_tokens, *cache, (int)format, *rope, positions,
@@ -655,6 +666,9 @@ dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
         (v_out && !row_ok(v_out, v_stride, heads, dim)))
         return DSA_ERR_INVALID_ARG;
     if (batch->total_q == 0 || (!k_out && !v_out)) return DSA_OK;
+    if (rows_in_cache(k_out, batch->total_q, k_stride, heads, *cache) ||
+        rows_in_cache(v_out, batch->total_q, v_stride, heads, *cache))
+        return DSA_ERR_INVALID_ARG;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(launch_quant_read(to_args(batch), *cache, (int)format, k_out, k_stride,
                                          v_out, v_stride, dev_status, (cudaStream_t)stream));

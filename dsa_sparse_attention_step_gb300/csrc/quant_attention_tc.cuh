@@ -4,14 +4,20 @@
 // CTAs' shares of it and the joining of pieces; a row tile has 128 rows here.
 //
 //   S = Q K^T    M = 128 rows, N = 128 positions (64 for 256 dims); S in TMEM
-//   O += P V     A = P from TMEM (f16, where S was), B = V; O in TMEM
+//   O += P V     A = P from TMEM (f16, in the place of S), B = V; O in TMEM
 //
 // Codes are lifted to f16 once for all 128 rows: where mma.sync has every warp of 16 rows
-// lift for itself, which bounds it (40 rows over INT8 codes: 746 us where HBM takes 313; here 620),
-// eight warps here write the lifted tiles into the swizzled layout that both products read
-// (K as K-major, V as MN-major operand).  A thread of the softmax has half a row of S to
-// itself: no shuffles.  A block's key scale multiplies its 16 columns of S, its value scale goes
-// into the exponent, as in paged_attention.cuh.
+// lift for itself, which bounds it (up to 40 rows of 16 requests over INT8 codes: 746 us
+// where HBM takes 313; here 620), eight warps here write the lifted tiles into the swizzled
+// layout that both products read (K as K-major, V as MN-major operand).  A thread of the
+// softmax has half a row of S to itself: no shuffles.  A block's key scale multiplies its 16
+// columns of S, its value scale goes into the exponent, as in paged_attention.cuh.
+//
+// Measured: 1000 tokens of 32/8 heads of 128 over 16384 E4M3 positions, 371 us, 0.70
+// PFLOP/s (mma.sync: 857 us).  A step of 128 positions takes some 2900 cycles, of which a
+// softmax warp works 2400 and waits 500: maxima, the meeting of a row's halves, exponentials
+// and the store of P follow one another, and the products and lifts (1030 and 1300 cycles)
+// run beside them.
 //
 // Warps: 0-7 softmax and epilogue (two threads to a row), 8-11 lift K (and bring Q), 12-15
 // lift V, 16 and 18 copy (TMA into a ring of code tiles, K and V in turn), 17 issues the MMAs: S
@@ -330,9 +336,8 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                         for (int x = 0; x < C::kPages; ++x) sh.valid[st][x] = here[x];
                         const bool withheld = p.withhold && n == 0;  // by the test only
-                        if (!withheld) mbar_arrive_expect_tx(
-                            &sh.code_full[st],
-                            there * (C::kPageBytes + (kind == 0 ? 2 * kPage / kBlock * 4 : 0)));
+                        const int each = C::kPageBytes + (kind == 0 ? 2 * kPage / kBlock * 4 : 0);
+                        if (!withheld) mbar_arrive_expect_tx(&sh.code_full[st], there * each);
 #pragma unroll
                         for (int x = 0; x < C::kPages; ++x) {
                             if (!here[x] || withheld) continue;

@@ -604,15 +604,18 @@ typedef struct {
  *   code  = round(x * (1 / scale)), saturating at +-L
  * Divisions and products are fp32, code roundings to nearest even.  For E4M3 the
  * doubling of a scale loses nothing but what falls below the smallest codes; for INT8 it
- * costs the older codes up to half a step each time.
+ * costs the older codes up to half a step each time.  A scale does not shrink until the
+ * block's first row is written again (rejected tokens that others overwrite leave theirs).
  *   positions, q, k, v, q_out, num_q_heads, strides: as dsa_rope_append; num_axes 0
  *       means no turning
  *   slots [T] int64, as dsa_build_tables writes them: page * 64 + row.  Negative: the
  *       token's key and value are not stored.  Tokens of one block stand next to each
  *       other in the call, their slots ascending, and each block comes up in one place
  *       only.
- * q_out may be q itself with the same stride, else it must not overlap the inputs.
- * The call may be repeated on the same inputs: it writes the same scales and codes.
+ * q_out may be q itself with the same stride, else it must not overlap the inputs.  It
+ * lies outside the cache (DSA_ERR_INVALID_ARG).
+ * With q_out apart from q the call may be repeated on the same inputs: it writes the same
+ * scales and codes.
  * Recorded as DSA_ERR_DEVICE_CHECK in *dev_status:
  *   - a slot at or beyond num_pages * 64 (not stored);
  *   - a slot that does not exceed its predecessor's in the same block (not stored);
@@ -634,8 +637,8 @@ dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
  *   k_out[t,h,:] = code * scale, in fp32, rounded once to `format`; v_out likewise
  *   k_out, v_out  [T, num_kv_heads, head_dim], tokens *_stride elements apart (a multiple
  *                 of 8, at least a token's elements), 16-byte aligned; either may be NULL.
- *                 They overlap neither each other, unless as slices of one row, nor the
- *                 cache.
+ *                 They do not overlap each other, unless as slices of one row, and lie
+ *                 outside the cache (DSA_ERR_INVALID_ARG).
  * A token before position 0 (seq_lens[b] < n_b, a padding request), one whose page lies
  * outside [0, num_pages) and one of a request whose arrays contradict the host sizes keep
  * the rows that they had; the last two are recorded as DSA_ERR_DEVICE_CHECK.

@@ -108,6 +108,21 @@ def test_attention_refusals(lib, kw, code):
     assert _attention(lib, **kw) == code
 
 
+@pytest.mark.parametrize("at,inside", [
+    ((1 << 20), True), ((1 << 20) + 8 * 2 * 64 * 128 - 16, True), ((1 << 20) + 8 * 2 * 64 * 128, False),
+    ((1 << 20) - 512, False), ((1 << 20) - 496, True), ((2 << 20) + 64, True),
+    ((3 << 20) + 8 * 2 * 8 * 4 - 16, True), ((3 << 20) + 8 * 2 * 8 * 4, False)])
+def test_outputs_inside_the_cache_are_refused(lib, at, inside):
+    """(Those outside are let through these checks, and refused for a batch of another pool
+    or for a missing key pointer.)"""
+    p = ctypes.c_void_p(at)
+    if inside:
+        assert _read(lib, k=p) == INVALID and _read(lib, v=p) == INVALID
+        assert _append(lib, tokens=1, hq=2, out=p, os=256) == INVALID
+    else:
+        assert _read(lib, k=p, batch=dict(total_q=0)) == 0
+
+
 def test_calls_without_tokens_are_no_ops(lib):
     assert _append(lib, tokens=0) == 0
     assert _read(lib, batch=dict(total_q=0), k=None) == 0
