@@ -84,6 +84,8 @@ cudaError_t launch_paged_attention(const BatchArgs& bt, const dsa_kv_cache& cach
 
 Launch launch_quant_attention_64_e4m3, launch_quant_attention_128_e4m3,
     launch_quant_attention_256_e4m3;
+Launch launch_quant_attention_64_e4m3_many, launch_quant_attention_128_e4m3_many,
+    launch_quant_attention_256_e4m3_many;
 Launch launch_quant_attention_64_int8, launch_quant_attention_128_int8,
     launch_quant_attention_256_int8;
 
@@ -130,13 +132,23 @@ cudaError_t launch_quant_attention(const BatchArgs& bt, const dsa_quant_cache& c
                                                        : launch_quant_attention_tc_256;
         return launch(p, bytes, format, int8, launches, stream);
     }
+    const bool many = bt.max_q > 1 || whole;
     Launch* launch;
     switch (cache.head_dim) {
-        case 64: launch = int8 ? launch_quant_attention_64_int8 : launch_quant_attention_64_e4m3; break;
-        case 128:
-            launch = int8 ? launch_quant_attention_128_int8 : launch_quant_attention_128_e4m3;
+        case 64:
+            launch = int8   ? launch_quant_attention_64_int8
+                     : many ? launch_quant_attention_64_e4m3_many
+                            : launch_quant_attention_64_e4m3;
             break;
-        default: launch = int8 ? launch_quant_attention_256_int8 : launch_quant_attention_256_e4m3;
+        case 128:
+            launch = int8   ? launch_quant_attention_128_int8
+                     : many ? launch_quant_attention_128_e4m3_many
+                            : launch_quant_attention_128_e4m3;
+            break;
+        default:
+            launch = int8   ? launch_quant_attention_256_int8
+                     : many ? launch_quant_attention_256_e4m3_many
+                            : launch_quant_attention_256_e4m3;
     }
     return launch(p, bytes, format, launches, stream);
 }

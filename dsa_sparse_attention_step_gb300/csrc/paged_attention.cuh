@@ -1512,11 +1512,11 @@ cudaError_t launch_dim(const AttnParams& p, const dsa_kv_cache& cache, int forma
 }
 
 // Caches of 8-bit codes with a scale for every 16 tokens.  INT8 has no NaN, so that kMany
-// changes nothing.
-template <int kD, int kCode>
+// changes nothing and is false; E4M3 gains by it as above (64 requests of up to 500: 16.6 ->
+// 16.0 us, 200 of up to 300 19.6 -> 18.5).
+template <int kD, int kCode, bool kMany>
 cudaError_t launch_codes(const AttnParams& p, const dsa_kv_cache& cache, int format, int* launches,
                          cudaStream_t stream) {
-    constexpr bool kMany = kCode == kCodeE4m3;
     return format == DSA_FLOAT_BF16
                ? launch_rows<kD, true, true, kMany, kCode>(p, cache, launches, stream)
                : launch_rows<kD, true, false, kMany, kCode>(p, cache, launches, stream);

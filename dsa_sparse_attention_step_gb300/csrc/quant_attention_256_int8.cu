@@ -6,7 +6,7 @@ namespace dsa {
 
 cudaError_t launch_quant_attention_256_int8(const paged::AttnParams& p, const dsa_kv_cache& cache,
                                         int format, int* launches, cudaStream_t stream) {
-    return paged::launch_codes<256, paged::kCodeInt8>(p, cache, format, launches, stream);
+    return paged::launch_codes<256, paged::kCodeInt8, false>(p, cache, format, launches, stream);
 }
 
 }  // namespace dsa
