@@ -8,19 +8,19 @@
 //
 // Codes are lifted to f16 once for all 128 rows: where mma.sync has every warp of 16 rows
 // lift for itself, which bounds it (up to 40 rows of 16 requests over INT8 codes: 746 us
-// where HBM takes 313; here 620), eight warps here write the lifted tiles into the swizzled
+// where HBM takes 313; here 591), eight warps here write the lifted tiles into the swizzled
 // layout that both products read (K as K-major, V as MN-major operand).  A thread of the
 // softmax has half a row of S to itself: no shuffles.  A block's key scale multiplies its 16
 // columns of S, its value scale goes into the exponent, as in paged_attention.cuh.
 //
-// Measured: 1000 tokens of 32/8 heads of 128 over 16384 E4M3 positions, 371 us, 0.70
+// Measured: 1000 tokens of 32/8 heads of 128 over 16384 E4M3 positions, 356 us, 0.73
 // PFLOP/s (mma.sync: 857 us).  A step of 128 positions takes some 2900 cycles, of which a
 // softmax warp works 2400 and waits 500: maxima, the meeting of a row's halves, exponentials
 // and the store of P follow one another, and the products and lifts (1030 and 1300 cycles)
 // run beside them.
 //
-// Warps: 0-7 softmax and epilogue (two threads to a row), 8-11 lift K (and bring Q), 12-15
-// lift V, 16 and 18 copy (TMA into a ring of code tiles, K and V in turn), 17 issues the MMAs: S
+// Warps: 0-7 softmax and epilogue (two threads to a row), 8-11 lift K, 12-15 lift V (and
+// all eight bring Q), 16 and 18 copy (TMA into a ring of code tiles, K and V in turn), 17 issues the MMAs: S
 // of the next step before O of this one, so that the tensor cores run while the softmax
 // does.
 #pragma once
@@ -29,6 +29,10 @@
 
 namespace dsa {
 namespace paged {
+
+// What a unit costs besides its pages (its queries, its first step alone, its epilogue), in
+// pages of about 1450 cycles (counted as 7: 1000 tokens over 2000 positions 92 us, so 81).
+constexpr int kTcUnitCost = 20;
 
 template <int kD, int kCode_>
 struct TcCfg {
@@ -55,8 +59,7 @@ struct TcCfg {
                                  kRing * kEntryBytes;
     static constexpr uint32_t kColO = 2 * kStep, kCols = 512;
     static_assert(kColO + kD <= kCols, "");
-    // a unit's queries, its first step alone and its epilogue: about 6000 cycles, in pages
-    static constexpr int kUnitCost = kD == 64 ? 8 : 7;
+    static constexpr int kUnitCost = kTcUnitCost;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static constexpr int kSoftmaxRegs = 104, kLiftRegs = 96, kControlRegs = 80;
     static_assert(256 * kSoftmaxRegs + 256 * kLiftRegs + 128 * kControlRegs <=
@@ -75,7 +78,7 @@ struct TcShared {
     uint64_t code_full[C::kRing], code_empty[C::kRing];
     uint64_t k_full[C::kKBufs], k_empty[C::kKBufs], v_full[C::kVBufs], v_empty[C::kVBufs];
     uint64_t v_seen[C::kMeta], s_full[2], p_full[2], o_done[2];
-    uint64_t o_free, q_free, all_done;
+    uint64_t o_free, q_free, q_full, all_done;
     uint64_t pair[4];                // the two softmax warps of 32 rows
     uint32_t tmem;
     int abort;
@@ -272,6 +275,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         mbar_init(&sh.o_free, 8);
         mbar_init(&sh.q_free, 1);
+        mbar_init(&sh.q_full, 8);
         mbar_init(&sh.all_done, 1);
         for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
         fence_mbar_init();
@@ -387,6 +391,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // the buffer's P has been read: MMAs of other accumulators and shapes are
                 // not kept in order
                 if (x.g >= 2 && !wait(&sh.o_done[x.g & 1], (x.g - 2) >> 1 & 1)) return false;
+                if (x.step == 0 && !wait(&sh.q_full, x.unit & 1)) return false;
                 if (!wait(&sh.k_full[b], x.g / C::kKBufs & 1)) return false;
                 tc_fence_after();
                 const uint32_t d = tmem + (x.g & 1) * C::kStep;
@@ -402,7 +407,7 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                     C::kIdescS, s + k > 0);
                     mma_commit(&sh.s_full[x.g & 1]);
                     mma_commit(&sh.k_empty[b]);
-                    // and what this warp has seen through k_full: the scales and factors
+                    // and what this warp has seen: the scales and factors
                     mbar_arrive(&sh.s_full[x.g & 1]);
                     if (last) mma_commit(&sh.q_free);
                 }
@@ -452,13 +457,17 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (; ok && x.more(); x.next(p)) {
             const Cursor<C::kRows>& u = x.w.u;
             const int tile_row = u.rt * C::kRows;
-            if (!values && x.step == 0) {
-                // Queries, a warp to a row; their scaling as in paged_attention.cuh.
-                if (x.unit > 0 && !(ok = phase_wait(&sh.q_free, (x.unit - 1) & 1)))
-                    break;
+            if (x.step == 0) {
+                // Queries, a warp of either group to a row; their scaling as in
+                // paged_attention.cuh.
+                if (x.unit > 0) {
+                    ok = phase_wait(&sh.q_free, (x.unit - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
                 constexpr int kWords = kD / 64;
 #pragma unroll 8
-                for (int r = warp - kLiftWarp; r < C::kRows; r += 4) {
+                for (int r = warp - kLiftWarp; r < C::kRows; r += 8) {
                     const int row = tile_row + r, j = token_of(p, row);
                     uint32_t w[kWords];
 #pragma unroll
@@ -513,6 +522,9 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                             make_uint4(w[0], w[kWords > 1 ? 1 : 0], w[kWords > 2 ? 2 : 0],
                                        w[kWords > 2 ? 3 : 0]);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full);
             }
             const int n = 2 * x.g + values, st = n % C::kRing;
             const int bufs = values ? C::kVBufs : C::kKBufs, b = x.g % bufs;
@@ -814,16 +826,19 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 
 // Whether a call takes this kernel.  mma.sync takes a request's rows in tiles of up to 64,
 // each of which lifts for itself; it is the faster up to 32 rows (48 of 64 dims: 886 us and
-// here 1005 for five tokens of eight heads over 16 x 131072 positions of INT8; 128 dims
-// 1494 and 1210, with four tokens 1109 and 1189).  A launch here costs some 35 us more
-// (first steps alone, 128 rows to join), which it makes up for at 2.2 times the rate: the
-// sides meet at 1.3 to 2.5 * 10^10 operations by the host's sizes (16 requests of 4000
-// positions, 64 rows: 91 and 83 us; of 1000: 29 and 48; 1000 new tokens over 1000: 61 and 71).
+// here 1022 for five tokens of eight heads over 16 x 131072 positions of INT8; 128 dims
+// 1493 and 1192, with four tokens 1109 and 1147).  A launch here costs some 25 us more
+// (first steps alone, 128 rows to join), which it makes up for at 2.4 times the rate: the
+// sides meet at 8 * 10^9 operations by the host's sizes (16 requests of 2000 positions, 64
+// rows: 48 and 47 us; of 1000: 29 and 37; 500 new tokens over 1000: 41 and 44, 1000: 62 and 60).
 inline bool takes_tensor_cores(const BatchArgs& bt, int num_q_heads, int kv_heads, int head_dim,
                                bool whole) {
     const int64_t rows = (int64_t)bt.max_q * (num_q_heads / kv_heads);
     const double work = 4.0 * bt.total_q * num_q_heads * head_dim * (double)bt.max_seq;
-    return !whole && rows > (head_dim == 64 ? 48 : 32) && work >= 2.5e10;
+    // positions in the list are 32-bit
+    const double list = most_units(bt, kv_heads, num_q_heads / kv_heads, 128) *
+                        ((double)bt.max_seq / kPage + 2 + kTcUnitCost);
+    return !whole && rows > (head_dim == 64 ? 48 : 32) && work >= 9e9 && list < 2147483648.0;
 }
 
 template <typename C, bool kQBf16>

@@ -32,7 +32,7 @@ class Case:
     """A batch over shuffled pages.  What no token may see is wild: pages that no request
     holds, rows past a context's end (NaN codes of E4M3, -128 of INT8) and the scales of
     blocks without a live row (NaN, infinite, 0).  far: a last request of one token, so long
-    that the call is work enough for the tensor core kernel (2.5 * 10^10 operations; it takes
+    that the call is work enough for the tensor core kernel (9 * 10^9 operations; it takes
     requests of more than 32 rows, 48 of 64 dims, to a KV head)."""
 
     def __init__(self, lens, new, hq, hkv, d, dtype=BF16, code=E4M3, seed=0, q_scale=2.0,
