@@ -261,7 +261,33 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
         if (lane < count && !ascends) record_error(a.status, DSA_ERR_DEVICE_CHECK);
         const uint32_t all_joined = __ballot_sync(0xffffffffu, joined);
         const uint32_t all_ascend = __ballot_sync(0xffffffffu, ascends);
-        const bool leads = lane < count && own >= 0 && !joined;
+        bool leads = lane < count && own >= 0 && !joined;
+        // Behind tokens that are not stored the block of the last one that is may come up
+        // again: whoever writes that block may be at it now, so these tokens are left out.
+        const bool behind_gap = leads && before < 0 && first + lane > 0;
+        if (__any_sync(0xffffffffu, behind_gap)) {
+            const uint32_t kept = __ballot_sync(0xffffffffu, lane <= reach && slot >= 0);
+            int64_t earlier = -1;  // the last kept slot before the window
+            if (__any_sync(0xffffffffu, behind_gap && (kept & ((2u << lane) - 1u)) == 0)) {
+                for (int64_t at = first - 2; at >= 0; at -= 32) {
+                    int64_t s = at >= lane ? __ldg(a.slots + at - lane) : -1;
+                    if (s >= a.slot_end) s = -1;
+                    const uint32_t there = __ballot_sync(0xffffffffu, s >= 0);
+                    if (there != 0) {
+                        earlier = __shfl_sync(0xffffffffu, s, __ffs(there) - 1);
+                        break;
+                    }
+                }
+            }
+            if (behind_gap) {
+                const uint32_t m = kept & ((2u << lane) - 1u);  // s_slot[0 .. lane]
+                const int64_t last = m != 0 ? s_slot[31 - __clz(m)] : earlier;
+                if (last >= 0 && last / kBlock == own / kBlock) {
+                    record_error(a.status, DSA_ERR_DEVICE_CHECK);
+                    leads = false;
+                }
+            }
+        }
         const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
         int end = 0;
         if (leads) {

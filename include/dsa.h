@@ -619,6 +619,8 @@ typedef struct {
  * Recorded as DSA_ERR_DEVICE_CHECK in *dev_status:
  *   - a slot at or beyond num_pages * 64 (not stored);
  *   - a slot that does not exceed its predecessor's in the same block (not stored);
+ *   - a block that comes up again behind tokens that are not stored (its tokens there are
+ *     not stored either);
  *   - a block begun earlier whose scale lies outside [2^-48, 2^33] (its tokens are not
  *     stored);
  *   - infinite and NaN values.  need is that of the finite ones; infinite ones saturate,

@@ -449,3 +449,47 @@ def test_python_checks():
         with pytest.raises((TypeError, ValueError)):
             dsa.dsa_quant_read(batch, cache, k, v)
     assert encode(torch.tensor([0.5]), INT8).item() == 0  # the oracle's ties go to even
+
+
+def pieces(c, *parts):
+    """(slots, k, v): tokens of c, None for one that is not stored, in the order given."""
+    at = [t for part in parts for t in part]
+    pick = torch.tensor([0 if t is None else t for t in at], device=DEV)
+    gone = torch.tensor([t is None for t in at], device=DEV)
+    return torch.where(gone, -1, c.slots[pick]), c.k[pick], c.v[pick]
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("gap", [1, 3, 14, 15, 16, 31, 40, 200, 1000])
+@pytest.mark.parametrize("cached,more,beyond", [(0, 0, False), (0, 0, True), (5, 0, False), (0, 700, False)])
+def test_a_block_again_behind_tokens_that_are_not_stored_is_left_and_recorded(cached, gap, code,
+                                                                               more, beyond):
+    """Four tokens of a block, tokens that are not stored, four more of the block and the
+    first three of the next: the second four are left out, and nothing else is."""
+    c = Append([cached, 0], [11 + 16 - 8 - cached, more], 2, 3, 64, BF16, code, seed=20)
+    first, later = list(range(0, 4)), list(range(4, 8))
+    fresh = [t for t in range(len(c.slots) - more) if (cached + t) // BLOCK == 1][:3]
+    tail = list(range(len(c.slots) - more, len(c.slots)))
+    slots, k, v = pieces(c, first, [None] * gap, later, fresh, tail)
+    if beyond:
+        slots[4:4 + gap] = c.pages * PAGE + 3
+    keep = slots.clone()
+    keep[4 + gap:8 + gap] = -1
+    keep[4:4 + gap] = -1
+    want_k, scales, _ = append_reference(c.k_pages, c.scales, 0, keep, k.float())
+    want_v, scales, _ = append_reference(c.v_pages, scales, 1, keep, v.float())
+    q = torch.zeros(len(slots), 2, 64, dtype=BF16, device=DEV)
+    c.run(status=DEVICE_CHECK, slots=slots, q=q, k=k, v=v, q_out=torch.empty_like(q))
+    c.check((want_k, want_v, scales))
+
+
+def test_other_blocks_behind_tokens_that_are_not_stored_are_written():
+    """A gap before another block, before the first token and after the last one."""
+    c = Append([0, 3], [40, 60], 2, 2, 128, F16, INT8, seed=21)
+    slots, k, v = pieces(c, [None] * 5, list(range(0, 16)), [None] * 45, list(range(16, 40)),
+                         [None], list(range(40, 100)), [None] * 7)
+    want_k, scales, _ = append_reference(c.k_pages, c.scales, 0, slots, k.float())
+    want_v, scales, _ = append_reference(c.v_pages, scales, 1, slots, v.float())
+    q = torch.zeros(len(slots), 2, 128, dtype=F16, device=DEV)
+    c.run(slots=slots, q=q, k=k, v=v, q_out=torch.empty_like(q))
+    c.check((want_k, want_v, scales))
