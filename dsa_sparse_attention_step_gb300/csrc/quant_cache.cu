@@ -295,7 +295,16 @@ __global__ void __launch_bounds__(kThreads, 3) quant_append_kernel(const QuantAr
             r.first = lane;
             // tokens behind this one that are joined to their predecessor
             r.count = min(__ffs(~(all_joined >> (lane + 1))), kBlock);
-            r.stored = (all_ascend >> lane) & ((1u << r.count) - 1u);
+            const uint32_t all = (1u << r.count) - 1u;
+            r.stored = (all_ascend >> lane) & all;
+            if (r.stored != all) {  // those that exceed every one before, so that no row comes twice
+                int64_t most = own;
+                for (int i = 1; i < r.count; ++i) {
+                    const int64_t s = s_slot[lane + 1 + i];
+                    if (s > most) most = s;
+                    else r.stored &= ~(1u << i);
+                }
+            }
             end = lane + r.count;
             s_run[__popc(leaders & ((1u << lane) - 1u))] = r;
         }

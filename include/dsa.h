@@ -618,7 +618,8 @@ typedef struct {
  * scales and codes.
  * Recorded as DSA_ERR_DEVICE_CHECK in *dev_status:
  *   - a slot at or beyond num_pages * 64 (not stored);
- *   - a slot that does not exceed its predecessor's in the same block (not stored);
+ *   - a slot that does not exceed those before it of the same block (not stored; nor are
+ *     tokens of a block behind its sixteenth, among which there always is such a slot);
  *   - a block that comes up again behind tokens that are not stored (its tokens there are
  *     not stored either);
  *   - a block begun earlier whose scale lies outside [2^-48, 2^33] (its tokens are not

@@ -493,3 +493,30 @@ def test_other_blocks_behind_tokens_that_are_not_stored_are_written():
     q = torch.zeros(len(slots), 2, 128, dtype=F16, device=DEV)
     c.run(slots=slots, q=q, k=k, v=v, q_out=torch.empty_like(q))
     c.check((want_k, want_v, scales))
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("before", [0, 1, 7, 500])
+@pytest.mark.parametrize("rows,kept", [
+    ([0, 5, 3, 5, 6], [1, 1, 0, 0, 1]), ([2, 9, 1, 2, 3, 9, 10, 4], [1, 1, 0, 0, 0, 0, 1, 0]),
+    ([0, 15, 1, 2, 3, 14, 15], [1, 1, 0, 0, 0, 0, 0]),
+    (list(range(16)) + [0, 1, 2], [1] * 16 + [0] * 3),
+    ([0] * 15 + [1, 2, 3], [1] + [0] * 14 + [1, 0, 0])])
+def test_slots_of_a_block_that_do_not_exceed_those_before_are_left_out(rows, kept, before, code):
+    """No row is written twice: a token counts where its slot exceeds every earlier one of the
+    block, and is among the block's first sixteen tokens."""
+    n = len(rows)
+    c = Append([0, 0], [32, max(before, 1)], 2, 2, 128, F16, code, seed=23)
+    start = int(c.slots[0]) // PAGE * PAGE
+    slots = torch.cat([c.slots[32:32 + before],
+                       torch.tensor([start + r for r in rows], device=DEV), c.slots[16:20]])
+    k, v = (x[torch.arange(len(slots), device=DEV) % len(c.slots)] for x in (c.k, c.v))
+    k[before + 2:before + n] *= 3  # a token that is left out does not count for the scale
+    keep = slots.clone()
+    keep[before:before + n] = torch.where(torch.tensor(kept, device=DEV) > 0,
+                                          slots[before:before + n], -1)
+    want_k, scales, _ = append_reference(c.k_pages, c.scales, 0, keep, k.float())
+    want_v, scales, _ = append_reference(c.v_pages, scales, 1, keep, v.float())
+    q = torch.zeros(len(slots), 2, 128, dtype=F16, device=DEV)
+    c.run(status=DEVICE_CHECK, slots=slots, q=q, k=k, v=v, q_out=torch.empty_like(q))
+    c.check((want_k, want_v, scales))
