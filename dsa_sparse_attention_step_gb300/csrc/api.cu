@@ -1,5 +1,6 @@
 // api.cu -- the extern "C" boundary of libdsa.so: argument validation,
 // workspace arithmetic and kernel launches.  See include/dsa.h.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -228,14 +229,52 @@ bool overlap(const Span& a, const Span& b) {
     return a.begin < b.end && b.begin < a.end && a.begin < a.end && b.begin < b.end;
 }
 
-// Whether token rows of 16-bit outputs share bytes with a quantised cache.
-bool rows_in_cache(const void* p, int64_t tokens, int64_t stride, int64_t heads,
-                   const dsa_quant_cache& c) {
-    const Span rows(p, (tokens - 1) * stride + heads * c.head_dim, 2);
+// `count` rows of `length` elements, `stride` elements apart, in bytes; whether two such sets
+// share any (slices of one projection lie between one another's rows and do not).
+struct Rows {
+    int64_t begin, count, stride, length;
+    Rows(const void* p, int64_t count_, int64_t stride_, int64_t length_, int size)
+        : begin((int64_t)reinterpret_cast<uintptr_t>(p)), count(p ? count_ : 0),
+          // (beyond any address space it is all the same)
+          stride(size * (count > 1 ? std::min(stride_, (INT64_MAX >> 3) / count / size) : length_)),
+          length(size * length_) {}
+    Rows(const void* p, int64_t length_, int size) : Rows(p, 1, length_, length_, size) {}
+    bool empty() const { return count <= 0 || length <= 0; }
+    int64_t end() const { return begin + (count - 1) * stride + length; }
+};
+bool overlap(const Rows& a, const Rows& b) {
+    if (a.empty() || b.empty() || a.begin >= b.end() || b.begin >= a.end()) return false;
+    if (a.count > 1 && b.count > 1 && a.stride != b.stride) {  // row by row
+        for (int64_t i = 0, j = 0; i < a.count && j < b.count;) {
+            const int64_t x = a.begin + i * a.stride, y = b.begin + j * b.stride;
+            if (x + a.length <= y) ++i;
+            else if (y + b.length <= x) ++j;
+            else return true;
+        }
+        return false;
+    }
+    // Row j of b begins d + (j - i) s behind row i of a; they share bytes from -b.length + 1 to
+    // a.length - 1.  The least j - i that there is from the former on decides.
+    const int64_t s = a.count > 1 ? a.stride : b.stride, d = b.begin - a.begin;
+    const int64_t least = 1 - b.length - d;
+    int64_t k = least > 0 ? (least + s - 1) / s : -(-least / s);
+    if (k < 1 - a.count) k = 1 - a.count;
+    return k < b.count && d + k * s < a.length;
+}
+
+// Whether an output shares bytes with a quantised cache.
+bool in_cache(const Rows& rows, const dsa_quant_cache& c) {
     const int64_t pages = (int64_t)c.num_pages * c.num_kv_heads;
-    return overlap(rows, Span(c.k_pages, pages * kPage * c.head_dim, 1)) ||
-           overlap(rows, Span(c.v_pages, pages * kPage * c.head_dim, 1)) ||
-           overlap(rows, Span(c.scales, pages * (2 * kPage / DSA_QUANT_BLOCK), 4));
+    return overlap(rows, Rows(c.k_pages, pages * kPage * c.head_dim, 1)) ||
+           overlap(rows, Rows(c.v_pages, pages * kPage * c.head_dim, 1)) ||
+           overlap(rows, Rows(c.scales, pages * (2 * kPage / DSA_QUANT_BLOCK), 4));
+}
+
+// Whether an output shares bytes with the arrays of a batch.
+bool in_batch(const Rows& rows, const dsa_batch& b) {
+    return overlap(rows, Rows(b.q_offsets, (int64_t)b.num_requests + 1, 4)) ||
+           overlap(rows, Rows(b.seq_lens, b.num_requests, 4)) ||
+           overlap(rows, Rows(b.block_table, (int64_t)b.num_requests * b.max_pages, 4));
 }
 
 constexpr int kMaxHeads = 1 << 14;  // query heads, and KV heads, of one layer
@@ -643,7 +682,9 @@ dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
         return DSA_ERR_INVALID_ARG;
     if (num_q_heads > 0 && (!row_ok(q, q_stride, num_q_heads, dim) ||
                             !row_ok(q_out, q_out_stride, num_q_heads, dim) ||
-                            rows_in_cache(q_out, num_tokens, q_out_stride, num_q_heads, *cache)))
+                            in_cache(Rows(q_out, num_tokens, q_out_stride,
+                                          (int64_t)num_q_heads * dim, 2),
+                                     *cache)))
         return DSA_ERR_INVALID_ARG;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(launch_quant_append(num_tokens, *cache, (int)format, *rope, positions,
@@ -666,8 +707,9 @@ dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
         (v_out && !row_ok(v_out, v_stride, heads, dim)))
         return DSA_ERR_INVALID_ARG;
     if (batch->total_q == 0 || (!k_out && !v_out)) return DSA_OK;
-    if (rows_in_cache(k_out, batch->total_q, k_stride, heads, *cache) ||
-        rows_in_cache(v_out, batch->total_q, v_stride, heads, *cache))
+    const int64_t row = (int64_t)heads * dim;
+    if (in_cache(Rows(k_out, batch->total_q, k_stride, row, 2), *cache) ||
+        in_cache(Rows(v_out, batch->total_q, v_stride, row, 2), *cache))
         return DSA_ERR_INVALID_ARG;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(launch_quant_read(to_args(batch), *cache, (int)format, k_out, k_stride,
@@ -709,6 +751,20 @@ static dsa_status quant_attention(const dsa_batch* batch, const dsa_quant_cache*
     if (!ws || !aligned16(ws) ||
         ws_bytes < dsa_quant_attention_workspace_size(batch, cache, num_q_heads))
         return DSA_ERR_WORKSPACE;
+    // all three are written while other CTAs read the inputs
+    const int64_t row = (int64_t)num_q_heads * cache->head_dim;
+    const Rows outs[] = {Rows(out, batch->total_q * row, 2),
+                         Rows(lse, (int64_t)batch->total_q * num_q_heads, 4),
+                         Rows(ws, (int64_t)dsa_quant_attention_workspace_size(batch, cache,
+                                                                              num_q_heads),
+                              1)};
+    const Rows queries(q, batch->total_q, q_stride, row, 2);
+    for (int i = 0; i < 3; ++i) {
+        if (in_cache(outs[i], *cache) || in_batch(outs[i], *batch) || overlap(outs[i], queries))
+            return DSA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return DSA_ERR_INVALID_ARG;
+    }
     const bool whole = g_batch_invariant.load(std::memory_order_relaxed) != 0;
     int launches = 0;
     const dsa_status rc = cuda_status(launch_quant_attention(

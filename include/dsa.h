@@ -657,6 +657,8 @@ dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
  * values' codes is probability times the block's scale, rounded to f16: half a step each,
  * 2^-11 of it (of those below 2^-26 of the row's largest such product, 2^-37 of that).
  * NaN codes of E4M3 reach the tokens that see them, in their own dim.
+ * out, lse and the used bytes of ws overlap neither one another nor q, the cache or the
+ * batch's arrays (DSA_ERR_INVALID_ARG).
  * sm_scale is finite and > 0, and sm_scale * log2 e a normal fp32 number
  * (DSA_ERR_INVALID_ARG).  Times log2 e and the row's power of two it counts as no less than
  * 2^-78 and no more than 2^94.

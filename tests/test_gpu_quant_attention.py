@@ -486,3 +486,33 @@ def test_python_checks():
         with pytest.raises(dsa.DsaError):
             dsa.dsa_quant_attention(batch, cache, c.q, bad.get("sm", 0.1), out, None,
                                     bad.get("ws", ws))
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("new,far", [(2, False), (60, True)])
+def test_outputs_beside_the_cache(code, new, far):
+    """One allocation holds workspace, scales, out, keys, lse, values and queries without a
+    gap: nothing is refused and nothing outside the outputs is written."""
+    c = Case([300, 130], [new, 1], 8, 2, 64, BF16, code, seed=51, far=far)
+    want, want_lse = c.run()
+    batch = c.batch()
+    need = dsa.dsa_quant_attention_workspace_size(batch, c.cache(), c.hq)
+    tokens = c.offsets[-1]
+    sizes = [-(-need // 16) * 16, c.scales.numel() * 4, want.numel() * 2, c.k.numel(),
+             want_lse.numel() * 4, c.v.numel(), c.q.numel() * 2]
+    one = torch.full((sum(sizes),), 0x55, dtype=torch.uint8, device=DEV)
+    ws, scales, out, k, lse, v, q = one.split(sizes)
+    scales = scales.view(torch.float32).view(c.scales.shape)
+    k, v = (x.view(code).view(c.k.shape) for x in (k, v))
+    q, out = (x.view(BF16).view(c.q.shape) for x in (q, out))
+    lse = lse.view(torch.float32).view(want_lse.shape)
+    assert out.data_ptr() + tokens * c.hq * 64 * 2 == k.data_ptr()
+    scales.copy_(c.scales)
+    k.view(torch.uint8).copy_(c.k.view(torch.uint8))
+    v.view(torch.uint8).copy_(c.v.view(torch.uint8))
+    q.copy_(c.q)
+    dsa.dsa_quant_attention(batch, dsa.QuantCache(k, v, scales), q, c.sm_scale, out, lse, ws[:need])
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert torch.equal(scales.view(torch.int32), c.scales.view(torch.int32)) and torch.equal(q, c.q)
+    assert torch.equal(k.view(torch.uint8), c.k.view(torch.uint8))
+    assert torch.equal(v.view(torch.uint8), c.v.view(torch.uint8))

@@ -139,3 +139,42 @@ def test_attention_workspace_follows_rows_and_head_dim(lib):
     assert 0 < size(4) <= size(64) <= size(128)
     assert size(4, head_dim=256) > size(4) > size(4, head_dim=64)
     assert size(5) == 0 and size(0) == 0 and size(4, head_dim=96) == 0
+
+
+POOL = 8 * 2 * 64 * 128  # bytes of the keys' and of the values' codes of _cache()
+K, V, S = 1 << 20, 2 << 20, 3 << 20
+
+
+@pytest.mark.parametrize("begin,size", [(K, POOL), (V, POOL), (S, 8 * 2 * 8 * 4)])
+@pytest.mark.parametrize("which", ["out", "lse", "ws"])
+def test_attention_outputs_inside_the_cache_are_refused(lib, which, begin, size):
+    """At its first and last bytes, in the middle and around it; apart from the address the
+    call is one that the library takes."""
+    b, c = _batch(), _cache()
+    need = lib.dsa_quant_attention_workspace_size(ctypes.byref(b), ctypes.byref(c), 4)
+    bytes_ = {"out": 4 * 128 * 2, "lse": 4 * 4, "ws": need}[which]
+    step = 4 if which == "lse" else 16
+    for at in (begin, begin + size - step, begin + size // 2, begin - bytes_ + step):
+        if at <= 0:
+            continue
+        p = dict(out=1 << 40, lse=1 << 41, ws=1 << 42)
+        p[which] = at // step * step
+        assert lib.dsa_quant_attention(ctypes.byref(b), ctypes.byref(c), 0, 4, 1 << 43, 512, 0.1,
+                                       p["out"], p["lse"], p["ws"], need, None, None) == INVALID
+
+
+@pytest.mark.parametrize("a,b", [("out", "q"), ("lse", "q"), ("ws", "q"), ("out", "lse"), ("ws", "out"),
+                                 ("ws", "lse"), ("out", "table"), ("lse", "lens"), ("ws", "offsets")])
+def test_attention_outputs_that_overlap_are_refused(lib, a, b):
+    batch, c = _batch(num_requests=3, total_q=3), _cache()
+    need = lib.dsa_quant_attention_workspace_size(ctypes.byref(batch), ctypes.byref(c), 4)
+    p = {name: (i + 1) << 40 for i, name in enumerate(("out", "lse", "ws", "q", "table", "lens",
+                                                       "offsets"))}
+    last = dict(q=3 * 2 * 512 - 16, lse=32, out=3 * 1024 - 16, table=3 * 64 * 4 - 16, lens=8, offsets=0)
+    size = dict(out=3 * 1024, lse=48, ws=need)
+    for at in (p[b], p[b] + last[b], p[b] - size[a] + 16):
+        x = dict(p)
+        x[a] = at // (4 if a == "lse" else 16) * (4 if a == "lse" else 16)
+        batch.block_table, batch.seq_lens, batch.q_offsets = x["table"], x["lens"], x["offsets"]
+        assert lib.dsa_quant_attention(ctypes.byref(batch), ctypes.byref(c), 0, 4, x["q"], 1024, 0.1,
+                                       x["out"], x["lse"], x["ws"], need, None, None) == INVALID
