@@ -680,12 +680,23 @@ dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
     if (!row_ok(k, k_stride, cache->num_kv_heads, dim) ||
         !row_ok(v, v_stride, cache->num_kv_heads, dim))
         return DSA_ERR_INVALID_ARG;
-    if (num_q_heads > 0 && (!row_ok(q, q_stride, num_q_heads, dim) ||
-                            !row_ok(q_out, q_out_stride, num_q_heads, dim) ||
-                            in_cache(Rows(q_out, num_tokens, q_out_stride,
-                                          (int64_t)num_q_heads * dim, 2),
-                                     *cache)))
-        return DSA_ERR_INVALID_ARG;
+    if (num_q_heads > 0) {
+        if (!row_ok(q, q_stride, num_q_heads, dim) || !row_ok(q_out, q_out_stride, num_q_heads, dim))
+            return DSA_ERR_INVALID_ARG;
+        // a CTA's queries are written while other CTAs read theirs, and all keys and values
+        const int64_t row = (int64_t)num_q_heads * dim, kv_row = (int64_t)cache->num_kv_heads * dim;
+        const Rows out(q_out, num_tokens, q_out_stride, row, 2);
+        const bool in_place = q_out == q && (num_tokens == 1 || q_out_stride == q_stride);
+        if (in_cache(out, *cache) ||
+            (!in_place && overlap(out, Rows(q, num_tokens, q_stride, row, 2))) ||
+            // (in place and not turned, queries stay what they are)
+            ((!in_place || pairs > 0) && (overlap(out, Rows(k, num_tokens, k_stride, kv_row, 2)) ||
+                                          overlap(out, Rows(v, num_tokens, v_stride, kv_row, 2)))) ||
+            overlap(out, Rows(slots, num_tokens, 8)) ||
+            (pairs > 0 && (overlap(out, Rows(positions, (int64_t)rope->num_axes * num_tokens, 4)) ||
+                           overlap(out, Rows(rope->inv_freq, pairs, 8)))))
+            return DSA_ERR_INVALID_ARG;
+    }
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(launch_quant_append(num_tokens, *cache, (int)format, *rope, positions,
                                            slots, num_q_heads, q, q_stride, k, k_stride, v,

@@ -6,6 +6,8 @@ value by e <= 2^-21 of the sum of its two products' sizes; a scale, fp32 quotien
 largest, by 2^-21 of the block's largest such sum over L (and a rounding, 2^-24); a decoded
 key by half a step of its code, e, and the scale's and its reciprocal's roundings
 (2^-22 of the value)."""
+import random
+
 import pytest
 import torch
 
@@ -520,3 +522,49 @@ def test_slots_of_a_block_that_do_not_exceed_those_before_are_left_out(rows, kep
     q = torch.zeros(len(slots), 2, 128, dtype=F16, device=DEV)
     c.run(status=DEVICE_CHECK, slots=slots, q=q, k=k, v=v, q_out=torch.empty_like(q))
     c.check((want_k, want_v, scales))
+
+
+def test_layouts_of_one_buffer():
+    """Queries, keys, values and turned queries anywhere in one buffer, a few rows of them at
+    strides that agree or not: refused exactly where q_out shares an element with an input
+    that it is not, else written as from separate tensors."""
+    rng, d, seen = random.Random(3), 64, [0, 0]
+    freq = 10000.0 ** (-torch.arange(32, device=DEV, dtype=torch.float64) / 32)
+    for _ in range(400):
+        tokens, hq, hkv = rng.randint(1, 5), rng.randint(1, 3), rng.randint(1, 2)
+        common = (hq + 2 * hkv) * d + rng.choice([0, 8, 200])
+
+        def layout(heads):
+            stride = common if rng.random() < 0.7 else heads * d + 8 * rng.randint(0, 60)
+            return heads, 8 * rng.randint(0, 200), stride
+        parts = [layout(hq), layout(hkv), layout(hkv), layout(hq)]
+        if rng.random() < 0.5:  # as in a fused projection, here and there
+            parts = [(h, at, common) for h, at in ((hq, 0), (hkv, hq * d), (hkv, (hq + hkv) * d),
+                                                   (hq, rng.choice([0, 0, 8, tokens * common])))]
+        size = max(at + (tokens - 1) * s + h * d for h, at, s in parts)
+        buffer = torch.randn(size, device=DEV).to(BF16)
+        q, k, v, out = (torch.as_strided(buffer, (tokens, h, d), (s, d, 1), at) for h, at, s in parts)
+        own = [{at + t * s + i for t in range(tokens) for i in range(h * d)} for h, at, s in parts]
+        in_place = parts[0][1] == parts[3][1] and (tokens == 1 or parts[0][2] == parts[3][2])
+        clash = bool(own[3] & (own[1] | own[2])) or (not in_place and bool(own[3] & own[0]))
+        c = Append([3], [tokens], 1, hkv, d, BF16, INT8, seed=30)
+        pos = torch.arange(tokens, dtype=torch.int32, device=DEV) + 1000
+        start, before = c.state(), buffer.clone()
+        want = torch.empty(tokens, hq, d, dtype=BF16, device=DEV)
+        c.run(dsa.Rope(freq), pos, q=q.clone(), k=k.clone(), v=v.clone(), q_out=want)
+        state = c.state()
+        for x, y in zip((c.k_pages.view(torch.uint8), c.v_pages.view(torch.uint8), c.scales), start):
+            x.copy_(y)
+        seen[clash] += 1
+        if clash:
+            with pytest.raises(dsa.DsaError):
+                c.run(dsa.Rope(freq), pos, q=q, k=k, v=v, q_out=out)
+            torch.cuda.synchronize()
+            assert torch.equal(buffer, before)
+        else:
+            c.run(dsa.Rope(freq), pos, q=q, k=k, v=v, q_out=out)
+            c.check(state)
+            assert torch.equal(out, want)
+            torch.as_strided(before, out.shape, out.stride(), parts[3][1]).copy_(want)
+            assert torch.equal(buffer, before)
+    assert min(seen) > 50, seen

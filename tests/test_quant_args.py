@@ -178,3 +178,41 @@ def test_attention_outputs_that_overlap_are_refused(lib, a, b):
         batch.block_table, batch.seq_lens, batch.q_offsets = x["table"], x["lens"], x["offsets"]
         assert lib.dsa_quant_attention(ctypes.byref(batch), ctypes.byref(c), 0, 4, x["q"], 1024, 0.1,
                                        x["out"], x["lse"], x["ws"], need, None, None) == INVALID
+
+
+FAR = [ctypes.c_void_p((i + 1) << 40) for i in range(6)]  # apart from one another and the cache
+
+
+@pytest.mark.parametrize("at,qs,os", [
+    (0, 512, 520), (16, 512, 512), (-1008, 512, 512), (2 * 520 * 2, 520, 520), (512, 1024, 2048),
+    (2048 - 1008, 1024, 1024), (4096 - 2 * 1032 * 2, 1024, 1032)])
+def test_queries_written_over_others_are_refused(lib, at, qs, os):
+    """q_out begins `at` bytes behind q: three rows of 1024 bytes each, every so many values;
+    over the first of q's rows, the last, or one in the middle."""
+    assert _append(lib, tokens=3, hq=4, q=FAR[0], qs=qs, k=FAR[1], v=FAR[2], slots=FAR[3],
+                   positions=FAR[4], freq=FAR[5].value, out=ctypes.c_void_p(FAR[0].value + at),
+                   os=os) == INVALID
+
+
+@pytest.mark.parametrize("name", ["k", "v", "slots", "positions", "freq"])
+@pytest.mark.parametrize("axes,sections,hq", [(1, (64, 0, 0), 4), (3, (16, 24, 24), 2), (0, (0, 0, 0), 4)])
+def test_queries_written_over_other_inputs_are_refused(lib, name, axes, sections, hq):
+    """At an input's first and last bytes."""
+    if axes == 0 and name in ("positions", "freq"):
+        return  # not read
+    args = dict(tokens=5, axes=axes, sections=sections, hq=hq, q=FAR[0], k=FAR[1], v=FAR[2],
+                slots=FAR[3], positions=FAR[4], freq=FAR[5].value, ks=264, vs=512)
+    last = dict(k=(4 * 264 + 256) * 2 - 16, v=(4 * 512 + 256) * 2 - 16, slots=32,
+                positions=axes * 5 * 4 // 16 * 16, freq=512 - 16)[name]
+    base = args[name] if name == "freq" else args[name].value
+    for at in (base, base + last, base - (4 * 512 + hq * 128) * 2 + 16):
+        assert _append(lib, out=ctypes.c_void_p(at), os=512, **args) == INVALID
+
+
+def test_keys_within_queries_turned_in_place_are_refused(lib):
+    """A key that is a slice of queries that the same call turns in place."""
+    args = dict(tokens=3, hq=4, q=FAR[0], out=FAR[0], v=FAR[2], slots=FAR[3], positions=FAR[4],
+                freq=FAR[5].value, k=ctypes.c_void_p(FAR[0].value + 512), ks=512)
+    assert _append(lib, **args) == INVALID
+    args.update(k=FAR[1], v=ctypes.c_void_p(FAR[0].value + 512), vs=512)
+    assert _append(lib, **args) == INVALID
