@@ -262,12 +262,24 @@ bool overlap(const Rows& a, const Rows& b) {
     return k < b.count && d + k * s < a.length;
 }
 
-// Whether an output shares bytes with a quantised cache.
-bool in_cache(const Rows& rows, const dsa_quant_cache& c) {
-    const int64_t pages = (int64_t)c.num_pages * c.num_kv_heads;
-    return overlap(rows, Rows(c.k_pages, pages * kPage * c.head_dim, 1)) ||
-           overlap(rows, Rows(c.v_pages, pages * kPage * c.head_dim, 1)) ||
-           overlap(rows, Rows(c.scales, pages * (2 * kPage / DSA_QUANT_BLOCK), 4));
+// The arrays of a quantised cache.
+struct CacheRows {
+    Rows k, v, scales;
+    explicit CacheRows(const dsa_quant_cache& c)
+        : k(c.k_pages, (int64_t)c.num_pages * c.num_kv_heads * kPage * c.head_dim, 1),
+          v(c.v_pages, (int64_t)c.num_pages * c.num_kv_heads * kPage * c.head_dim, 1),
+          scales(c.scales, (int64_t)c.num_pages * c.num_kv_heads * (2 * kPage / DSA_QUANT_BLOCK),
+                 4) {}
+};
+
+// Whether a quantised cache shares bytes with `rows`, and its arrays with one another.
+bool in_cache(const Rows& rows, const dsa_quant_cache& cache) {
+    const CacheRows c(cache);
+    return overlap(rows, c.k) || overlap(rows, c.v) || overlap(rows, c.scales);
+}
+bool shares_arrays(const dsa_quant_cache& cache) {
+    const CacheRows c(cache);
+    return overlap(c.k, c.v) || overlap(c.k, c.scales) || overlap(c.v, c.scales);
 }
 
 // Whether an output shares bytes with the arrays of a batch.
@@ -680,21 +692,28 @@ dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
     if (!row_ok(k, k_stride, cache->num_kv_heads, dim) ||
         !row_ok(v, v_stride, cache->num_kv_heads, dim))
         return DSA_ERR_INVALID_ARG;
+    // what the call writes: the cache, apart from what it reads and each of its arrays from the
+    // others, and the turned queries
+    const int64_t row = (int64_t)num_q_heads * dim, kv_row = (int64_t)cache->num_kv_heads * dim;
+    const Rows keys(k, num_tokens, k_stride, kv_row, 2), values(v, num_tokens, v_stride, kv_row, 2);
+    const Rows places(slots, num_tokens, 8);
+    const Rows steps(pairs > 0 ? positions : nullptr, (int64_t)rope->num_axes * num_tokens, 4);
+    const Rows rates(pairs > 0 ? rope->inv_freq : nullptr, pairs, 8);
+    if (shares_arrays(*cache) || in_cache(keys, *cache) || in_cache(values, *cache) ||
+        in_cache(places, *cache) || in_cache(steps, *cache) || in_cache(rates, *cache))
+        return DSA_ERR_INVALID_ARG;
     if (num_q_heads > 0) {
         if (!row_ok(q, q_stride, num_q_heads, dim) || !row_ok(q_out, q_out_stride, num_q_heads, dim))
             return DSA_ERR_INVALID_ARG;
         // a CTA's queries are written while other CTAs read theirs, and all keys and values
-        const int64_t row = (int64_t)num_q_heads * dim, kv_row = (int64_t)cache->num_kv_heads * dim;
         const Rows out(q_out, num_tokens, q_out_stride, row, 2);
+        const Rows queries(q, num_tokens, q_stride, row, 2);
         const bool in_place = q_out == q && (num_tokens == 1 || q_out_stride == q_stride);
-        if (in_cache(out, *cache) ||
-            (!in_place && overlap(out, Rows(q, num_tokens, q_stride, row, 2))) ||
+        if (in_cache(out, *cache) || in_cache(queries, *cache) ||
+            (!in_place && overlap(out, queries)) ||
             // (in place and not turned, queries stay what they are)
-            ((!in_place || pairs > 0) && (overlap(out, Rows(k, num_tokens, k_stride, kv_row, 2)) ||
-                                          overlap(out, Rows(v, num_tokens, v_stride, kv_row, 2)))) ||
-            overlap(out, Rows(slots, num_tokens, 8)) ||
-            (pairs > 0 && (overlap(out, Rows(positions, (int64_t)rope->num_axes * num_tokens, 4)) ||
-                           overlap(out, Rows(rope->inv_freq, pairs, 8)))))
+            ((!in_place || pairs > 0) && (overlap(out, keys) || overlap(out, values))) ||
+            overlap(out, places) || overlap(out, steps) || overlap(out, rates))
             return DSA_ERR_INVALID_ARG;
     }
     g_launches.fetch_add(1, std::memory_order_relaxed);

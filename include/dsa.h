@@ -612,8 +612,8 @@ typedef struct {
  *       token's key and value are not stored.  Tokens of one block stand next to each
  *       other in the call, their slots ascending, and each block comes up in one place
  *       only.
- * q_out may be q itself with the same stride, else it does not overlap the inputs; it lies
- * outside the cache (DSA_ERR_INVALID_ARG).
+ * q_out may be q itself with the same stride, else it does not overlap the inputs.  q_out and
+ * the inputs lie outside the cache, whose arrays do not overlap (DSA_ERR_INVALID_ARG).
  * With q_out apart from q the call may be repeated on the same inputs: it writes the same
  * scales and codes.
  * Recorded as DSA_ERR_DEVICE_CHECK in *dev_status:

@@ -216,3 +216,24 @@ def test_keys_within_queries_turned_in_place_are_refused(lib):
     assert _append(lib, **args) == INVALID
     args.update(k=FAR[1], v=ctypes.c_void_p(FAR[0].value + 512), vs=512)
     assert _append(lib, **args) == INVALID
+
+
+APART = dict(tokens=3, hq=4, q=FAR[0], out=ctypes.c_void_p(1 << 44), k=FAR[1], v=FAR[2], slots=FAR[3],
+             positions=FAR[4], freq=FAR[5].value)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(v_pages=K), dict(v_pages=K + POOL - 16), dict(k_pages=V + 16), dict(scales=K + POOL - 16),
+    dict(scales=K - 8 * 2 * 8 * 4 + 16), dict(scales=V), dict(scales=V + POOL // 2)])
+def test_an_append_to_a_cache_whose_arrays_overlap_is_refused(lib, kw):
+    assert _append(lib, cache=_cache(**kw), **APART) == INVALID
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "slots", "positions", "freq"])
+@pytest.mark.parametrize("begin,size", [(K, POOL), (V, POOL), (S, 8 * 2 * 8 * 4)])
+def test_an_append_of_what_lies_in_the_cache_is_refused(lib, name, begin, size):
+    least = dict(q=3 * 1024, k=3 * 512, v=3 * 512, slots=24, positions=12, freq=512)[name]
+    for at in (begin, begin + size - 16, begin - least // 16 * 16 + 16):
+        kw = dict(APART)
+        kw[name] = at if name == "freq" else ctypes.c_void_p(at)
+        assert _append(lib, **kw) == INVALID
