@@ -738,8 +738,10 @@ dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
         return DSA_ERR_INVALID_ARG;
     if (batch->total_q == 0 || (!k_out && !v_out)) return DSA_OK;
     const int64_t row = (int64_t)heads * dim;
-    if (in_cache(Rows(k_out, batch->total_q, k_stride, row, 2), *cache) ||
-        in_cache(Rows(v_out, batch->total_q, v_stride, row, 2), *cache))
+    const Rows keys(k_out, batch->total_q, k_stride, row, 2);
+    const Rows values(v_out, batch->total_q, v_stride, row, 2);
+    if (in_cache(keys, *cache) || in_cache(values, *cache) || in_batch(keys, *batch) ||
+        in_batch(values, *batch) || overlap(keys, values))
         return DSA_ERR_INVALID_ARG;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(launch_quant_read(to_args(batch), *cache, (int)format, k_out, k_stride,

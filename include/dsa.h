@@ -640,8 +640,8 @@ dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
  *   k_out[t,h,:] = code * scale, in fp32, rounded once to `format`; v_out likewise
  *   k_out, v_out  [T, num_kv_heads, head_dim], tokens *_stride elements apart (a multiple
  *                 of 8, at least a token's elements), 16-byte aligned; either may be NULL.
- *                 They do not overlap each other, unless as slices of one row, and lie
- *                 outside the cache (DSA_ERR_INVALID_ARG).
+ *                 They share no bytes (slices of the same rows do not) and lie outside the
+ *                 cache and the batch's arrays (DSA_ERR_INVALID_ARG).
  * A token before position 0 (seq_lens[b] < n_b, a padding request), one whose page lies
  * outside [0, num_pages) and one of a request whose arrays contradict the host sizes keep
  * the rows that they had; the last two are recorded as DSA_ERR_DEVICE_CHECK.

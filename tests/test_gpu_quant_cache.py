@@ -568,3 +568,46 @@ def test_layouts_of_one_buffer():
             torch.as_strided(before, out.shape, out.stride(), parts[3][1]).copy_(want)
             assert torch.equal(buffer, before)
     assert min(seen) > 50, seen
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("tokens", [1, 9])
+def test_outputs_beside_and_between_the_arrays(code, tokens):
+    """Read: one allocation holds keys' codes, k_out, the scales, v_out and the values' codes
+    without a gap, and k_out and v_out as slices of the same rows do not overlap.  Append: q_out
+    in the place of k_out, of a stride that leaves the scales between two rows of it."""
+    hkv, d = 2, 64
+    c = Append([30 - tokens], [tokens], 2, hkv, d, BF16, code, seed=31)
+    want = c.reference()
+    lens, row = [30], hkv * d * 2
+    batch = dsa.Batch(i32([0, tokens]), i32(lens), c.table, c.pages, lens, [tokens])
+    sizes = [c.k_pages.numel(), tokens * row, c.scales.numel() * 4, tokens * row, c.v_pages.numel()]
+    one = torch.full((sum(sizes),), 0x55, dtype=torch.uint8, device=DEV)
+    k, k_out, scales, v_out, v = one.split(sizes)
+    k, v = (x.view(code).view(c.k_pages.shape) for x in (k, v))
+    scales = scales.view(torch.float32).view(c.scales.shape)
+    for x, y in ((k, c.k_pages), (v, c.v_pages)):
+        x.view(torch.uint8).copy_(y.view(torch.uint8))
+    scales.copy_(c.scales)
+    k_out, v_out = (x.view(BF16).view(tokens, hkv, d) for x in (k_out, v_out))
+    cache, st = dsa.QuantCache(k, v, scales), i32([0])
+    dsa.dsa_quant_append(cache, None, None, c.slots, c.q, c.k, c.v, k_out, st)
+    assert torch.equal(k_out, c.q)
+    dsa.dsa_quant_read(batch, cache, k_out, v_out, st)
+    wide = torch.zeros(tokens, 2 * hkv, d, dtype=BF16, device=DEV)
+    dsa.dsa_quant_read(batch, cache, wide[:, :hkv], wide[:, hkv:], st)
+    assert int(st.item()) == 0
+    assert torch.equal(k_out, wide[:, :hkv]) and torch.equal(v_out, wide[:, hkv:])
+    ref = decoded(want[0], want[2], 0)[c.slots // PAGE, :, c.slots % PAGE]
+    assert torch.equal(k_out, ref.float().to(BF16))
+    c.k_pages, c.v_pages, c.scales = k, v, scales
+    c.check(want)
+    # rows of queries on both sides of an array of scales
+    if tokens > 1:
+        apart = c.scales.numel() * 2 + hkv * d  # values from row to row: 1 KB and more
+        buffer = torch.full((apart * tokens,), 7.0, dtype=BF16, device=DEV)
+        between = buffer[hkv * d:apart].view(torch.float32).view(c.scales.shape)
+        between.copy_(c.scales)
+        out = torch.as_strided(buffer, (tokens, 2, d), (apart, d, 1), 0)
+        dsa.dsa_quant_append(dsa.QuantCache(k, v, between), None, None, c.slots, c.q, c.k, c.v, out, st)
+        assert torch.equal(out, c.q) and torch.equal(between, c.scales) and int(st.item()) == 0

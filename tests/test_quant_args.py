@@ -237,3 +237,22 @@ def test_an_append_of_what_lies_in_the_cache_is_refused(lib, name, begin, size):
         kw = dict(APART)
         kw[name] = at if name == "freq" else ctypes.c_void_p(at)
         assert _append(lib, **kw) == INVALID
+
+
+@pytest.mark.parametrize("at,ks,vs", [
+    (0, 256, 256), (16, 256, 256), (496, 512, 512), (-496, 512, 512), (1024 - 496, 512, 512),
+    (4096 + 496, 512, 512), (2 * 512 * 2, 512, 520)])
+def test_keys_and_values_read_over_one_another_are_refused(lib, at, ks, vs):
+    """v_out begins `at` bytes behind k_out: five rows of 512 bytes each."""
+    batch = dict(num_requests=5, total_q=5)
+    assert _read(lib, batch=batch, k=FAR[0], ks=ks, v=ctypes.c_void_p(FAR[0].value + at),
+                 vs=vs) == INVALID
+
+
+@pytest.mark.parametrize("array,size", [("q_offsets", 24), ("seq_lens", 20), ("block_table", 5 * 64 * 4)])
+def test_outputs_read_over_the_batch_are_refused(lib, array, size):
+    for at in (1 << 40, (1 << 40) + (size - 1) // 16 * 16, (1 << 40) - (4 * 600 + 256) * 2 + 16):
+        batch = dict(num_requests=5, total_q=5, q_offsets=1 << 42, seq_lens=1 << 43, block_table=1 << 44)
+        batch[array] = 1 << 40
+        assert _read(lib, batch=batch, k=ctypes.c_void_p(at), ks=600, v=None) == INVALID
+        assert _read(lib, batch=batch, v=ctypes.c_void_p(at), vs=600, k=None) == INVALID
