@@ -642,9 +642,10 @@ dsa_status dsa_quant_append(int32_t num_tokens, const dsa_quant_cache* cache,
  *                 of 8, at least a token's elements), 16-byte aligned; either may be NULL.
  *                 They share no bytes (slices of the same rows do not) and lie outside the
  *                 cache and the batch's arrays (DSA_ERR_INVALID_ARG).
- * A token before position 0 (seq_lens[b] < n_b, a padding request), one whose page lies
- * outside [0, num_pages) and one of a request whose arrays contradict the host sizes keep
- * the rows that they had; the last two are recorded as DSA_ERR_DEVICE_CHECK.
+ * A token that no request owns (q_offsets[B] < total_q, a step of fixed size), one before
+ * position 0 (seq_lens[b] < n_b, a padding request), one whose page lies outside
+ * [0, num_pages) and one of a request whose arrays contradict the host sizes keep the rows
+ * that they had; the last two are recorded as DSA_ERR_DEVICE_CHECK.
  * batch->num_pages must equal cache->num_pages.  One kernel launch. */
 dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
                           dsa_float_format format, void* k_out, int64_t k_stride, void* v_out,

@@ -611,3 +611,52 @@ def test_outputs_beside_and_between_the_arrays(code, tokens):
         out = torch.as_strided(buffer, (tokens, 2, d), (apart, d, 1), 0)
         dsa.dsa_quant_append(dsa.QuantCache(k, v, between), None, None, c.slots, c.q, c.k, c.v, out, st)
         assert torch.equal(out, c.q) and torch.equal(between, c.scales) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("new", [[3, 5, 0], [0, 0, 0], [40, 1, 9], [64, 64, 64]])
+def test_a_step_of_fixed_size_with_unused_rows(new):
+    """Tables, append and read of a captured step with room for 64 tokens a request: rows that
+    no request fills are left as they are, and nothing is recorded."""
+    cached, hkv, d, room = [10, 0, 70], 2, 64, 192
+    c = Append(cached, new, 2, hkv, d, BF16, INT8, seed=40)
+    cache, st = dsa.QuantCache(c.k_pages, c.v_pages, c.scales), i32([0])
+    lens = [a + b for a, b in zip(cached, new)]
+    table = torch.full((3, 8), -7, dtype=torch.int32, device=DEV)
+    table[:, :c.table.shape[1]] = c.table
+    held = [-(-n // PAGE) for n in cached]
+    free = [int(table[b, i]) for b in range(3) for i in range(held[b], -(-lens[b] // PAGE))]
+    offsets, seq = i32([0] * 4), i32([0] * 3)
+    slots = torch.empty(room, dtype=torch.int64, device=DEV)
+    positions, taken = torch.empty(room, dtype=torch.int32, device=DEV), i32([0])
+    tokens = sum(new)
+    q, k, v = (torch.zeros(room, h, d, dtype=BF16, device=DEV) for h in (2, hkv, hkv))
+    q[:tokens], k[:tokens], v[:tokens] = c.q, c.k, c.v
+    q_out, k_out, v_out = torch.full((3, room, hkv, d), 7.0, dtype=BF16, device=DEV)
+    want = c.reference()
+    free = i32(free + [c.pages - 1])  # one more than is needed
+    dsa.dsa_build_tables(i32(cached), i32(new), free, c.pages, table, offsets, seq, slots, positions,
+                         None, taken, st)
+    dsa.dsa_quant_append(cache, None, None, slots, q, k, v, q_out, st)
+    batch = dsa.Batch(offsets, seq, table, c.pages, [8 * PAGE] * 3, [64] * 3)
+    assert batch.total_q == room
+    dsa.dsa_quant_read(batch, cache, k_out, v_out, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    c.check(want)
+    assert (k_out[tokens:] == 7).all() and (v_out[tokens:] == 7).all()
+    page, row = c.slots // PAGE, c.slots % PAGE
+    for out, pool, which in ((k_out, want[0], 0), (v_out, want[1], 1)):
+        assert torch.equal(out[:tokens], decoded(pool, want[2], which)[page, :, row].float().to(BF16))
+
+
+@pytest.mark.parametrize("offsets", [[0, 5, 9, 7], [0, -4, 3, 9], [2, 3, 4, 5], [0, 3, 4, 40]])
+def test_offsets_that_contradict_the_host_sizes_are_still_recorded(offsets):
+    g = generator(79)
+    lens = [20, 30, 40]
+    table, pages = tables_of(g, lens)
+    k, v, scales = random_cache(g, pages, 1, 64, E4M3)
+    out, st = torch.full((12, 1, 64), 7.0, dtype=BF16, device=DEV), i32([0])
+    batch = dsa.Batch(i32([0, 4, 8, 12]), i32(lens), table, pages, lens, [4, 4, 4])
+    batch.q_offsets.copy_(i32(offsets))
+    dsa.dsa_quant_read(batch, dsa.QuantCache(k, v, scales), out, None, st)
+    assert int(st.item()) == DEVICE_CHECK
