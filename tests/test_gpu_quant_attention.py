@@ -516,3 +516,85 @@ def test_outputs_beside_the_cache(code, new, far):
     assert torch.equal(scales.view(torch.int32), c.scales.view(torch.int32)) and torch.equal(q, c.q)
     assert torch.equal(k.view(torch.uint8), c.k.view(torch.uint8))
     assert torch.equal(v.view(torch.uint8), c.v.view(torch.uint8))
+
+
+def seen_positions(c):
+    """[T]: the positions that each row's token sees."""
+    return torch.tensor([max(0, length - n + j + 1) for length, n in zip(c.lens, c.new)
+                         for j in range(n)], dtype=torch.float64, device=DEV)
+
+
+def check_rows(c, out, lse, r=None, beyond=None):
+    """As Case.check, with every row held to the positions that it sees itself, whatever the
+    longest request has: n of the sums' errors is the row's own.  beyond: what products below
+    f16's normal range may be off by, of n positions (2^-37 of the largest scale times code)."""
+    r = r or c.reference()
+    n = seen_positions(c)[:, None]
+    e = (c.d + 9) * 2.0**-23 * r["terms"]
+    if beyond is None:
+        fine = torch.isfinite(c.scales)
+        beyond = 2.0**-37 * float(torch.where(fine, c.scales, 0.0).max()) * 448
+    share = 2.0**-11 + 2.0**-16 + n * 2.0**-24 + 2.0**-20 + 2 * e
+    tol = torch.finfo(c.dtype).eps / 2 * r["out"].abs() + share[..., None] * r["mean_abs"]
+    tol += n[..., None] * beyond + (2.0**-25 if c.dtype == F16 else 0.0)
+    err = (out.double() - r["out"]).abs()
+    assert (err <= tol).all(), float((err / tol.clamp_min(1e-30)).max())
+    empty = torch.isinf(r["lse"])
+    assert torch.equal(torch.isneginf(lse), empty)
+    off = torch.where(empty, 0.0, (lse.double() - r["lse"]).abs())
+    lse_tol = e + 2.0**-16 + n * 2.0**-24 + 2.0**-20 + 2.0**-22 * r["lse"].abs().nan_to_num(0, 0, 0)
+    assert (off <= lse_tol).all(), float((off / lse_tol).max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (64, 49, 1), (128, 8, 2), (128, 33, 1), (256, 8, 2),
+                                      (256, 5, 5)])
+def test_rows_beside_a_long_request_keep_their_own_accuracy(d, hq, hkv, code, dtype):
+    """The tensor core kernel: short requests of one token, of a few and of chunks, beside the
+    long one that makes the call large enough."""
+    lens = [1, 2, 15, 16, 17, 64, 65, 127, 128, 129, 130, 200, 257, 700, 1500]
+    new = [1, 2, 15, 1, 3, 20, 65, 1, 70, 5, 130, 199, 257, 13, 40]
+    c = Case(lens, new, hq, hkv, d, dtype, code, seed=60 + hq, far=True)
+    check_rows(c, *c.run())
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("d,hq,lens,new", [
+    (64, 64, [900, 300], [1, 3]), (128, 40, [900, 700], [1, 1]), (256, 40, [900, 64], [1, 1]),
+    (128, 8, [400, 900], [100, 60])])
+def test_scales_far_apart_beside_a_long_request(code, d, hq, lens, new):
+    """As test_scales_far_apart, rows held to their own lengths."""
+    hkv = 1 if hq > 8 else 2
+    c = Case(lens, new, hq, hkv, d, F16, code, seed=61, far=True, q_scale=1.0)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    spread_ = torch.randint(-30, 7, c.scales[:, :, 1].shape, generator=g, device=DEV)
+    fine = torch.isfinite(c.scales[:, :, 1]) & (c.scales[:, :, 1] > 0)
+    c.scales[:, :, 1] = torch.where(fine, torch.exp2(spread_.float() - 7), c.scales[:, :, 1])
+    r = c.reference()
+    # a product below 2^-26 of the row's largest, which is at most its largest mean_abs
+    check_rows(c, *c.run(), r=r, beyond=(2.0**-37 * 448 * r["mean_abs"].amax(-1, keepdim=True)))
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("new", [[2, 1, 3], [0, 0, 0], [60, 1, 33]])
+def test_rows_that_no_request_owns_are_not_written(new, far):
+    """A step of fixed size: room for 64 tokens a request, offsets that use fewer."""
+    lens = [300, 1, 90]
+    c = Case(lens, new if max(new) > 12 or not far else [40, 1, 3], 8, 2, 64, BF16, INT8, seed=62,
+             far=far)
+    tokens, room = c.offsets[-1], 64 * len(c.lens)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    batch = dsa.Batch(i32(c.offsets), i32(c.lens), c.table, c.pages, c.lens, [64] * len(c.lens))
+    q = torch.full((room, 8, 64), NAN, dtype=BF16, device=DEV)
+    q[:tokens] = c.q
+    out, lse = torch.full_like(q, 7.0), torch.full((room, 8), 7.0, device=DEV)
+    ws = torch.empty(dsa.dsa_quant_attention_workspace_size(batch, c.cache(), 8), dtype=torch.uint8,
+                     device=DEV)
+    st = i32([0])
+    dsa.dsa_quant_attention(batch, c.cache(), q, c.sm_scale, out, lse, ws, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert (out[tokens:] == 7).all() and (lse[tokens:] == 7).all()
+    check_rows(c, out[:tokens], lse[:tokens])

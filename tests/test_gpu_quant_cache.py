@@ -660,3 +660,100 @@ def test_offsets_that_contradict_the_host_sizes_are_still_recorded(offsets):
     batch.q_offsets.copy_(i32(offsets))
     dsa.dsa_quant_read(batch, dsa.QuantCache(k, v, scales), out, None, st)
     assert int(st.item()) == DEVICE_CHECK
+
+
+@pytest.mark.parametrize("dtype,code,hq,hkv,d", [(BF16, E4M3, 4, 2, 128), (F16, INT8, 2, 1, 64),
+                                                 (BF16, INT8, 1, 1, 256)])
+@pytest.mark.parametrize("cached,new,pad", [
+    ([37], [456], 0), ([37], [457], 0), ([0, 9], [400, 190], 3), ([5], [912], 0), ([13], [913], 1),
+    ([6], [1824], 0), ([0, 30], [1000, 829], 1), ([7], [3000], 0), ([2 * b for b in range(300)],
+                                                                    [1 + b % 4 for b in range(300)], 7)])
+def test_appends_of_every_number_of_tokens_to_a_cta(dtype, code, hq, hkv, d, cached, new, pad):
+    """Calls of 457, 913 and 1825 tokens and more give a CTA two, four and eight."""
+    c = Append(cached, new, hq, hkv, d, dtype, code, seed=d + hq, pad=pad)
+    want = fast_reference(c)
+    c.run()
+    c.check(want)
+    assert torch.equal(c.q_out, c.q)
+
+
+def fast_reference(c):
+    """append_reference for many tokens: all blocks at once, in the same fp32 operations."""
+    t = torch.nonzero(c.slots >= 0)[:, 0]
+    slots = c.slots[t]
+    blocks, nth = torch.unique_consecutive(slots // BLOCK, return_inverse=True)
+    page, part = blocks // (PAGE // BLOCK), blocks % (PAGE // BLOCK)
+    fresh = torch.zeros(len(blocks), device=DEV).index_reduce_(
+        0, nth, (slots % BLOCK == 0).float(), "amax")[:, None] > 0
+    pools, scales = [], c.scales.clone()
+    for which, pool, x in ((0, c.k_pages, c.k), (1, c.v_pages, c.v)):
+        pool, x = pool.clone(), x[t].float()
+        top = torch.zeros(len(blocks), c.hkv, device=DEV).index_reduce_(0, nth, x.abs().amax(-1), "amax")
+        need = (top / torch.full_like(top, LARGEST[pool.dtype])).clamp(2.0**-48, 2.0**32)
+        begun = scales[page, :, which, part]
+        k = torch.zeros_like(begun, dtype=torch.int32)
+        for _ in range(100):
+            k += (torch.ldexp(begun, k) < need).int()
+        k = torch.where(fresh, 0, k)
+        scale = torch.where(fresh, need, torch.ldexp(begun, k))
+        scales[page, :, which, part] = scale
+        rows = pool.view(torch.uint8).view(-1, c.hkv, PAGE // BLOCK, BLOCK, c.d)
+        held = rows[page, :, part].view(pool.dtype).float()
+        rows[page, :, part] = encode(torch.ldexp(held, -k[..., None, None]), pool.dtype).view(torch.uint8)
+        rows[page[nth], :, part[nth], slots % BLOCK] = encode(
+            x * (torch.ones_like(scale) / scale)[nth][..., None], pool.dtype).view(torch.uint8)
+        pools.append(pool)
+    return (*pools, scales)
+
+
+@pytest.mark.parametrize("dtype,code,interleaved", [(BF16, INT8, False), (F16, E4M3, True)])
+def test_a_long_prompt(dtype, code, interleaved):
+    """Sixteen tokens to a CTA, from 16384 on; turned, and the same prompt in calls of at most
+    2000 tokens that end at blocks' borders gives the same cache and queries, bit for bit."""
+    c = Append([11], [16384 + 5 + 3], 2, 1, 64, dtype, code, seed=33, pad=2)
+    want = fast_reference(c)
+    start = c.state()
+    c.run()
+    c.check(want)
+    freq = 10000.0 ** (-torch.arange(32, device=DEV, dtype=torch.float64) / 32)
+    pos = torch.arange(len(c.slots), dtype=torch.int32, device=DEV) + 11
+    results = []
+    for each in (len(c.slots), 2000):
+        for x, y in zip((c.k_pages.view(torch.uint8), c.v_pages.view(torch.uint8), c.scales), start):
+            x.copy_(y)
+        c.q_out.fill_(NAN)
+        at = 0
+        while at < len(c.slots):
+            to = min(len(c.slots), at + each - (0 if at or each > 2000 else 11))  # 11 are cached
+            part = slice(at, to)
+            c.run(dsa.Rope(freq, interleaved=interleaved), pos[part], slots=c.slots[part], q=c.q[part],
+                  k=c.k[part], v=c.v[part], q_out=c.q_out[part])
+            at = to
+        results.append(c.state() + [c.q_out.clone()])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("requests", [31, 32, 33, 64, 65, 100, 700, 1025, 3000])
+@pytest.mark.parametrize("some_empty", [False, True])
+def test_reads_of_many_requests(requests, some_empty):
+    """More requests than are looked through at a time, among them such that bring nothing."""
+    g, rng = generator(requests), random.Random(requests)
+    lens = [rng.randint(1, 90) for _ in range(requests)]
+    new = [0 if some_empty and rng.random() < 0.6 else rng.randint(0, min(n, 20)) for n in lens]
+    new[-1] = max(new[-1], 1)
+    table, pages = tables_of(g, lens)
+    k, v, scales = random_cache(g, pages, 1, 64, INT8)
+    offsets = [0]
+    for n in new:
+        offsets.append(offsets[-1] + n)
+    owner = torch.repeat_interleave(torch.arange(requests), torch.tensor(new))
+    at = torch.arange(offsets[-1]) - torch.tensor(offsets)[owner]
+    pos = (torch.tensor(lens) - torch.tensor(new))[owner] + at
+    page, row = table[owner.to(DEV), (pos // PAGE).to(DEV)].long(), (pos % PAGE).to(DEV)
+    out, st = torch.full((2, offsets[-1], 1, 64), 7.0, dtype=F16, device=DEV), i32([0])
+    batch = dsa.Batch(i32(offsets), i32(lens), table, pages, lens, new)
+    dsa.dsa_quant_read(batch, dsa.QuantCache(k, v, scales), out[0], out[1], st)
+    assert int(st.item()) == 0
+    for which, x in ((0, k), (1, v)):
+        want = x[page, :, row].float() * scales[page, :, which, row // BLOCK][..., None]
+        assert torch.equal(out[which], want.to(F16))
