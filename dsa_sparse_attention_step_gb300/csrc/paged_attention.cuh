@@ -814,11 +814,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // 2^-63, whose scores are 0 in fp32 next to any other
                 const uint32_t e = top >> 7;
                 float up = 1.f;
-                if (e >= 64 && e < 254) {
-                    up = __uint_as_float((254 - e) << 23);
+                if (e >= 64 && e < 255) {
+                    const uint32_t by = min(e, 253u);  // 2^-127 is no normal number: 2..4 then
+                    up = __uint_as_float((254 - by) << 23);
                     // (not below fp32's normal range, where the scores are 0 anyway: a
                     // factor of 0 would make NaN of a masked -inf)
-                    factor = fmaxf(factor * __uint_as_float(e << 23), 0x1p-126f);
+                    factor = fmaxf(factor * __uint_as_float(by << 23), 0x1p-126f);
                 }
 #pragma unroll
                 for (int i = 0; i < kWords; ++i)

@@ -500,9 +500,10 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                             top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
                         const uint32_t e = __reduce_max_sync(0xffffffffu, top) >> 7;
                         float up = 1.f;
-                        if (e >= 64 && e < 254) {
-                            up = __uint_as_float((254 - e) << 23);
-                            factor = factor * __uint_as_float(e << 23);
+                        if (e >= 64 && e < 255) {
+                            const uint32_t by = min(e, 253u);
+                            up = __uint_as_float((254 - by) << 23);
+                            factor = factor * __uint_as_float(by << 23);
                         }
 #pragma unroll
                         for (int i = 0; i < kWords; ++i)

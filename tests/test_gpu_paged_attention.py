@@ -380,3 +380,17 @@ def test_python_checks():
         with pytest.raises(dsa.DsaError):
             dsa.dsa_paged_attention(batch, cache, c.q, bad.get("sm", 0.1), out, None,
                                     bad.get("ws", ws))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_at_the_end_of_bf16_over_fp8(d):
+    """Rows whose largest value is 2^127 or more, alone and beside small ones."""
+    c = Case([600, 601, 602], [1, 1, 1], 4, 2, d, BF16, FP8, seed=63)
+    largest = float(torch.finfo(BF16).max)
+    c.q[0] = c.q[0] / c.q[0].abs().amax(-1, keepdim=True) * largest
+    c.q[1] = c.q[1] / c.q[1].abs().amax(-1, keepdim=True) * 2.0**126
+    c.q[2, :, 5], c.q[2, :, 7] = largest, -(2.0**127)
+    c.sm_scale = 2.0**-119  # times 0.02 log2 e the least that is taken
+    c.k = (c.k.float() * 2.0**-6).to(FP8)
+    assert torch.isfinite(c.q).all()
+    c.check(*c.run())

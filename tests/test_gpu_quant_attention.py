@@ -598,3 +598,18 @@ def test_rows_that_no_request_owns_are_not_written(new, far):
     assert int(st.item()) == 0
     assert (out[tokens:] == 7).all() and (lse[tokens:] == 7).all()
     check_rows(c, out[:tokens], lse[:tokens])
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("d,more", [(64, 0), (128, 0), (256, 0), (64, 40), (128, 40), (256, 40)])
+def test_queries_at_the_end_of_bf16(code, d, more):
+    """Rows whose largest value is 2^127 or more, alone and beside small ones."""
+    c = Case([600, 601, 602] + [500] * (more > 0), [1, 1, 1] + [more] * (more > 0), 4, 2, d, BF16,
+             code, seed=63, far=more > 0)
+    largest = float(torch.finfo(BF16).max)
+    c.q[0] = c.q[0] / c.q[0].abs().amax(-1, keepdim=True) * largest
+    c.q[1] = c.q[1] / c.q[1].abs().amax(-1, keepdim=True) * 2.0**126
+    c.q[2, :, 5], c.q[2, :, 7] = largest, -(2.0**127)
+    c.sm_scale = 2.0**-125
+    assert torch.isfinite(c.q).all()
+    check_rows(c, *c.run())
