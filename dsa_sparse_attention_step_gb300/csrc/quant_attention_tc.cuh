@@ -830,8 +830,13 @@ quant_attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
 // here 1022 for five tokens of eight heads over 16 x 131072 positions of INT8; 128 dims
 // 1493 and 1192, with four tokens 1109 and 1147).  A launch here costs some 25 us more
 // (first steps alone, 128 rows to join), which it makes up for at 2.4 times the rate: the
-// sides meet at 8 * 10^9 operations by the host's sizes (16 requests of 2000 positions, 64
-// rows: 48 and 47 us; of 1000: 29 and 37; 500 new tokens over 1000: 41 and 44, 1000: 62 and 60).
+// sides meet between 8 and 10 * 10^9 operations by the host's sizes (16 requests of 2000
+// positions, 64 rows, 8.4 * 10^9: 48 and 47 us; of 1000: 29 and 37; 500 new tokens over 1000,
+// 8.2 * 10^9: 41 and 44, 1000: 62 and 60).
+// The largest request decides for all, and total_q tokens are counted over max_seq positions
+// each.  Both err towards this kernel where requests differ: of 64 requests of one token over up
+// to 32768 positions, 64 / 8 heads of 128 and E4M3, 278 us by themselves, one with five tokens
+// makes it 507 (two calls 295), and a chunk of 1000 over 16384 beside them 1208 (two calls 940).
 inline bool takes_tensor_cores(const BatchArgs& bt, int num_q_heads, int kv_heads, int head_dim,
                                bool whole) {
     const int64_t rows = (int64_t)bt.max_q * (num_q_heads / kv_heads);

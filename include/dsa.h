@@ -132,8 +132,8 @@ uint64_t dsa_launch_count(void);
  * token depend on its own inputs alone, and equal the default plan's wherever
  * that plan runs the token whole.  Small batches then use fewer SMs.
  * Process-wide; read once by each later call of dsa_sparse_mla(_ex),
- * dsa_decode(_ex) and dsa_decode_noalloc, and by dsa_paged_attention, whose
- * default plan differs (see there).  Workspace sizes do not change.
+ * dsa_decode(_ex) and dsa_decode_noalloc, and by dsa_paged_attention and
+ * dsa_quant_attention, whose default plan differs (see there).  Workspace sizes do not change.
  * Returns the previous setting (0 or 1); the default is 0. */
 int32_t dsa_set_batch_invariant(int32_t enabled);
 
@@ -606,12 +606,15 @@ typedef struct {
  * doubling of a scale loses nothing but what falls below the smallest codes; for INT8 it
  * costs the older codes up to half a step each time.  A scale does not shrink until the
  * block's first row is written again (rejected tokens that others overwrite leave theirs).
+ * So rows that earlier calls wrote change where their block is begun: unlike dsa_rope_append
+ * this call may not run beside one that reads a partly filled block that it adds to.
  *   positions, q, k, v, q_out, num_q_heads, strides: as dsa_rope_append; num_axes 0
  *       means no turning
  *   slots [T] int64, as dsa_build_tables writes them: page * 64 + row.  Negative: the
  *       token's key and value are not stored.  Tokens of one block stand next to each
  *       other in the call, their slots ascending, and each block comes up in one place
- *       only.
+ *       only: the scale and codes of one that comes up again behind another block's tokens
+ *       are undefined.
  * q_out may be q itself with the same stride, else it does not overlap the inputs.  q_out and
  * the inputs lie outside the cache, whose arrays do not overlap (DSA_ERR_INVALID_ARG).
  * With q_out apart from q the call may be repeated on the same inputs: it writes the same
@@ -656,7 +659,9 @@ dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
  * block's scale.  Codes are lifted to f16 exactly; bf16 queries are scaled by a power of
  * two per row so that f16 holds them.  Scores, maxima and sums are fp32.  What meets the
  * values' codes is probability times the block's scale, rounded to f16: half a step each,
- * 2^-11 of it (of those below 2^-26 of the row's largest such product, 2^-37 of that).
+ * 2^-11 of it (of those below 2^-26 of the row's largest such product, 2^-37 of that).  The
+ * scale's logarithm, good to 2^-22 of itself, joins the exponent in fp32: the product is off by
+ * another 2^-24 (|score| log2 e + 63) or so of itself.
  * NaN codes of E4M3 reach the tokens that see them, in their own dim.
  * out, lse and the used bytes of ws overlap neither one another nor q, the cache or the
  * batch's arrays (DSA_ERR_INVALID_ARG).
@@ -664,7 +669,10 @@ dsa_status dsa_quant_read(const dsa_batch* batch, const dsa_quant_cache* cache,
  * (DSA_ERR_INVALID_ARG).  Times log2 e and the row's power of two it counts as no less than
  * 2^-78 and no more than 2^94.
  * Large calls of many rows (a few tokens of 8 heads a KV head, prompt chunks) run on the
- * fifth-generation tensor cores, whose row tile is 128; the workspace follows. */
+ * fifth-generation tensor cores, whose row tile is 128; the workspace follows.  The batch's
+ * largest request and its host sizes decide for the whole call, and requests of one token
+ * then take about twice as long as in a call of their own: a step that has many of them
+ * beside a chunk or a verification is the faster as two calls, one for each kind. */
 size_t dsa_quant_attention_workspace_size(const dsa_batch* batch, const dsa_quant_cache* cache,
                                           int32_t num_q_heads);
 dsa_status dsa_quant_attention(const dsa_batch* batch, const dsa_quant_cache* cache,
