@@ -757,3 +757,21 @@ def test_reads_of_many_requests(requests, some_empty):
     for which, x in ((0, k), (1, v)):
         want = x[page, :, row].float() * scales[page, :, which, row // BLOCK][..., None]
         assert torch.equal(out[which], want.to(F16))
+
+
+@pytest.mark.parametrize("gap", [2046, 2047, 2048, 2049, 4097, 20000])
+@pytest.mark.parametrize("again", [False, True])
+def test_a_block_behind_thousands_of_tokens_that_are_not_stored(gap, again):
+    """The same look back over more slots than a CTA sees at a time, to the block itself and to
+    another one."""
+    c = Append([0], [40], 2, 2, 64, BF16, INT8, seed=24)
+    slots, k, v = pieces(c, list(range(0, 4)), [None] * gap,
+                         list(range(4, 8)) if again else list(range(20, 24)), list(range(32, 35)))
+    keep = slots.clone()
+    if again:
+        keep[4 + gap:8 + gap] = -1
+    want_k, scales, _ = append_reference(c.k_pages, c.scales, 0, keep, k.float())
+    want_v, scales, _ = append_reference(c.v_pages, scales, 1, keep, v.float())
+    q = torch.zeros(len(slots), 2, 64, dtype=BF16, device=DEV)
+    c.run(status=DEVICE_CHECK if again else 0, slots=slots, q=q, k=k, v=v, q_out=torch.empty_like(q))
+    c.check((want_k, want_v, scales))
