@@ -172,7 +172,8 @@ __device__ __forceinline__ uint32_t max_abs8(uint32_t m, const uint4& u) {
 // in shared memory: INT_MAX).  2048 slots at a time: where the first 28672 of a prompt's 32768
 // tokens are not stored the call takes 100 us (without the search 96, by a warp's 32 slots at a
 // time 515).  Not inline: prompts of 7 requests 106.1 us, so 105.6, without the search 105.1.
-__device__ __noinline__ int64_t slot_before(const int64_t* slots, int64_t at, int64_t slot_end, int* near) {
+__device__ __noinline__ int64_t slot_before(const int64_t* slots, int64_t at, int64_t slot_end,
+                                            int* near) {
     constexpr int kLook = 8;
     const int tid = threadIdx.x;
 #pragma unroll 1
@@ -640,8 +641,8 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const ReadArgs a) 
         const bool spare = b + 1 == a.bt.num_requests && q0 >= 0 && q0 <= q1 && q1 <= t;
         if (spare) {
             // keeps what it has
-        } else if (q0 < 0 || t < q0 || t >= q1 || q1 > a.bt.total_q || q1 - q0 > a.bt.max_q || seq < 0 ||
-            seq > a.bt.max_seq) {
+        } else if (q0 < 0 || t < q0 || t >= q1 || q1 > a.bt.total_q || q1 - q0 > a.bt.max_q ||
+                   seq < 0 || seq > a.bt.max_seq) {
             if (tid < count) record_error(a.status, DSA_ERR_DEVICE_CHECK);
         } else if (tid < count) {
             const int pos = seq - (q1 - t);
